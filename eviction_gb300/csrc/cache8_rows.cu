@@ -1,0 +1,387 @@
+// cache8_rows.cu -- rows into and out of the 8-bit paged cache: quantise new
+// tokens (append), make a cache dense for an event (gather), move the rows that
+// an event kept into new blocks (compact).
+//
+// All three are bound by memory: append reads 2 d and writes d bytes per token
+// and head, gather reads d and writes 2 d, compact reads and writes d.  A block's
+// scale needs all of its rows before the first code can be written, so append and
+// compact give one warp a whole block of one head: the warp keeps the rows in
+// registers between the two steps (the rows past its registers, of blocks over 16
+// tokens of 128 values, are read again, from L2), and the maximum is a warp
+// reduction with no shared memory and no barrier.
+#include "cache8.cuh"
+
+namespace kvc {
+namespace cache8 {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kKeep = 8;  // 16-byte chunks a lane keeps in registers
+
+__device__ __forceinline__ void report(const Cache& c, uint32_t bits) {
+  if (bits) atomicOr(c.status, bits);
+}
+
+// ---- append ----
+
+// Largest |x| of 8 bf16 values as bf16 bits, folded into both halves of m.
+__device__ __forceinline__ uint32_t max_abs8(uint4 v, uint32_t m) {
+  m = __vmaxu2(m, v.x & 0x7fff7fffu);
+  m = __vmaxu2(m, v.y & 0x7fff7fffu);
+  m = __vmaxu2(m, v.z & 0x7fff7fffu);
+  return __vmaxu2(m, v.w & 0x7fff7fffu);
+}
+
+// The same over the finite values only.
+__device__ __forceinline__ uint32_t finite(uint32_t two) {
+  two &= 0x7fff7fffu;
+  return ((two & 0x7fffu) < 0x7f80u ? two & 0x7fffu : 0u) |
+         ((two >> 16) < 0x7f80u ? two & 0x7fff0000u : 0u);
+}
+__device__ __forceinline__ uint32_t max_abs8_finite(uint4 v, uint32_t m) {
+  return max_abs8(make_uint4(finite(v.x), finite(v.y), finite(v.z), finite(v.w)), m);
+}
+
+__device__ __forceinline__ uint32_t warp_max_half(uint32_t m) {
+  m = max(m & 0xffffu, m >> 16);
+  return __reduce_max_sync(0xffffffffu, m);
+}
+
+// 8 bf16 values to 8 codes.
+template <int FMT>
+__device__ __forceinline__ uint2 encode8(uint4 v, float inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = encode2<FMT>(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+  return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+}
+
+// Codes times `ratio`, as codes again.
+template <int FROM, int TO>
+__device__ __forceinline__ uint32_t recode4(uint32_t four, float ratio) {
+  float x[4];
+  decode4<FROM>(four, x);
+  return encode2<TO>(x[0] * ratio, x[1] * ratio) | (encode2<TO>(x[2] * ratio, x[3] * ratio) << 16);
+}
+template <int FROM, int TO>
+__device__ __forceinline__ uint4 recode16(uint4 v, float ratio) {
+  return make_uint4(recode4<FROM, TO>(v.x, ratio), recode4<FROM, TO>(v.y, ratio),
+                    recode4<FROM, TO>(v.z, ratio), recode4<FROM, TO>(v.w, ratio));
+}
+
+// One warp: one touched block of one head, keys (blockIdx.y 0) or values.
+template <int D, int FMT>
+__global__ void __launch_bounds__(32 * kWarps)
+    append_kernel(Cache c, Rows k_new, Rows v_new, int n, int per_seq, const int32_t* n_new) {
+  constexpr int CH = D / 8;  // 16-byte chunks of a bf16 row
+  const int lane = threadIdx.x % 32;
+  const long long task = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
+  // heads fastest: the rows of a token-major source then lie side by side
+  const int h = static_cast<int>(task % c.H);
+  const long long t1 = task / c.H;
+  const int ib = static_cast<int>(t1 % per_seq);
+  const long long t2 = t1 / per_seq;
+  const int b = static_cast<int>(t2 % c.B);
+  const long long l = t2 / c.B;
+  if (l >= c.L) return;
+  const int nn = n_new[b];
+  bool bad = false;
+  const int len = length_of(c, b, &bad);
+  if (bad || nn < 0 || nn > n || nn > len) {
+    if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
+    return;
+  }
+  const int start = len - nn;
+  const int i = start / c.bs + ib;
+  if (nn == 0 || static_cast<long long>(i) * c.bs >= len) return;
+  const int first = i * c.bs;
+  const int blk = block_at(c, b, i);
+  if (blk < 0) {
+    if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
+    return;
+  }
+  const int lo = max(first, start), hi = min(len, first + c.bs);
+  const Rows& src = blockIdx.y ? v_new : k_new;
+  const uint16_t* x = src.at(static_cast<int>(l), b, h, lo - start);
+  const int total = (hi - lo) * CH;
+  auto load = [&](int idx) {
+    return __ldg(reinterpret_cast<const uint4*>(x + (idx / CH) * src.token + (idx % CH) * 8));
+  };
+  uint4 keep[kKeep];
+  uint32_t m = 0;
+#pragma unroll
+  for (int s = 0; s < kKeep; ++s) {
+    const int idx = lane + 32 * s;
+    keep[s] = idx < total ? load(idx) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int s = 0; s < kKeep; ++s) m = max_abs8(keep[s], m);
+  for (int idx = lane + 32 * kKeep; idx < total; idx += 32) m = max_abs8(load(idx), m);
+  m = warp_max_half(m);
+  if (m >= 0x7f80u) {  // an infinity or a NaN: the finite values alone give the scale
+    if (lane == 0) report(c, KVC_STATUS_NONFINITE);
+    m = 0;
+    for (int idx = lane; idx < total; idx += 32) m = max_abs8_finite(load(idx), m);
+    m = warp_max_half(m);
+  }
+  float scale = exp2_int(scale_exp<FMT>(__uint_as_float(m << 16)));
+  float* scale_ptr = c.scale[blockIdx.y] + scale_at(c, static_cast<int>(l), blk, h);
+  uint8_t* rows = c.pool[blockIdx.y] + block_row(c, static_cast<int>(l), blk, h) * D;
+  if (lo > first) {  // older rows: the scale only grows, and they follow it
+    const float old = *scale_ptr;
+    if (old >= scale) {
+      scale = old;
+    } else {
+      const float ratio = old / scale;
+      uint4* p = reinterpret_cast<uint4*>(rows);
+      for (int idx = lane; idx < (lo - first) * (D / 16); idx += 32)
+        p[idx] = recode16<FMT, FMT>(p[idx], ratio);
+    }
+    __syncwarp();  // every lane has read the old scale
+  }
+  const float inv = 1.f / scale;  // exact
+  uint2* to = reinterpret_cast<uint2*>(rows + static_cast<size_t>(lo - first) * D);
+#pragma unroll
+  for (int s = 0; s < kKeep; ++s) {
+    const int idx = lane + 32 * s;
+    if (idx < total) to[idx] = encode8<FMT>(keep[s], inv);
+  }
+  for (int idx = lane + 32 * kKeep; idx < total; idx += 32) to[idx] = encode8<FMT>(load(idx), inv);
+  if (lane == 0) *scale_ptr = scale;
+}
+
+// ---- gather ----
+
+constexpr int kGatherThreads = 256;
+constexpr int kGatherUnroll = 4;
+
+// 8 codes to 8 bf16 values (exact: at most 7 significant bits, times a power of two).
+template <int FMT>
+__device__ __forceinline__ uint4 values8(uint2 v, float scale) {
+  float x[4], y[4];
+  decode4<FMT>(v.x, x);
+  decode4<FMT>(v.y, y);
+  return make_uint4(bf16x2(x[0] * scale, x[1] * scale), bf16x2(x[2] * scale, x[3] * scale),
+                    bf16x2(y[0] * scale, y[1] * scale), bf16x2(y[2] * scale, y[3] * scale));
+}
+
+// One thread: 8 values of kGatherUnroll rows, of keys and values.
+template <int D, int FMT>
+__global__ void __launch_bounds__(kGatherThreads)
+    gather_kernel(Cache c, int T, int ctas_per_unit, uint16_t* k_out, uint16_t* v_out,
+                  int32_t* pad_out) {
+  constexpr int CH = D / 8;
+  const int u = blockIdx.x / ctas_per_unit;
+  const int part = blockIdx.x % ctas_per_unit;
+  const int h = u % c.H, b = (u / c.H) % c.B, l = u / (c.H * c.B);
+  bool bad = false;
+  int len = length_of(c, b, &bad);
+  if (len > T) {
+    bad = true;
+    len = 0;
+  }
+  const int pad = T - len;
+  if (l == 0 && h == 0 && part == 0 && threadIdx.x == 0) pad_out[b] = pad;
+  const int ch = threadIdx.x % CH;
+  const int row0 = part * (kGatherThreads / CH * kGatherUnroll) + threadIdx.x / CH;
+  uint2 kc[kGatherUnroll], vc[kGatherUnroll];
+  float ks[kGatherUnroll], vs[kGatherUnroll];
+#pragma unroll
+  for (int i = 0; i < kGatherUnroll; ++i) {
+    const int t = row0 + i * (kGatherThreads / CH);
+    kc[i] = vc[i] = make_uint2(0, 0);
+    ks[i] = vs[i] = 0.f;
+    if (t < T && t >= pad) {
+      const int pos = t - pad;
+      const int blk = block_at(c, b, pos / c.bs);
+      if (blk < 0) {
+        bad = true;
+      } else {
+        const size_t at = (block_row(c, l, blk, h) + pos % c.bs) * CH + ch;
+        const size_t sc = scale_at(c, l, blk, h);
+        kc[i] = __ldg(reinterpret_cast<const uint2*>(c.pool[0]) + at);
+        ks[i] = __ldg(c.scale[0] + sc);
+        if (v_out) {
+          vc[i] = __ldg(reinterpret_cast<const uint2*>(c.pool[1]) + at);
+          vs[i] = __ldg(c.scale[1] + sc);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kGatherUnroll; ++i) {
+    const int t = row0 + i * (kGatherThreads / CH);
+    if (t < T) {
+      const size_t at = (static_cast<size_t>(u) * T + t) * CH + ch;
+      reinterpret_cast<uint4*>(k_out)[at] = values8<FMT>(kc[i], ks[i]);
+      if (v_out) reinterpret_cast<uint4*>(v_out)[at] = values8<FMT>(vc[i], vs[i]);
+    }
+  }
+  if (bad) report(c, KVC_STATUS_BAD_INDEX);
+}
+
+// ---- compact ----
+
+constexpr int kKeepCodes = 4;  // 16-byte chunks of codes a lane keeps
+
+// Largest finite |code| of 16.
+template <int FMT>
+__device__ __forceinline__ float max_code16(uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x[4];
+    decode4<FMT>(w[i], x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(x[j]));  // a NaN code does not count
+  }
+  return m;
+}
+
+// One warp: one new block of one head, keys (blockIdx.y 0) or values.
+template <int D, int FROM, int TO>
+__global__ void __launch_bounds__(32 * kWarps)
+    compact_kernel(Cache c, Cache to, CompactArgs a, int per_unit) {
+  constexpr int CH = D / 16;
+  const int lane = threadIdx.x % 32;
+  const long long task = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
+  const long long u = task / per_unit;
+  const int jb = static_cast<int>(task % per_unit);
+  const int h = static_cast<int>(u % c.H);
+  const int b = static_cast<int>((u / c.H) % c.B);
+  const int l = static_cast<int>(u / (static_cast<long long>(c.H) * c.B));
+  if (l >= c.L) return;
+  bool bad = false;
+  const int len = length_of(c, b, &bad);
+  const int nk = a.n_kept[u];
+  const int new_len = length_of(to, b, &bad);
+  if (bad || nk < 0 || nk > a.budget || nk != new_len) {
+    if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
+    return;
+  }
+  const int j0 = jb * to.bs;
+  const int pad = a.pad[b];
+  const int32_t* kept = a.kept + u * a.budget;
+  if (a.credit_out && blockIdx.y == 0) {
+    for (int j = j0 + lane; j < min(j0 + to.bs, a.budget); j += 32) {
+      const int slot = j < nk ? kept[j] : -1;
+      a.credit_out[u * a.budget + j] =
+          slot >= 0 && slot < a.T ? a.credit_post[u * a.T + slot] : 0.f;
+    }
+  }
+  const int rows = min(nk - j0, to.bs);
+  if (rows <= 0) return;
+  const int new_blk = block_at(to, b, jb);
+  if (new_blk < 0) {
+    if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
+    return;
+  }
+  const uint4* pool = reinterpret_cast<const uint4*>(c.pool[blockIdx.y]);
+  const float* scales = c.scale[blockIdx.y];
+  // a chunk of row r and its scale; zeros for an index outside the sequence
+  auto load = [&](int idx, uint4* v, float* s) {
+    const int slot = kept[j0 + idx / CH];
+    const long long pos = static_cast<long long>(slot) - pad;
+    *v = make_uint4(0, 0, 0, 0);
+    *s = 0.f;
+    if (pos < 0 || pos >= len || slot < 0 || slot >= a.T) {
+      bad = true;
+      return;
+    }
+    const int blk = block_at(c, b, static_cast<int>(pos) / c.bs);
+    if (blk < 0) {
+      bad = true;
+      return;
+    }
+    *v = __ldg(pool + (block_row(c, l, blk, h) + static_cast<int>(pos) % c.bs) * CH + idx % CH);
+    *s = __ldg(scales + scale_at(c, l, blk, h));
+  };
+  const int total = rows * CH;
+  uint4 keep[kKeepCodes];
+  float ks[kKeepCodes];
+  float m = 0.f;
+#pragma unroll
+  for (int s = 0; s < kKeepCodes; ++s) {
+    const int idx = lane + 32 * s;
+    keep[s] = make_uint4(0, 0, 0, 0);
+    ks[s] = 0.f;
+    if (idx < total) load(idx, &keep[s], &ks[s]);
+  }
+#pragma unroll
+  for (int s = 0; s < kKeepCodes; ++s) m = fmaxf(m, max_code16<FROM>(keep[s]) * ks[s]);
+  for (int idx = lane + 32 * kKeepCodes; idx < total; idx += 32) {
+    uint4 v;
+    float s;
+    load(idx, &v, &s);
+    m = fmaxf(m, max_code16<FROM>(v) * s);
+  }
+  const float scale = exp2_int(scale_exp<TO>(warp_max(m)));
+  const float inv = 1.f / scale;  // exact
+  uint4* out = reinterpret_cast<uint4*>(to.pool[blockIdx.y]) + block_row(to, l, new_blk, h) * CH;
+#pragma unroll
+  for (int s = 0; s < kKeepCodes; ++s) {
+    const int idx = lane + 32 * s;
+    if (idx < total) out[idx] = recode16<FROM, TO>(keep[s], ks[s] * inv);
+  }
+  for (int idx = lane + 32 * kKeepCodes; idx < total; idx += 32) {
+    uint4 v;
+    float s;
+    load(idx, &v, &s);
+    out[idx] = recode16<FROM, TO>(v, s * inv);
+  }
+  if (lane == 0) to.scale[blockIdx.y][scale_at(to, l, new_blk, h)] = scale;
+  if (bad) report(c, KVC_STATUS_BAD_INDEX);
+}
+
+int ctas(long long tasks) { return static_cast<int>((tasks + kWarps - 1) / kWarps); }
+
+}  // namespace
+
+cudaError_t launch_append(const Cache& c, int format, const Rows& k, const Rows& v, int n,
+                          const int32_t* n_new, cudaStream_t s) {
+  const int most = min(n, c.max_blocks * c.bs);  // a sequence has no more new tokens than that
+  const int per_seq = (most - 1 + c.bs - 1) / c.bs + 1;  // blocks that they can touch
+  const dim3 grid(ctas(static_cast<long long>(c.L) * c.B * c.H * per_seq), 2);
+  auto* kernel = c.d == 64 ? (format == KVC_CACHE8_E4M3 ? append_kernel<64, KVC_CACHE8_E4M3>
+                                                        : append_kernel<64, KVC_CACHE8_INT8>)
+                           : (format == KVC_CACHE8_E4M3 ? append_kernel<128, KVC_CACHE8_E4M3>
+                                                        : append_kernel<128, KVC_CACHE8_INT8>);
+  kernel<<<grid, 32 * kWarps, 0, s>>>(c, k, v, n, per_seq, n_new);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gather(const Cache& c, int format, int T, uint16_t* k_out, uint16_t* v_out,
+                          int32_t* pad, cudaStream_t s) {
+  const int rows = kGatherThreads / (c.d / 8) * kGatherUnroll;
+  const int per_unit = (T + rows - 1) / rows;
+  const int grid = c.L * c.B * c.H * per_unit;
+  auto* kernel = c.d == 64 ? (format == KVC_CACHE8_E4M3 ? gather_kernel<64, KVC_CACHE8_E4M3>
+                                                        : gather_kernel<64, KVC_CACHE8_INT8>)
+                           : (format == KVC_CACHE8_E4M3 ? gather_kernel<128, KVC_CACHE8_E4M3>
+                                                        : gather_kernel<128, KVC_CACHE8_INT8>);
+  kernel<<<grid, kGatherThreads, 0, s>>>(c, T, per_unit, k_out, v_out, pad);
+  return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_compact_d(const Cache& c, int from, const Cache& to, int to_format,
+                                    const CompactArgs& a, cudaStream_t s) {
+  const int per_unit = (a.budget + to.bs - 1) / to.bs;
+  const dim3 grid(ctas(static_cast<long long>(c.L) * c.B * c.H * per_unit), 2);
+  constexpr int E = KVC_CACHE8_E4M3, I = KVC_CACHE8_INT8;
+  auto* kernel = from == E ? (to_format == E ? compact_kernel<D, E, E> : compact_kernel<D, E, I>)
+                           : (to_format == E ? compact_kernel<D, I, E> : compact_kernel<D, I, I>);
+  kernel<<<grid, 32 * kWarps, 0, s>>>(c, to, a, per_unit);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_compact(const Cache& src, int src_format, const Cache& dst, int dst_format,
+                           const CompactArgs& a, cudaStream_t s) {
+  return src.d == 64 ? launch_compact_d<64>(src, src_format, dst, dst_format, a, s)
+                     : launch_compact_d<128>(src, src_format, dst, dst_format, a, s);
+}
+
+}  // namespace cache8
+}  // namespace kvc

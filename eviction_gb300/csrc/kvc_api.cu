@@ -7,7 +7,7 @@
 #include <cstring>
 #include <new>
 
-#include "kvc_internal.cuh"
+#include "api_util.cuh"
 
 namespace kvc {
 size_t attention_usage_smem_bytes(int d, int R);
@@ -16,19 +16,17 @@ size_t segment_smem_bytes(const kvc_config& c, int T);
 size_t select_smem_bytes(const kvc_config& c, int T);
 }  // namespace kvc
 
+using kvc::aligned16;
+using kvc::cuda_fail;
+using kvc::fail;
+using kvc::mark_begin;
+using kvc::mark_end;
+using kvc::scale_log2_of;
+
 namespace {
 
 constexpr int kMaxT = 65536;
 constexpr int kMaxRows = 4096;  // G*W query rows per unit
-
-int fail(kvc_handle* h, int code, const std::string& msg) {
-  if (h) h->last_error = msg;
-  return code;
-}
-
-bool aligned16(const void* p) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
 
 size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -38,60 +36,11 @@ int check_T(kvc_handle* h, int T) {
   return KVC_OK;
 }
 
-int cuda_fail(kvc_handle* h, cudaError_t e, const char* where) {
-  return fail(h, KVC_ERR_CUDA, std::string(where) + ": " + cudaGetErrorString(e));
-}
-
 const char* const kKernelNames[kvc::kNumKernels] = {
     "usage_pass1_rowstats_tcgen05", "usage_pass2_colsum_tcgen05", "mass_pool_ema",
     "segment_quota", "select_topk", "gather_compact", "refresh_trigger", "compact_paged",
-    "redundancy_score", "mass_segment_select"};
-
-cudaEvent_t prof_event(kvc_handle* h) {
-  auto& P = h->prof;
-  if (!P.pool.empty()) {
-    cudaEvent_t e = P.pool.back();
-    P.pool.pop_back();
-    return e;
-  }
-  cudaEvent_t e = nullptr;
-  if (cudaEventCreate(&e) != cudaSuccess) {
-    cudaGetLastError();
-    return nullptr;
-  }
-  return e;
-}
-
-// Record the start of one kernel launch (nullptr when tracing is off).
-cudaEvent_t mark_begin(kvc_handle* h, cudaStream_t s) {
-  if (!h->prof.enabled) return nullptr;
-  cudaEvent_t e = prof_event(h);
-  if (e) cudaEventRecord(e, s);
-  return e;
-}
-
-void mark_end(kvc_handle* h, int kernel, cudaEvent_t begin, cudaStream_t s) {
-  if (!begin) return;
-  cudaEvent_t e = prof_event(h);
-  if (!e) {
-    h->prof.pool.push_back(begin);
-    return;
-  }
-  cudaEventRecord(e, s);
-  h->prof.pending.push_back({kernel, begin, e});
-}
-
-#define KVC_REQUIRE_PTR(p)                                                    \
-  do {                                                                        \
-    if (!(p)) return fail(h, KVC_ERR_ARG, "null pointer: " #p);               \
-    if (!aligned16(p)) return fail(h, KVC_ERR_ALIGN, "not 16-byte aligned: " #p); \
-  } while (0)
-
-float scale_log2_of(const kvc_config& c) {
-  const double s = c.softmax_scale > 0.f ? static_cast<double>(c.softmax_scale)
-                                         : 1.0 / std::sqrt(static_cast<double>(c.head_dim));
-  return static_cast<float>(s * 1.4426950408889634);
-}
+    "redundancy_score", "mass_segment_select", "cache8_grow", "cache8_append", "cache8_attend",
+    "cache8_gather", "cache8_compact", "cache8_fork", "cache8_free"};
 
 // Step 1: both passes of the window attention usage into the workspace.
 int run_usage(kvc_handle* h, const uint16_t* q, const uint16_t* k, int T, const int32_t* pad,
@@ -414,6 +363,7 @@ int kvc_create(const kvc_config* cfg, kvc_handle** out) {
   const size_t o_q = take(U * S * 4);
   const size_t o_ns = take(U * 4);
   const size_t o_st = take(256);
+  const size_t o_at = take(kvc::cache8_attend_workspace(d.d));
   void* base = nullptr;
   if (cudaMalloc(&base, off) != cudaSuccess) {
     cudaGetLastError();
@@ -441,6 +391,7 @@ int kvc_create(const kvc_config* cfg, kvc_handle** out) {
   w.quota = reinterpret_cast<int32_t*>(p + o_q);
   w.n_seg = reinterpret_cast<int32_t*>(p + o_ns);
   w.status = reinterpret_cast<uint32_t*>(p + o_st);
+  w.attend = p + o_at;
   if (!create_host_io(h->io)) {
     cudaFree(base);
     delete h;

@@ -29,7 +29,8 @@ struct Workspace {
   int32_t* quota = nullptr;
   int32_t* n_seg = nullptr;     // [U]
   uint32_t* status = nullptr;   // device status bits; status[1] = the error word of
-                                // the running paged compaction
+                                // the running paged compaction or cache fork
+  void* attend = nullptr;       // kvc_cache8_attend: partial results of split sequences
   void* base = nullptr;         // single allocation
   size_t bytes = 0;
 };
@@ -53,6 +54,13 @@ enum KernelId {
   kKernelCompactPaged,
   kKernelRedundancy,
   kKernelUnitPost,
+  kKernelCache8Grow,
+  kKernelCache8Append,
+  kKernelCache8Attend,
+  kKernelCache8Gather,
+  kKernelCache8Compact,
+  kKernelCache8Fork,
+  kKernelCache8Free,
   kNumKernels
 };
 
@@ -182,6 +190,9 @@ cudaError_t launch_refresh(const kvc_handle* h, const uint16_t* q, float* q_ref,
 cudaError_t launch_redundancy(const kvc_handle* h, const uint16_t* k, const float* score, int T,
                               const int32_t* pad, float* sel, float* red, cudaStream_t s);
 size_t redundancy_smem_bytes(int D, int T);
+
+// Bytes of Workspace::attend (cache8_attend.cu).
+size_t cache8_attend_workspace(int d);
 
 // One thread waits (bounded) on a barrier nothing completes: the timeout path.
 cudaError_t launch_wait_self_test(const kvc_handle* h, cudaStream_t s);

@@ -21,7 +21,9 @@ ENTRY_POINTS = ("kvc_default_config", "kvc_create", "kvc_destroy", "kvc_stage_si
                 "kvc_get_device_status", "kvc_last_error", "kvc_status_string", "kvc_profile",
                 "kvc_profile_read", "kvc_mass_noalloc", "kvc_refresh_decision",
                 "kvc_compact_paged", "kvc_redundancy_score", "kvc_wait_self_test",
-                "kvc_event_host", "kvc_mass_select")
+                "kvc_event_host", "kvc_mass_select", "kvc_cache8_check", "kvc_cache8_grow",
+                "kvc_cache8_append", "kvc_cache8_attend", "kvc_cache8_gather",
+                "kvc_cache8_compact", "kvc_cache8_fork", "kvc_cache8_free")
 
 STATUS = {0: "KVC_OK", -1: "KVC_ERR_ARG", -2: "KVC_ERR_SHAPE", -3: "KVC_ERR_ALIGN",
           -4: "KVC_ERR_NOMEM", -5: "KVC_ERR_CUDA", -6: "KVC_ERR_DEVICE", -7: "KVC_ERR_TIMEOUT",
@@ -118,6 +120,18 @@ class _HostBuffers(ctypes.Structure):
                  for side in ("dev", "host")])
 
 
+class _CCache8(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_void_p) for k in ("k_pool", "v_pool", "k_scale", "v_scale", "table",
+                                                "seq_len", "free_list", "free_top", "ref_count")] +
+                [(k, ctypes.c_int) for k in ("format", "n_layers", "n_blocks", "block_size",
+                                             "max_blocks")])
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p)] + [(k, ctypes.c_int64)
+                                              for k in ("layer", "seq", "head", "token")]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -160,6 +174,14 @@ def load_library():
     L.kvc_redundancy_score.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P]
     L.kvc_wait_self_test.argtypes = [_P, _P]
     L.kvc_event_host.argtypes = [_P, ctypes.POINTER(_HostBuffers), _I, _I, _P]
+    L.kvc_cache8_check.argtypes = [ctypes.POINTER(_CConfig), _P, ctypes.POINTER(ctypes.c_char_p)]
+    L.kvc_cache8_grow.argtypes = [_P] * 4
+    L.kvc_cache8_append.argtypes = [_P, _P, _P, _P, _I, _P, _P]
+    L.kvc_cache8_attend.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P]
+    L.kvc_cache8_gather.argtypes = [_P, _P, _I, _P, _P, _P, _P]
+    L.kvc_cache8_compact.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P, _P, _P]
+    L.kvc_cache8_fork.argtypes = [_P, _P, _I, _P, _P, _P]
+    L.kvc_cache8_free.argtypes = [_P, _P, _I, _P, _P]
     L.kvc_status_string.argtypes = [_I]
     L.kvc_status_string.restype = ctypes.c_char_p
     for name in ENTRY_POINTS:
@@ -205,6 +227,74 @@ def mass_noalloc(cfg: Config, q, k, T, pad, n_carry, credit_in, credit_post, mas
         _stream_ptr(stream))
 
 
+class Cache8:
+    """An 8-bit paged cache (kvc_cache8 of include/kvc.h): the caller's tensors, checked once.
+
+    k_pool, v_pool [L, n_blocks, H, block_size, d] torch.float8_e4m3fn or torch.int8 (the format);
+    k_scale, v_scale [L, n_blocks, H] fp32; table [B, max_blocks], seq_len [B], free_list
+    [n_blocks], free_top [1], ref_count [n_blocks] int32; all contiguous, on one CUDA device.
+    The object keeps the tensors; entry points change them in place."""
+
+    def __init__(self, k_pool, v_pool, k_scale, v_scale, table, seq_len, free_list, free_top,
+                 ref_count):
+        import torch
+        formats = {torch.float8_e4m3fn: 0, torch.int8: 1}
+        if not isinstance(k_pool, torch.Tensor) or k_pool.dtype not in formats:
+            raise TypeError("k_pool: expected a torch.float8_e4m3fn or torch.int8 tensor")
+        if k_pool.dim() != 5 or table.dim() != 2:
+            raise ValueError("k_pool must be [L, n_blocks, H, block_size, d], table [B, max_blocks]")
+        L, N, H, bs, d = k_pool.shape
+        B, M = table.shape
+        want = dict(k_pool=(k_pool.dtype, (L, N, H, bs, d)), v_pool=(k_pool.dtype, (L, N, H, bs, d)),
+                    k_scale=(torch.float32, (L, N, H)), v_scale=(torch.float32, (L, N, H)),
+                    table=(torch.int32, (B, M)), seq_len=(torch.int32, (B,)),
+                    free_list=(torch.int32, (N,)), free_top=(torch.int32, (1,)),
+                    ref_count=(torch.int32, (N,)))
+        given = dict(k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale, table=table,
+                     seq_len=seq_len, free_list=free_list, free_top=free_top, ref_count=ref_count)
+        self._c = _CCache8(format=formats[k_pool.dtype], n_layers=L, n_blocks=N, block_size=bs,
+                           max_blocks=M)
+        for name, t in given.items():
+            ptr = _dev(t, want[name][0], name)
+            if tuple(t.shape) != want[name][1]:
+                raise ValueError(f"{name}: expected shape {want[name][1]}, got {tuple(t.shape)}")
+            if t.device != k_pool.device:
+                raise ValueError(f"{name}: on {t.device}, k_pool on {k_pool.device}")
+            setattr(self._c, name, ptr.value)
+            setattr(self, name, t)
+        self._ref = ctypes.byref(self._c)
+        self.n_layers, self.batch, self.n_kv_heads, self.head_dim = L, B, H, d
+        self.device = k_pool.device
+
+    @classmethod
+    def allocate(cls, cfg: Config, n_blocks, block_size, max_blocks, dtype=None, device="cuda"):
+        """An empty cache for cfg's layers, sequences and heads, every block free (torch
+        allocates; the library never does).  dtype: torch.float8_e4m3fn (default) or torch.int8."""
+        import torch
+        shape = (cfg.n_layers, n_blocks, cfg.n_kv_heads)
+        i = dict(dtype=torch.int32, device=device)
+        pools = [torch.zeros(shape + (block_size, cfg.head_dim), dtype=torch.uint8, device=device)
+                 .view(dtype or torch.float8_e4m3fn) for _ in "kv"]
+        scales = [torch.ones(shape, device=device) for _ in "kv"]
+        return cls(*pools, *scales, torch.full((cfg.batch, max_blocks), -1, **i),
+                   torch.zeros(cfg.batch, **i), torch.arange(n_blocks, **i),
+                   torch.full((1,), n_blocks, **i), torch.zeros(n_blocks, **i))
+
+    def layers(self, first, last=None):
+        """The same cache as calls on layers [first, last) take it (one layer by default)."""
+        last = first + 1 if last is None else last
+        if not 0 <= first < last <= self.n_layers:
+            raise ValueError(f"layers [{first}, {last}) of {self.n_layers}")
+        return Cache8(self.k_pool[first:last], self.v_pool[first:last], self.k_scale[first:last],
+                      self.v_scale[first:last], self.table, self.seq_len, self.free_list,
+                      self.free_top, self.ref_count)
+
+    def with_sequences(self, table, seq_len):
+        """A cache of other sequences in the same pools and free stack (kvc_cache8_compact's dst)."""
+        return Cache8(self.k_pool, self.v_pool, self.k_scale, self.v_scale, table, seq_len,
+                      self.free_list, self.free_top, self.ref_count)
+
+
 class Handle:
     """A kvc_handle: validated config plus the device workspace."""
 
@@ -217,6 +307,8 @@ class Handle:
         if rc != 0:
             raise KvcError(rc, "kvc_create failed")
         self._h = h
+        import torch
+        self._device = torch.device("cuda", torch.cuda.current_device())
 
     # -- helpers -------------------------------------------------------------
     def _check(self, rc, what):
@@ -354,6 +446,129 @@ class Handle:
             _stream_ptr(stream))
         self._check(rc, "kvc_compact_paged")
 
+    # -- the 8-bit paged cache -------------------------------------------------
+    def _cache8(self, cache, name="cache"):
+        if not isinstance(cache, Cache8):
+            raise TypeError(f"{name}: expected a Cache8")
+        c = self.cfg
+        if (cache.batch, cache.n_kv_heads, cache.head_dim) != (c.batch, c.n_kv_heads, c.head_dim):
+            raise ValueError(f"{name}: batch, heads or head_dim differ from the handle's")
+        if cache.device != self._device:
+            raise ValueError(f"{name}: on {cache.device}, the handle on {self._device}")
+        return cache._ref
+
+    def _ints(self, t, name, shape, device):
+        import torch
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+        return self._on(t, torch.int32, name, device)
+
+    @staticmethod
+    def _on(t, dtype, name, device):
+        ptr = _dev(t, dtype, name)
+        if t.device != device:
+            raise ValueError(f"{name}: on {t.device}, the cache on {device}")
+        return ptr
+
+    @staticmethod
+    def _rows(t, name, shape, device):
+        """kvc_rows of a bf16 tensor [L, B, heads, n, d] of any strides, d contiguous."""
+        import torch
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+            raise TypeError(f"{name}: expected a torch.bfloat16 tensor")
+        if t.device != device:
+            raise ValueError(f"{name}: on {t.device}, the cache on {device}")
+        if t.shape != shape or t.stride(-1) != 1:
+            raise ValueError(f"{name}: expected shape {shape}, the last axis contiguous")
+        return ctypes.byref(_Rows(t.data_ptr(), *t.stride()[:4]))
+
+    def cache8_grow(self, cache, n_new, stream=None):
+        """kvc_cache8_grow: blocks for n_new [B] int32 further tokens of every sequence."""
+        self._check(load_library().kvc_cache8_grow(
+            self._h, self._cache8(cache), self._ints(n_new, "n_new", (cache.batch,), cache.device),
+            _stream_ptr(stream)), "kvc_cache8_grow")
+
+    def cache8_append(self, cache, k, v, n_new, stream=None):
+        """kvc_cache8_append: quantise the newest tokens' rows k, v [L, B, H, n, d] bf16 (any
+        strides) into their blocks; n_new [B] int32 of them for each sequence."""
+        ref = self._cache8(cache)
+        n = k.shape[3] if k.dim() == 5 else 0
+        shape = (cache.n_layers, cache.batch, cache.n_kv_heads, n, cache.head_dim)
+        self._check(load_library().kvc_cache8_append(
+            self._h, ref, self._rows(k, "k", shape, cache.device),
+            self._rows(v, "v", shape, cache.device), n,
+            self._ints(n_new, "n_new", (cache.batch,), cache.device), _stream_ptr(stream)),
+            "kvc_cache8_append")
+
+    def cache8_attend(self, cache, q, out, lse=None, n_q=None, stream=None):
+        """kvc_cache8_attend: q, out [L, B, H*G, n, d] bf16 (any strides), lse [L, B, H*G, n]
+        fp32 or None, n_q [B] int32 or None (n queries for every sequence)."""
+        import torch
+        ref = self._cache8(cache)
+        n = q.shape[3] if q.dim() == 5 else 0
+        heads = cache.n_kv_heads * self.cfg.group
+        shape = (cache.n_layers, cache.batch, heads, n, cache.head_dim)
+        if lse is not None and lse.shape != shape[:4]:
+            raise ValueError(f"lse: expected shape {shape[:4]}, got {tuple(lse.shape)}")
+        self._check(load_library().kvc_cache8_attend(
+            self._h, ref, self._rows(q, "q", shape, cache.device), n,
+            None if n_q is None else self._ints(n_q, "n_q", (cache.batch,), cache.device),
+            self._rows(out, "out", shape, cache.device),
+            None if lse is None else self._on(lse, torch.float32, "lse", cache.device),
+            _stream_ptr(stream)), "kvc_cache8_attend")
+
+    def cache8_gather(self, cache, T, pad, k_out, v_out=None, stream=None):
+        """kvc_cache8_gather: dense left-padded k_out, v_out (or None) [L, B, H, T, d] bf16 and
+        pad [B] int32, as kvc_mass_select takes them."""
+        import torch
+        ref = self._cache8(cache)
+        shape = (cache.n_layers, cache.batch, cache.n_kv_heads, T, cache.head_dim)
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is not None and t.shape != shape:
+                raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+        self._check(load_library().kvc_cache8_gather(
+            self._h, ref, T, self._on(k_out, torch.bfloat16, "k_out", cache.device),
+            None if v_out is None else self._on(v_out, torch.bfloat16, "v_out", cache.device),
+            self._ints(pad, "pad", (cache.batch,), cache.device), _stream_ptr(stream)),
+            "kvc_cache8_gather")
+
+    def cache8_compact(self, cache, dst, T, pad, kept_idx, n_kept, credit_post=None,
+                       credit_out=None, stream=None):
+        """kvc_cache8_compact: the kept rows of `cache`, per layer and head, to the first
+        positions of `dst` (grown by n_kept before); kept_idx [L, B, H, budget], n_kept
+        [L, B, H], credit_post [L, B, H, T] -> credit_out [L, B, H, budget] (or both None)."""
+        import torch
+        ref, ref_dst = self._cache8(cache), self._cache8(dst, "dst")
+        if dst.n_layers != cache.n_layers or dst.device != cache.device:
+            raise ValueError("dst: other layers or device than the cache")
+        units = (cache.n_layers, cache.batch, cache.n_kv_heads)
+        budget = self.cfg.budget
+        credit = []
+        for name, t, n in (("credit_post", credit_post, T), ("credit_out", credit_out, budget)):
+            if t is not None and t.shape != units + (n,):
+                raise ValueError(f"{name}: expected shape {units + (n,)}, got {tuple(t.shape)}")
+            credit.append(None if t is None else self._on(t, torch.float32, name, cache.device))
+        self._check(load_library().kvc_cache8_compact(
+            self._h, ref, ref_dst, T, self._ints(pad, "pad", (cache.batch,), cache.device),
+            self._ints(kept_idx, "kept_idx", units + (budget,), cache.device),
+            self._ints(n_kept, "n_kept", units, cache.device), *credit, _stream_ptr(stream)),
+            "kvc_cache8_compact")
+
+    def cache8_fork(self, cache, src, dst, stream=None):
+        """kvc_cache8_fork: start the empty sequences dst [n] int32 from src [n] int32."""
+        ref = self._cache8(cache)
+        self._check(load_library().kvc_cache8_fork(
+            self._h, ref, src.numel(), self._ints(src, "src", (src.numel(),), cache.device),
+            self._ints(dst, "dst", (src.numel(),), cache.device), _stream_ptr(stream)),
+            "kvc_cache8_fork")
+
+    def cache8_free(self, cache, seqs, stream=None):
+        """kvc_cache8_free: give the sequences seqs [n] int32 up."""
+        ref = self._cache8(cache)
+        self._check(load_library().kvc_cache8_free(
+            self._h, ref, seqs.numel(), self._ints(seqs, "seqs", (seqs.numel(),), cache.device),
+            _stream_ptr(stream)), "kvc_cache8_free")
+
     def wait_self_test(self, stream=None):
         """kvc_wait_self_test: a bounded wait that runs out on purpose (about
         2 s); afterwards device_status() reports KVC_STATUS_WAIT_TIMEOUT."""
@@ -374,9 +589,9 @@ class Handle:
 
     def profile_read(self, reset: bool = False):
         """[{name, launches, total_ms}] per kernel (waits for the recorded events)."""
-        arr = (_KernelTime * 16)()
+        arr = (_KernelTime * 32)()
         n = _I()
-        self._check(load_library().kvc_profile_read(self._h, arr, 16, ctypes.byref(n),
+        self._check(load_library().kvc_profile_read(self._h, arr, 32, ctypes.byref(n),
                                                     1 if reset else 0), "kvc_profile_read")
         return [dict(name=arr[i].name.decode(), launches=arr[i].launches,
                      total_ms=arr[i].total_ms) for i in range(n.value)]

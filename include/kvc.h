@@ -83,7 +83,11 @@ extern "C" {
                                         was changed)                          */
 #define KVC_STATUS_POOL_EXHAUSTED 0x4u /* kvc_compact_paged: the free stack
                                         held fewer blocks than the compacted
-                                        caches need (nothing was changed)     */
+                                        caches need (nothing was changed);
+                                        also kvc_cache8_grow / kvc_cache8_fork */
+#define KVC_STATUS_NONFINITE 0x8u /* kvc_cache8_append met an infinity (stored
+                                     as the largest code) or a NaN (stored as
+                                     zero)                                    */
 
 /* ---- configuration ------------------------------------------------------ */
 typedef struct {
@@ -365,6 +369,166 @@ int kvc_compact_paged(kvc_handle* h, uint16_t* k_pool, uint16_t* v_pool, int n_b
  * caller-owned; asynchronous on `stream`; no allocation. */
 int kvc_refresh_decision(kvc_handle* h, const uint16_t* q, float* q_ref, float threshold,
                          int32_t* flag, float* sim, void* stream);
+
+/* ---- 8-bit paged cache ----------------------------------------------------
+ * The decode loop around the event, over a cache held in 8 bits: keys and
+ * values live in pages ("blocks") of block_size tokens, one byte a value, with
+ * one power-of-two scale for each block, head and layer.  A step of decoding is
+ *   kvc_cache8_grow    reserve blocks for the new tokens (once a step)
+ *   kvc_cache8_append  quantise a layer's new keys and values into them
+ *   kvc_cache8_attend  attention of the layer's new queries over the cache
+ * and a compression event every few hundred steps is
+ *   kvc_cache8_gather  the cache as the dense rows that kvc_mass_select takes
+ *   kvc_cache8_compact the kept rows, requantised, into another cache's blocks
+ *   kvc_cache8_free    the old blocks back onto the free stack.
+ * kvc_cache8_fork starts further samples of a prompt from its cache.
+ *
+ * Codes.  A code c stands for c * scale.  KVC_CACHE8_E4M3: c is an e4m3 float
+ * (4 exponent bits, 3 mantissa bits, largest 448); KVC_CACHE8_INT8: c is a signed
+ * integer, -127..127.  The scale of a block is the smallest power of two in
+ * [2^-64, 2^64] under which the largest finite magnitude of the block's rows is
+ * at most 448 (127); values are divided by it (exact) and rounded to the nearest
+ * code, ties to even.  Larger magnitudes and infinities become the largest code,
+ * NaN becomes 0.  Codes from elsewhere must be finite in the rows that a call
+ * reads; rows past a sequence's end may hold anything.
+ *
+ * Memory.  All pointers are device memory of the caller; the pools and scales
+ * point at the first layer that a call works on, so that the same arrays serve
+ * calls on all layers and on one:
+ *   k_pool, v_pool   [n_layers][n_blocks][H][block_size][d] codes (16-byte aligned)
+ *   k_scale, v_scale [n_layers][n_blocks][H] fp32
+ *   table     [B][max_blocks] int32: token t of sequence b is row t % block_size
+ *             of block table[b][t / block_size], in every layer and head
+ *   seq_len   [B] int32 tokens held
+ *   free_list [n_blocks] int32, free_top [1] int32: entries [0, *free_top) are the
+ *             free blocks, a stack
+ *   ref_count [n_blocks] int32: sequences that hold the block.  A block that is
+ *             not full is never shared.
+ * B, H, G and d come from the handle; sequences may be longer than max_T.
+ * block_size 1..1024; n_blocks * H * block_size, B * max_blocks and
+ * max_blocks * block_size < 2^31.
+ *
+ * Every entry point checks what it reads from these arrays: an index out of
+ * range sets KVC_STATUS_BAD_INDEX and is never followed.  grow, fork and free
+ * change nothing then (nor when the free stack is too short,
+ * KVC_STATUS_POOL_EXHAUSTED); the others skip what they cannot reach.  A failed
+ * grow or fork leaves the step without its blocks: read the status before the
+ * step's results are used.  Calls of one handle run one after another (they share
+ * its workspace), also when they were captured into different graphs. */
+#define KVC_CACHE8_E4M3 0
+#define KVC_CACHE8_INT8 1
+
+typedef struct {
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  float* k_scale;
+  float* v_scale;
+  int32_t* table;
+  int32_t* seq_len;
+  int32_t* free_list;
+  int32_t* free_top;
+  int32_t* ref_count;
+  int format;      /* KVC_CACHE8_E4M3 or KVC_CACHE8_INT8 */
+  int n_layers;    /* layers in this call, >= 1          */
+  int n_blocks;
+  int block_size;
+  int max_blocks;
+} kvc_cache8;
+
+/* Rows of d bf16 values, d contiguous, at data + layer*l + seq*b + head*h +
+ * token*j (strides in values, each a multiple of 8 and >= 0; data 16-byte
+ * aligned): [l][b][h][j][d] as elsewhere, or token-major as a projection
+ * leaves them. */
+typedef struct {
+  uint16_t* data;
+  int64_t layer, seq, head, token;
+} kvc_rows;
+
+/* Check a cache description against a configuration, on the host alone (no
+ * device, nothing read through the pointers).  KVC_OK or the code that the
+ * entry points below would return; the reason goes to *why (a static string)
+ * where why is not NULL. */
+int kvc_cache8_check(const kvc_config* cfg, const kvc_cache8* c, const char** why);
+
+/* Reserve blocks for n_new[b] >= 0 further tokens of every sequence and add them
+ * to seq_len.  New blocks are taken from the top of the free stack: with S blocks
+ * needed in all, sequence by sequence and block by block, the entries
+ * free_list[*free_top - S ...] in ascending order; their ref_count becomes 1.
+ *   n_new  [B] int32
+ * Changes nothing, with KVC_STATUS_BAD_INDEX, where a sequence would outgrow
+ * max_blocks, a count or a block is out of range, or a started block is shared. */
+int kvc_cache8_grow(kvc_handle* h, const kvc_cache8* c, const int32_t* n_new, void* stream);
+
+/* Write the newest tokens: row j < n_new[b] of k and v goes to position
+ * seq_len[b] - n_new[b] + j (grow has counted them in).  A block that already
+ * holds older tokens keeps them: its scale only grows, and the older codes are
+ * then rounded to the new scale.  Writing the same rows again changes nothing.
+ *   k, v   [n_layers][B][H][n][d] bf16 rows
+ *   n_new  [B] int32, 0..n (rows past it are not read); a sequence whose count
+ *          is out of range, or above its seq_len, is skipped (BAD_INDEX) */
+int kvc_cache8_append(kvc_handle* h, const kvc_cache8* c, const kvc_rows* k, const kvc_rows* v,
+                      int n, const int32_t* n_new, void* stream);
+
+/* Attention of the newest tokens' queries over the cache:
+ *   out_j = sum_t softmax_t(scale q_j . k_t) v_t over t <= seq_len[b] - n_q[b] + j,
+ * for the H*G query heads (head h*G+g reads KV head h); scale is the
+ * configuration's softmax_scale.  Arithmetic: the products take q, the codes and
+ * the softmax weights in at least bf16's precision and accumulate in fp32; maxima
+ * and sums are fp32.
+ *   q      [n_layers][B][H*G][n][d] bf16 rows, 1 <= n <= window
+ *   n_q    [B] int32, 0..n, or NULL: n for every sequence.  Rows past n_q[b] are
+ *          neither read nor written
+ *   out    as q.  A query that sees no token (its position is before the first)
+ *          gets zeros
+ *   lse    [n_layers][B][H*G][n] fp32 contiguous, or NULL: the natural logarithm
+ *          of the sum of exp(scale q.k), -inf for a query that sees no token
+ * A sequence whose n_q is out of range is skipped; tokens in a block that is out
+ * of range count as absent (both BAD_INDEX). */
+int kvc_cache8_attend(kvc_handle* h, const kvc_cache8* c, const kvc_rows* q, int n,
+                      const int32_t* n_q, const kvc_rows* out, float* lse, void* stream);
+
+/* The cache as dense, left-padded bf16 rows, as kvc_mass_select and kvc_event
+ * take them: pad[b] = T - seq_len[b], slot pad[b] + t holds token t, padding is
+ * zero.  Every code times its scale is a bf16 value: nothing is rounded.
+ *   k_out, v_out  [n_layers][B][H][T][d] bf16, contiguous; v_out may be NULL
+ *   pad           [B] int32 out
+ * A sequence longer than T (T <= max_T) is taken as empty (BAD_INDEX). */
+int kvc_cache8_gather(kvc_handle* h, const kvc_cache8* c, int T, uint16_t* k_out,
+                      uint16_t* v_out, int32_t* pad, void* stream);
+
+/* Step 6 of the event between caches: the rows that an event kept go, per layer
+ * and head, to positions 0, 1, ... of dst, whose blocks are there already
+ * (kvc_cache8_grow with n_kept); blocks of dst take their scale from the rows
+ * they receive.  dst may lie in the same pools (its blocks are others then) or
+ * in pools of another format or block size.
+ *   T, pad, kept_idx, n_kept  as kvc_select / kvc_event leave them for the dense
+ *                  rows of kvc_cache8_gather ([L][B][H][budget], [L][B][H]);
+ *                  n_kept must equal dst's seq_len[b], else the unit is skipped
+ *   credit_post [n_layers][B][H][T] -> credit_out [n_layers][B][H][budget], as in
+ *                  kvc_compact (zero past n_kept); both may be NULL
+ * An index outside the sequence writes a zero row (BAD_INDEX). */
+int kvc_cache8_compact(kvc_handle* h, const kvc_cache8* src, const kvc_cache8* dst, int T,
+                       const int32_t* pad, const int32_t* kept_idx, const int32_t* n_kept,
+                       const float* credit_post, float* credit_out, void* stream);
+
+/* Start sequences dst[i] (empty, all different) from the caches of src[i] (which
+ * may repeat): full blocks are shared (ref_count + 1), the rows of a started block
+ * are copied, in all n_layers layers, into a block from the free stack (in list
+ * order, as in grow).
+ *   src, dst  [n] int32 sequence numbers; n = 0 does nothing
+ * Changes nothing, with a status bit, where a number or block is out of range, a
+ * dst repeats, is not empty or is also a src, or the stack is too short. */
+int kvc_cache8_fork(kvc_handle* h, const kvc_cache8* c, int n, const int32_t* src,
+                    const int32_t* dst, void* stream);
+
+/* Give up sequences: ref_count of their blocks - 1, and blocks that nobody holds
+ * any more go onto the free stack, in list order and then block order (a block
+ * that several of them shared: at its last place).  Their seq_len becomes 0 and
+ * their table rows -1.
+ *   seqs  [n] int32, all different; n = 0 does nothing
+ * Changes nothing, with KVC_STATUS_BAD_INDEX, where a number repeats or anything
+ * is out of range. */
+int kvc_cache8_free(kvc_handle* h, const kvc_cache8* c, int n, const int32_t* seqs, void* stream);
 
 /* ---- failure-path self-test -------------------------------------------
  * No counterpart in the pages: a check of the library's own failure path.
