@@ -40,8 +40,9 @@ int check_cache(const kvc_config& cfg, const kvc_cache8* c, const char** why) {
   const long long B = cfg.batch, H = cfg.n_kv_heads, N = c->n_blocks, M = c->max_blocks;
   if (N > INT_MAX / H || N * H > INT_MAX / c->block_size)
     return bad(KVC_ERR_UNSUPPORTED, "n_blocks * n_kv_heads * block_size must be < 2^31");
-  if (B * M > INT_MAX || M * c->block_size > INT_MAX)
-    return bad(KVC_ERR_UNSUPPORTED, "batch * max_blocks and max_blocks * block_size must be < 2^31");
+  if (B * M > INT_MAX || M * c->block_size > (1 << 30))
+    return bad(KVC_ERR_UNSUPPORTED,
+               "batch * max_blocks must be < 2^31, max_blocks * block_size <= 2^30");
   if (B * H * c->n_layers > INT_MAX / 2)
     return bad(KVC_ERR_UNSUPPORTED, "n_layers * batch * n_kv_heads must be < 2^30");
   return KVC_OK;

@@ -389,8 +389,9 @@ int kvc_refresh_decision(kvc_handle* h, const uint16_t* q, float* q_ref, float t
  * [2^-64, 2^64] under which the largest finite magnitude of the block's rows is
  * at most 448 (127); values are divided by it (exact) and rounded to the nearest
  * code, ties to even.  Larger magnitudes and infinities become the largest code,
- * NaN becomes 0.  Codes from elsewhere must be finite in the rows that a call
- * reads; rows past a sequence's end may hold anything.
+ * NaN becomes 0.  Codes and scales from elsewhere must keep to this (finite codes
+ * in the rows that a call reads, powers of two); rows past a sequence's end may
+ * hold anything.  The value scales of one sequence and head may lie 2^100 apart.
  *
  * Memory.  All pointers are device memory of the caller; the pools and scales
  * point at the first layer that a call works on, so that the same arrays serve
@@ -405,8 +406,8 @@ int kvc_refresh_decision(kvc_handle* h, const uint16_t* q, float* q_ref, float t
  *   ref_count [n_blocks] int32: sequences that hold the block.  A block that is
  *             not full is never shared.
  * B, H, G and d come from the handle; sequences may be longer than max_T.
- * block_size 1..1024; n_blocks * H * block_size, B * max_blocks and
- * max_blocks * block_size < 2^31.
+ * block_size 1..1024; n_blocks * H * block_size and B * max_blocks < 2^31,
+ * max_blocks * block_size <= 2^30.
  *
  * Every entry point checks what it reads from these arrays: an index out of
  * range sets KVC_STATUS_BAD_INDEX and is never followed.  grow, fork and free

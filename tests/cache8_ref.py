@@ -259,6 +259,8 @@ class RefCache:
                 nq = n if n_q is None else int(n_q[b])
                 for h in range(self.H):
                     k, v = self.rows(0, l, b, h), self.rows(1, l, b, h)
+                    vs = np.array([self.scale[1][l, self.table[b, t // self.bs], h] for t in range(m)],
+                                  np.float64)
                     for g in range(h * G, (h + 1) * G):
                         for j in range(nq):
                             end = m - nq + j + 1
@@ -273,12 +275,13 @@ class RefCache:
                             zabs = (np.abs(k[:end]) @ np.abs(q[l, b, g, j])).max() * scale
                             qabs = np.abs(q[l, b, g, j]).max() * np.abs(k[:end]).sum(1).max() * scale
                             tol[l, b, g, j], ltol[l, b, g, j] = tolerances(
-                                out[l, b, g, j], p @ np.abs(v[:end]), lse[l, b, g, j], zabs, qabs,
-                                end, d)
+                                out[l, b, g, j], p @ np.abs(v[:end]),
+                                (p * vs[:end]).max() * (np.abs(v[:end]) / vs[:end, None]).sum(0),
+                                lse[l, b, g, j], zabs, qabs, end, d)
         return out, lse, tol, ltol
 
 
-def tolerances(out, weight, lse, zabs, qabs, T, d):
+def tolerances(out, weight, least, lse, zabs, qabs, T, d):
     """What fp32 accumulation and rounded operands can be off by.
 
     A score's error dz: d products and additions, the scaling and the exponential's argument in fp32,
@@ -286,8 +289,13 @@ def tolerances(out, weight, lse, zabs, qabs, T, d):
     row's largest where 11 significant bits do not reach (qabs = largest |q| times the sum of |k|); the
     exponential itself 2^-21.  A softmax weight is then off by 2 dz (its own and the sum's) and its
     rounding to 11 bits (2^-11); sums over T tokens by T 2^-24, the joining of parts by 2^-20.  The
-    result is rounded to bf16, half a step: 2^-8 of it."""
+    result is rounded to bf16, half a step: 2^-8 of it.
+    Weights are rounded in fp16, whose steps end at 2^-24: with the largest weight times scale taken as
+    1 or more, a smaller one is off by up to 2^-25 of that, times its token's codes; `least` is the
+    largest weight times scale, times the sum of the codes' magnitudes.  (A column of values that is
+    zero wherever the softmax has weight showed that this term was missing: its result, 2e-8 of the
+    other columns', comes from weights below fp16's last step.)"""
     dz = (d + 8) * 2.0 ** -24 * zabs + 2.0 ** -25 * qabs + 2.0 ** -21
-    err = weight * (2 * dz + 2.0 ** -11 + T * 2.0 ** -24 + 2.0 ** -20)
+    err = weight * (2 * dz + 2.0 ** -11 + T * 2.0 ** -24 + 2.0 ** -20) + 2.0 ** -25 * least
     return (err + 2.0 ** -8 * (np.abs(out) + err) + 1e-30,
             dz + T * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -23 * abs(lse))
