@@ -6,42 +6,48 @@
 // for the R = G n query rows of a KV head.  Every key and value is read once for
 // all rows, 2 d bytes a token, and the arithmetic on it is 4 R d operations: the
 // kernel is bound by memory as long as the instructions around the loads keep up.
-// A warp therefore takes its tokens straight from global memory into registers,
-// in the layout the tensor-core instruction wants (no shared memory, no barrier in
-// the loop), and holds the next 16 tokens' loads in flight while it works on the
-// present ones.
+// Each warp has tokens and a ring of stages in shared memory of its own: 32 tokens'
+// keys, values and scales a stage, filled by asynchronous 16-byte copies (absent
+// tokens are filled with zeros), so that the loop has no barrier and enough bytes
+// in flight to cover the latency of HBM.
 //
 // Per 16 tokens a warp computes S^T = K Q^T (m16n8k16, tokens on the M axis) and
 // O^T += V^T P^T (values on the M axis), so that the 8 columns are query rows and
 // nothing is wasted on a 16-row query tile that has 7 rows.  The order of d inside
-// the products is free: a lane's 16-byte load of a key row is four k-slices' worth
-// of its A fragment as it stands, with Q loaded in the same order; a lane's value
-// loads (16 bytes of 4 tokens) become A fragments by two byte permutes for each
-// pair of tokens.  Codes are converted to fp16, which holds both formats exactly;
-// q is scaled by a power of two per row so that fp16 holds it as well.
+// the products is free: 16 bytes of a key row are four k-slices' worth of a lane's A
+// fragment as they stand, with Q loaded in the same order; 16 bytes of 4 tokens'
+// values become A fragments by two byte permutes for each pair of tokens.  The
+// 16-byte chunks of a row are swizzled so that both reads are free of bank
+// conflicts (of 128 values; 64 have one on the values).  Codes are converted to
+// fp16, which holds both formats exactly; q is scaled by a power of two per row so
+// that fp16 holds it as well.
 //
 // The softmax is kept in base 2 with a running maximum.  The value scale 2^e of a
 // token's block joins its logit (x = z + e) instead of its weight, so that the
 // fp16 weights of the second product stay near 1 whatever the blocks' scales are;
 // the sum uses 2^-e again, in fp32.  The maximum is only raised when a logit
 // passes it by 2^8 (fp16 has the room), which turns the reduction over lanes into
-// one vote per 16 tokens.
+// one vote per 32 tokens.
 //
-// Tokens are split over the warps of a CTA and, when the heads alone do not fill
-// the GPU, over CTAs; the last CTA of a head to finish joins the parts in order.
+// Work is the list of all heads' steps of 32 tokens, one after another; every CTA
+// takes an equal stretch of it, whatever the lengths are, and walks the heads that
+// it meets.  A head that lies in one stretch is finished there; the parts of one
+// that does not go to the workspace, and the last CTA of it to finish joins them in
+// order (the result does not depend on which one that is).
+#include <atomic>
+
 #include "cache8.cuh"
 
 namespace kvc {
 namespace cache8 {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16;          // tokens of one step of a warp
-constexpr int kRowTile = 16;       // query rows of a CTA at most
-constexpr int kMaxParts = 2048;    // CTAs of a call that splits sequences
-constexpr int kMinTiles = 2 * kWarps;  // tiles of a part at least
-constexpr float kSlack = 8.f;      // log2 of how far a weight may pass 1
+constexpr int kTile = 32;        // tokens of one step of a warp
+constexpr int kRowTile = 16;     // query rows of a stretch at most
+constexpr int kStages = 2;
+constexpr int kSmWarps = 12;     // warps of an SM, by registers and shared memory
+constexpr int kMaxCtas = 512;    // CTAs of a call
+constexpr float kSlack = 8.f;    // log2 of how far a weight may pass 1
 
 // Division by the block size: floor(t / bs) = umulhi(t, mul) >> shift for
 // 0 <= t < 2^31 (bs > 1).
@@ -60,26 +66,39 @@ Div make_div(int bs) {
 }
 
 struct Split {
-  int per_unit;    // CTAs of a head and row tile
-  int row_tiles;
-  float* part;     // [kMaxParts][kRowTile][D + 2]
-  int* arrived;    // [kMaxParts] zero between calls
+  int row_tiles;  // of a head
+  float* part;    // [2 kMaxCtas][kRowTile][D + 2]: maximum, sum, values
+  int* arrived;   // [kMaxCtas] zero between calls
 };
 
-__device__ __forceinline__ uint4 load16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// Asynchronous copies global -> shared; where `there` is false, zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+               "r"(there ? 16 : 0)
+               : "memory");
 }
-__device__ __forceinline__ uint2 load8(const uint8_t* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void copy4(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from),
+               "r"(there ? 4 : 0)
+               : "memory");
 }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A stage of a warp's ring: kTile rows of keys, as many of values, their scales.
+template <int D>
+struct Stage {
+  static constexpr int kKeys = 0, kValues = kTile * D, kKeyScales = 2 * kTile * D,
+                       kValueScales = kKeyScales + kTile * 4, kBytes = kValueScales + kTile * 4;
+  // place of 16-byte chunk ch of row r
+  static __device__ __forceinline__ int at(int r, int ch) {
+    const int f = D == 128 ? ((((r >> 1) & 3) << 1) ^ ((r & 1) << 2)) : ((r >> 1) & 3);
+    return r * D + ((ch ^ f) << 4);
+  }
+};
 
 // Codes as signed integers, biased to 0..255, behind the exponent of 1024: the
 // fp16 number 1024 + u, from which 1152 leaves the value.
@@ -123,399 +142,541 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {
   return r;
 }
 
-// One row tile of one head over one part of its tokens.
-template <int D, int FMT, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
+template <int D, int NT, int W>
+constexpr int smem_bytes() {
+  const int ring = W * kStages * Stage<D>::kBytes, parts = W * 8 * NT * (D + 4) * 4;
+  return ring > parts ? ring : parts;
+}
+
+// Inclusive scan over a CTA of W warps; every thread gets the total too.
+template <int W>
+__device__ __forceinline__ long long scan(long long v, long long* sums, long long* total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  if (lane == 31) sums[warp] = v;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) before += sums[w];
+    all += sums[w];
+  }
+  __syncthreads();
+  *total = all;
+  return v + before;
+}
+
+// Steps of one head of sequence b; 0 for one that has no queries or is refused.
+__device__ __forceinline__ int steps_of(const Cache& c, const AttendArgs& a, int b, bool* bad) {
+  bool wrong = false;
+  const int len = length_of(c, b, &wrong);
+  const int nq = a.n_q ? a.n_q[b] : a.n;
+  if (wrong || nq < 0 || nq > a.n) {
+    *bad = true;
+    return 0;
+  }
+  return nq == 0 ? 0 : max((len + kTile - 1) / kTile, 1);
+}
+
+// Write kPer values of a row and, with the first ones, its lse.
+constexpr int kPer = 8;
+__device__ __forceinline__ void write_row(const Cache& c, const AttendArgs& a, int l, int b, int h,
+                                          int r, int nq, int d0, const float (&x)[kPer], float m,
+                                          float sum) {
+  const int hq = h * a.G + r / nq, j = r % nq;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  *reinterpret_cast<uint4*>(a.out.at(l, b, hq, j) + d0) =
+      make_uint4(bf16x2(x[0] * inv, x[1] * inv), bf16x2(x[2] * inv, x[3] * inv),
+                 bf16x2(x[4] * inv, x[5] * inv), bf16x2(x[6] * inv, x[7] * inv));
+  if (a.lse && d0 == 0)
+    a.lse[((static_cast<size_t>(l) * c.B + b) * c.H * a.G + hq) * a.n + j] =
+        (m + __log2f(sum)) * 0.6931471805599453f;
+}
+
+template <int D, int FMT, int NT, int W>
+__global__ void __launch_bounds__(32 * W, kSmWarps / W)
     attend_few_kernel(Cache c, AttendArgs a, Split sp, Div by_bs) {
   constexpr int KV = D / 64;   // 16-byte loads of a key row per lane
   constexpr int MT = D / 16;   // 16-value tiles of the output
   constexpr int Q = 8 * NT;    // query rows
   constexpr int OS = D + 4;    // row stride of the parts in shared memory
-  __shared__ float s_o[kWarps][Q][OS];
-  __shared__ float s_m[kWarps][Q], s_l[kWarps][Q];
-  __shared__ int s_last;
+  constexpr int TPR = D / kPer;
+  constexpr int kThreads = 32 * W;
+  using St = Stage<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  auto s_o = reinterpret_cast<float(*)[Q][OS]>(smem);  // after a head's loop, the warps' parts
+  __shared__ float s_m[W][Q], s_l[W][Q];
+  __shared__ long long s_scan[W];
+  __shared__ int s_seq, s_last;
+  __shared__ long long s_off;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, q4 = lane % 4;
-  const int part = blockIdx.x % sp.per_unit;
-  const int ur = blockIdx.x / sp.per_unit;  // unit and row tile
-  const int rt = ur % sp.row_tiles;
-  const int u = ur / sp.row_tiles;
-  const int h = u % c.H, b = (u / c.H) % c.B, l = u / (c.H * c.B);
   bool bad = false;
-  const int len = length_of(c, b, &bad);
-  const int nq = a.n_q ? a.n_q[b] : a.n;
-  if (bad || nq < 0 || nq > a.n) {
-    if (threadIdx.x == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
+
+  // ---- this CTA's stretch [lo, hi) of all steps, and the head that it begins in ----
+  const int heads = c.H * sp.row_tiles;  // of one sequence and layer
+  long long layer_steps, at;
+  {
+    long long mine = 0;
+    for (int b = threadIdx.x; b < c.B; b += kThreads) mine += steps_of(c, a, b, &bad);
+    if (blockIdx.x != 0) bad = false;  // one report is enough
+    scan<W>(mine, s_scan, &layer_steps);
+    layer_steps *= heads;
+  }
+  const long long total = layer_steps * c.L;
+  const long long n_cta = min(static_cast<long long>(gridDim.x), (total + W - 1) / W);
+  if (blockIdx.x >= n_cta) {
+    if (bad) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
     return;
   }
-  const int rows = min(a.G * nq - rt * Q, Q);  // rows of this tile: r = rt * Q + 0..rows-1
-  if (rows <= 0) return;
-  // the parts of this sequence: `per` tiles each
-  const int tiles = (len + kTile - 1) / kTile;
-  const int per = max((tiles + sp.per_unit - 1) / sp.per_unit, kMinTiles);
-  const int parts = max((tiles + per - 1) / per, 1);
-  if (part >= parts) return;
-  const int tile_end = min((part + 1) * per, tiles);
-
-  // ---- queries: row g of each 8-row tile, in the order of the key loads ----
-  // row r is head r / nq, query r % nq
-  uint32_t qf[NT][KV * 4][2];
-  float qscale[NT][2];  // of rows 2 q4, 2 q4 + 1: scale log2(e) 2^e
-  int limit[NT][2];     // last token that they see
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = rt * Q + nt * 8 + g;
-    const bool there = nt * 8 + g < rows;
-    uint4 w[KV][2];
-    float mx = 0.f;
-    const uint16_t* qp = a.q.at(l, b, h * a.G + (there ? r / nq : 0), there ? r % nq : 0);
-#pragma unroll
-    for (int k = 0; k < KV; ++k)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        w[k][i] = there ? __ldg(reinterpret_cast<const uint4*>(qp + (k * 4 + q4) * 16 + i * 8))
-                        : make_uint4(0, 0, 0, 0);
-        const uint32_t x[4] = {w[k][i].x, w[k][i].y, w[k][i].z, w[k][i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
+  auto first_of = [&](long long cta) { return total * cta / n_cta; };
+  const long long lo = first_of(blockIdx.x), hi = first_of(blockIdx.x + 1);
+  int l = static_cast<int>(lo / layer_steps);
+  {
+    const long long want = lo % layer_steps;
+    long long before = 0;  // of earlier chunks of sequences
+    for (int b0 = 0; b0 < c.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      bool unused = false;
+      const long long n = b < c.B ? static_cast<long long>(steps_of(c, a, b, &unused)) * heads : 0;
+      long long chunk;
+      const long long end = before + scan<W>(n, s_scan, &chunk);
+      if (n > 0 && want >= end - n && want < end) {
+        s_seq = b;
+        s_off = want - (end - n);
       }
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // the row's largest magnitude to [1, 2)
-    const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
-    const float down = exp2_int(-e);
-#pragma unroll
-    for (int k = 0; k < KV; ++k)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t x[4] = {w[k][i].x, w[k][i].y, w[k][i].z, w[k][i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          qf[nt][k * 4 + i * 2 + j / 2][j % 2] = half2_of(bf16_lo(x[j]) * down, bf16_hi(x[j]) * down);
-      }
-    const float up = a.scale_log2 * exp2_int(e);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      qscale[nt][i] = __shfl_sync(0xffffffffu, up, (2 * q4 + i) * 4);
-      const int rr = rt * Q + nt * 8 + 2 * q4 + i;
-      limit[nt][i] = len - nq + rr % nq;
+      before += chunk;
+      if (want < before) break;
     }
   }
+  __syncthreads();
+  int b = s_seq;
+  at = lo;
+  bool unused = false;
+  int steps = steps_of(c, a, b, &unused);  // of a head of this sequence
+  int head = static_cast<int>(s_off / steps), begin = static_cast<int>(s_off % steps);
 
-  float o[NT][MT][4];
-  float m[NT][2], sum[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
-    m[nt][0] = m[nt][1] = -INFINITY;
-    sum[nt][0] = sum[nt][1] = 0.f;
-  }
+  uint8_t* ring = smem + warp * (kStages * St::kBytes);
+  const uint32_t ring_addr = smem_u32(ring);
 
-  const uint8_t* kp = c.pool[0] + block_row(c, l, 0, h) * D;
-  const uint8_t* vp = c.pool[1] + block_row(c, l, 0, h) * D;
-  const float* ksp = c.scale[0] + scale_at(c, l, 0, h);
-  const float* vsp = c.scale[1] + scale_at(c, l, 0, h);
-  const int32_t* table = c.table + static_cast<size_t>(b) * c.max_blocks;
+  for (;;) {
+    const int h = head / sp.row_tiles, rt = head % sp.row_tiles;
+    const int end = static_cast<int>(min(static_cast<long long>(steps), begin + (hi - at)));
+    const int len = c.seq_len[b];
+    const int nq = a.n_q ? a.n_q[b] : a.n;
+    const int rows = min(a.G * nq - rt * Q, Q);  // of this tile: r = rt * Q + 0..rows-1
+    const int32_t* table = c.table + static_cast<size_t>(b) * c.max_blocks;
+    const uint8_t* kp = c.pool[0] + block_row(c, l, 0, h) * D;
+    const uint8_t* vp = c.pool[1] + block_row(c, l, 0, h) * D;
+    const float* ksp = c.scale[0] + scale_at(c, l, 0, h);
+    const float* vsp = c.scale[1] + scale_at(c, l, 0, h);
 
-  // Lane i (and i + 16) looks after token i of a tile: its block two tiles ahead,
-  // its row and scales one tile ahead.
-  const int tok = lane % 16;
-  auto block_of = [&](int tile) {
-    const int t = tile * kTile + tok;
-    return tile < tile_end && t < len ? __ldg(table + by_bs.div(t)) : -1;
-  };
-  int row = -1;        // of the tile whose loads are in flight
-  float ks = 0.f, vs = 1.f;
-  auto resolve = [&](int tile, int blk) {
-    const int t = tile * kTile + tok;
-    row = -1;
-    ks = 0.f;
-    vs = 1.f;
-    if (tile < tile_end && t < len) {
-      if (blk < 0 || blk >= c.n_blocks) {
-        bad = true;
-      } else {
-        const int in = t - by_bs.div(t) * by_bs.bs;
-        row = blk * c.H * by_bs.bs + in;  // below 2^31: checked on the host
-        ks = __ldg(ksp + static_cast<size_t>(blk) * c.H);
-        vs = __ldg(vsp + static_cast<size_t>(blk) * c.H);
+    // Lane i looks after token i of a step.
+    auto block_of = [&](int step) {
+      const int t = step * kTile + lane;
+      return step < end && t < len ? __ldg(table + by_bs.div(t)) : -1;
+    };
+    // start the copies of a step, whose tokens lie in the lanes' blocks `blk`
+    auto fetch = [&](int step, int blk, int stage) {
+      const uint32_t to = ring_addr + stage * St::kBytes;
+      if (step < end) {
+        const int t = step * kTile + lane;
+        int row = -1;
+        if (t < len) {
+          if (blk < 0 || blk >= c.n_blocks)
+            bad = true;
+          else
+            row = blk * c.H * by_bs.bs + (t - by_bs.div(t) * by_bs.bs);  // < 2^31: checked on the host
+        }
+        const size_t sc = row < 0 ? 0 : static_cast<size_t>(blk) * c.H;
+        copy4(to + St::kKeyScales + lane * 4, ksp + sc, row >= 0);
+        copy4(to + St::kValueScales + lane * 4, vsp + sc, row >= 0);
+        constexpr int CH = D / 16, RPI = 32 / CH;  // chunks of a row, rows of one copy
+#pragma unroll
+        for (int i = 0; i < kTile / RPI; ++i) {
+          const int r = lane / CH + i * RPI, ch = lane % CH;
+          const int from = __shfl_sync(0xffffffffu, row, r);
+          const size_t off = static_cast<size_t>(max(from, 0)) * D + ch * 16;
+          copy16(to + St::kKeys + St::at(r, ch), kp + off, from >= 0);
+          copy16(to + St::kValues + St::at(r, ch), vp + off, from >= 0);
+        }
       }
-    }
-  };
-  uint4 kr[2][KV];
-  uint4 vr[4];
-  auto load_keys = [&]() {
+      copies_commit();
+    };
+
+    int step = rows > 0 ? begin + warp : end;
+    int blk = block_of(step);
+    int next = block_of(step + W);
+    fetch(step, blk, 0);
+    int stage = 0;
+
+    // ---- queries: row g of each 8-row tile, in the order of the key reads ----
+    // row r is head r / nq of the group, query r % nq
+    uint32_t qf[NT][KV * 4][2];
+    float qscale[NT][2];  // of rows 2 q4, 2 q4 + 1: scale log2(e) 2^e
+    int limit[NT][2];     // last token that they see
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = __shfl_sync(0xffffffffu, row, g + 8 * i);
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = rt * Q + nt * 8 + g;
+      const bool there = nt * 8 + g < rows;
+      uint4 w[KV][2];
+      float mx = 0.f;
+      const uint16_t* qp = a.q.at(l, b, h * a.G + (there ? r / nq : 0), there ? r % nq : 0);
 #pragma unroll
       for (int k = 0; k < KV; ++k)
-        kr[i][k] = r >= 0 ? load16(kp + static_cast<size_t>(r) * D + (k * 4 + q4) * 16)
-                          : make_uint4(0, 0, 0, 0);
-    }
-  };
-  auto load_values = [&]() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = __shfl_sync(0xffffffffu, row, 2 * q4 + (i & 1) + 8 * (i >> 1));
-      if constexpr (D == 128) {
-        vr[i] = r >= 0 ? load16(vp + static_cast<size_t>(r) * D + g * 16) : make_uint4(0, 0, 0, 0);
-      } else {
-        const uint2 v = r >= 0 ? load8(vp + static_cast<size_t>(r) * D + g * 8) : make_uint2(0, 0);
-        vr[i] = make_uint4(v.x, v.y, 0, 0);
+        for (int i = 0; i < 2; ++i) {
+          w[k][i] = there ? __ldg(reinterpret_cast<const uint4*>(qp + (k * 4 + q4) * 16 + i * 8))
+                          : make_uint4(0, 0, 0, 0);
+          const uint32_t x[4] = {w[k][i].x, w[k][i].y, w[k][i].z, w[k][i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(x[j])), fabsf(bf16_hi(x[j]))));
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // the row's largest magnitude to [1, 2)
+      const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      const float down = exp2_int(-e);
+#pragma unroll
+      for (int k = 0; k < KV; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t x[4] = {w[k][i].x, w[k][i].y, w[k][i].z, w[k][i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            qf[nt][k * 4 + i * 2 + j / 2][j % 2] =
+                half2_of(bf16_lo(x[j]) * down, bf16_hi(x[j]) * down);
+        }
+      const float up = a.scale_log2 * exp2_int(e);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        qscale[nt][i] = __shfl_sync(0xffffffffu, up, (2 * q4 + i) * 4);
+        limit[nt][i] = len - nq + (rt * Q + nt * 8 + 2 * q4 + i) % nq;
       }
     }
-  };
 
-  int tile = part * per + warp;
-  int blk = block_of(tile);
-  resolve(tile, blk);
-  blk = block_of(tile + kWarps);
-  load_keys();
-  load_values();
-  for (; tile < tile_end; tile += kWarps) {
-    const int t0 = tile * kTile;
-    // this tile's scales and which of its tokens are there, by lane
-    const float ks_now = ks, vs_now = vs;
-    const int row_now = row;
-    resolve(tile + kWarps, blk);
-    blk = block_of(tile + 2 * kWarps);
+    float o[NT][MT][4];
+    float m[NT][2], sum[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      sum[nt][0] = sum[nt][1] = 0.f;
+    }
 
-    // ---- S^T = K Q^T ----
-    float z[NT][4];
+    for (; step < end; step += W) {
+      const int t0 = step * kTile;
+      fetch(step + W, next, stage ^ 1);
+      next = block_of(step + 2 * W);
+      copies_wait<1>();
+      __syncwarp();  // all lanes' copies of this step are there
+      const uint8_t* st = ring + stage * St::kBytes;
+      stage ^= 1;
+
+      // ---- S^T = K Q^T ----
+      float z[2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[mt][nt][j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KV; ++k)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint8_t* keys = st + St::kKeys;
+          const uint4 k0 = *reinterpret_cast<const uint4*>(keys + St::at(mt * 16 + g, k * 4 + q4));
+          const uint4 k1 =
+              *reinterpret_cast<const uint4*>(keys + St::at(mt * 16 + g + 8, k * 4 + q4));
+          const uint32_t x[4] = {k0.x, k0.y, k0.z, k0.w};
+          const uint32_t y[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a0, a1, a2, a3;
+            halves<FMT>(x[j], a0, a2);
+            halves<FMT>(y[j], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma(z[mt][nt], a0, a1, a2, a3, qf[nt][k * 4 + j][0], qf[nt][k * 4 + j][1]);
+          }
+        }
+
+      // ---- weights: this lane's tokens are g + 8 i ----
+      const float* k_scales = reinterpret_cast<const float*>(st + St::kKeyScales);
+      const float* v_scales = reinterpret_cast<const float*>(st + St::kValueScales);
+      float back[4];  // 2^-e, 0 for an absent token
+      const bool whole = t0 + kTile <= len - nq + 1;  // every query sees the step
+      bool up = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float ks = k_scales[g + 8 * i], vs = v_scales[g + 8 * i];
+        const int e = static_cast<int>(__float_as_uint(vs) >> 23) - 127;
+        const float ef = vs == 0.f ? -INFINITY : static_cast<float>(e);
+        back[i] = vs == 0.f ? 0.f : exp2_int(-e);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float& x = z[i / 2][nt][(i % 2) * 2 + j];
+            // (an absent token's product is 0: its key and scale are)
+            x = fmaf(x, ks * qscale[nt][j], ef);
+            if (vs == 0.f || (!whole && t0 + g + 8 * i > limit[nt][j])) x = -INFINITY;
+            up = up || x > m[nt][j] + kSlack;
+          }
+      }
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float x = fmaxf(fmaxf(z[0][nt][j], z[0][nt][2 + j]), fmaxf(z[1][nt][j], z[1][nt][2 + j]));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            x = fmaxf(x, m[nt][j]);
+            const float f = x > m[nt][j] ? ex2(m[nt][j] - x) : 1.f;
+            m[nt][j] = x;
+            sum[nt][j] *= f;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              o[nt][t][j] *= f;
+              o[nt][t][2 + j] *= f;
+            }
+          }
+      }
+      uint32_t p[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w0 = ex2(z[i / 2][nt][(i % 2) * 2] - m0);
+          const float w1 = ex2(z[i / 2][nt][(i % 2) * 2 + 1] - m1);
+          sum[nt][0] = fmaf(w0, back[i], sum[nt][0]);
+          sum[nt][1] = fmaf(w1, back[i], sum[nt][1]);
+          p[i / 2][nt][i % 2] = transpose8x8(half2_of(w0, w1));
+        }
+      }
+
+      // ---- O^T += V^T P^T ----
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        uint32_t vr[4][MT / 2];  // 2 MT codes of the tokens 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = kt * 16 + 2 * q4 + (i & 1) + 8 * (i >> 1);
+          const uint8_t* from = st + St::kValues + St::at(r, g * MT / 8) + (g * 2 * MT) % 16;
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(from);
+            vr[i][0] = v.x, vr[i][1] = v.y, vr[i][2] = v.z, vr[i][3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(from);
+            vr[i][0] = v.x, vr[i][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < MT / 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t sel = i == 0 ? 0x5140 : 0x7362;
+            uint32_t a0, a1, a2, a3;
+            halves<FMT>(__byte_perm(vr[0][j], vr[1][j], sel), a0, a1);
+            halves<FMT>(__byte_perm(vr[2][j], vr[3][j], sel), a2, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma(o[nt][2 * j + i], a0, a1, a2, a3, p[kt][nt][0], p[kt][nt][1]);
+          }
+      }
+      __syncwarp();  // every lane has read the stage before it is filled again
+    }
+
+    // ---- join the warps ----
+    copies_wait<0>();
+    __syncthreads();  // the rings become the parts
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) z[nt][j] = 0.f;
-#pragma unroll
-    for (int k = 0; k < KV; ++k) {
-      const uint32_t x[4] = {kr[0][k].x, kr[0][k].y, kr[0][k].z, kr[0][k].w};
-      const uint32_t y[4] = {kr[1][k].x, kr[1][k].y, kr[1][k].z, kr[1][k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t a0, a1, a2, a3;
-        halves<FMT>(x[j], a0, a2);
-        halves<FMT>(y[j], a1, a3);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma(z[nt], a0, a1, a2, a3, qf[nt][k * 4 + j][0], qf[nt][k * 4 + j][1]);
-      }
-    }
-    load_keys();
-
-    // ---- weights ----
-    const float ks0 = __shfl_sync(0xffffffffu, ks_now, g);
-    const float ks1 = __shfl_sync(0xffffffffu, ks_now, g + 8);
-    const int there0 = __shfl_sync(0xffffffffu, row_now, g);
-    const int there1 = __shfl_sync(0xffffffffu, row_now, g + 8);
-    const float vs0 = __shfl_sync(0xffffffffu, vs_now, g);
-    const float vs1 = __shfl_sync(0xffffffffu, vs_now, g + 8);
-    const float e0 = static_cast<float>(static_cast<int>(__float_as_uint(vs0) >> 23) - 127);
-    const float e1 = static_cast<float>(static_cast<int>(__float_as_uint(vs1) >> 23) - 127);
-    const bool whole = t0 + kTile <= len - nq + 1;  // every query sees the tile
-    bool up = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float x0 = fmaf(z[nt][i], ks0 * qscale[nt][i], e0);
-        float x1 = fmaf(z[nt][2 + i], ks1 * qscale[nt][i], e1);
-        if (there0 < 0 || (!whole && t0 + g > limit[nt][i])) x0 = -INFINITY;
-        if (there1 < 0 || (!whole && t0 + g + 8 > limit[nt][i])) x1 = -INFINITY;
-        z[nt][i] = x0;
-        z[nt][2 + i] = x1;
-        up = up || fmaxf(x0, x1) > m[nt][i] + kSlack;
-      }
-    }
-    if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float x = fmaxf(z[nt][i], z[nt][2 + i]);
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          x = fmaxf(x, m[nt][i]);
-          const float f = x > m[nt][i] ? ex2(m[nt][i] - x) : 1.f;
-          m[nt][i] = x;
-          sum[nt][i] *= f;
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            o[nt][t][i] *= f;
-            o[nt][t][2 + i] *= f;
-          }
+        float s = sum[nt][i];
+        s += __shfl_xor_sync(0xffffffffu, s, 4);
+        s += __shfl_xor_sync(0xffffffffu, s, 8);
+        s += __shfl_xor_sync(0xffffffffu, s, 16);
+        const int r = nt * 8 + 2 * q4 + i;
+        if (g == 0) {
+          s_m[warp][r] = m[nt][i];
+          s_l[warp][r] = s;
         }
-    }
-    const float back0 = exp2_int(-static_cast<int>(e0)), back1 = exp2_int(-static_cast<int>(e1));
-    uint32_t p[NT][2];
+        // this lane's values: tile t has d = 2 (g MT + t) in c0/c1 and one more in c2/c3
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float w[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float mm = m[nt][i] == -INFINITY ? 0.f : m[nt][i];
-        w[i] = ex2(z[nt][i] - mm);
-        w[2 + i] = ex2(z[nt][2 + i] - mm);
-        sum[nt][i] += w[i] * back0 + w[2 + i] * back1;
+        for (int t = 0; t < MT; t += 2)
+          *reinterpret_cast<float4*>(&s_o[warp][r][2 * (g * MT + t)]) =
+              make_float4(o[nt][t][i], o[nt][t][2 + i], o[nt][t + 1][i], o[nt][t + 1][2 + i]);
       }
-      p[nt][0] = transpose8x8(half2_of(w[0], w[1]));
-      p[nt][1] = transpose8x8(half2_of(w[2], w[3]));
+    __syncthreads();
+    constexpr size_t kSlot = static_cast<size_t>(kRowTile) * (D + 2);
+    const bool whole_head = begin == 0 && end == steps;
+    float* slot = sp.part + (2 * static_cast<size_t>(blockIdx.x) + (begin == 0 ? 1 : 0)) * kSlot;
+    for (int i = threadIdx.x; i < Q * TPR; i += kThreads) {
+      const int r = i / TPR, d0 = (i % TPR) * kPer;
+      if (r >= rows) continue;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < W; ++w) mm = fmaxf(mm, s_m[w][r]);
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      float x[kPer], s = 0.f;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) x[k] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = ex2(s_m[w][r] - ref);
+        s += f * s_l[w][r];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) x[k] += f * s_o[w][r][d0 + k];
+      }
+      if (whole_head) {
+        write_row(c, a, l, b, h, rt * Q + r, nq, d0, x, mm, s);
+      } else {
+        float* to = slot + r * (D + 2);
+#pragma unroll
+        for (int k = 0; k < kPer; k += 2)
+          *reinterpret_cast<float2*>(to + 2 + d0 + k) = make_float2(x[k], x[k + 1]);
+        if (d0 == 0) *reinterpret_cast<float2*>(to) = make_float2(mm, s);
+      }
     }
 
-    // ---- O^T += V^T P^T ----
+    // ---- join the parts of a head: the last CTA of it to arrive ----
+    if (!whole_head && rows > 0) {
+      // the CTAs that have a stretch of this head: the one with its first step to the
+      // one with its last
+      const long long head_lo = at - begin, head_hi = head_lo + steps;
+      auto owner = [&](long long step_at) {
+        long long k = step_at * n_cta / total;  // first_of(k) <= step_at up to rounding
+        while (first_of(k + 1) <= step_at) ++k;
+        while (first_of(k) > step_at) --k;
+        return static_cast<int>(k);
+      };
+      const int c0 = owner(head_lo), c1 = owner(head_hi - 1), n_part = c1 - c0 + 1;
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) s_last = atomicAdd(&sp.arrived[c0], 1) == n_part - 1;
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        if (threadIdx.x == 0) sp.arrived[c0] = 0;  // ready for the next call
+        // the first CTA's part of a head that begins in it, then the others'
+        auto part_of = [&](int i) {
+          return sp.part + (2 * static_cast<size_t>(c0 + i) + (i == 0 ? 1 : 0)) * kSlot;
+        };
+        for (int i = threadIdx.x; i < Q * TPR; i += kThreads) {
+          const int r = i / TPR, d0 = (i % TPR) * kPer;
+          if (r >= rows) continue;
+          float mm = -INFINITY, x[kPer], s = 0.f;
 #pragma unroll
-    for (int j = 0; j < MT / 2; ++j) {
-      const uint32_t x[4] = {j == 0 ? vr[0].x : j == 1 ? vr[0].y : j == 2 ? vr[0].z : vr[0].w,
-                             j == 0 ? vr[1].x : j == 1 ? vr[1].y : j == 2 ? vr[1].z : vr[1].w,
-                             j == 0 ? vr[2].x : j == 1 ? vr[2].y : j == 2 ? vr[2].z : vr[2].w,
-                             j == 0 ? vr[3].x : j == 1 ? vr[3].y : j == 2 ? vr[3].z : vr[3].w};
+          for (int k = 0; k < kPer; ++k) x[k] = 0.f;
+          // a few parts at a time, all their loads in flight together
+          constexpr int kBatch = 4;
+          for (int w0 = 0; w0 < n_part; w0 += kBatch) {
+            float2 ml[kBatch], v[kBatch][kPer / 2];
+            float top = mm;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t sel = i == 0 ? 0x5140 : 0x7362;
-        uint32_t a0, a1, a2, a3;
-        halves<FMT>(__byte_perm(x[0], x[1], sel), a0, a1);
-        halves<FMT>(__byte_perm(x[2], x[3], sel), a2, a3);
+            for (int w = 0; w < kBatch; ++w) {
+              const float* from = part_of(min(w0 + w, n_part - 1)) + r * (D + 2);
+              ml[w] = __ldcg(reinterpret_cast<const float2*>(from));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma(o[nt][2 * j + i], a0, a1, a2, a3, p[nt][0], p[nt][1]);
+              for (int k = 0; k < kPer / 2; ++k)
+                v[w][k] = __ldcg(reinterpret_cast<const float2*>(from + 2 + d0) + k);
+            }
+#pragma unroll
+            for (int w = 0; w < kBatch; ++w) {
+              if (w0 + w >= n_part) ml[w] = make_float2(-INFINITY, 0.f);
+              top = fmaxf(top, ml[w].x);
+            }
+            const float ref = top == -INFINITY ? 0.f : top;
+            const float keep = mm == -INFINITY ? 0.f : ex2(mm - ref);
+            s *= keep;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) x[k] *= keep;
+            mm = top;
+#pragma unroll
+            for (int w = 0; w < kBatch; ++w) {
+              if (w0 + w < n_part) {
+                const float f = ex2(ml[w].x - ref);
+                s += f * ml[w].y;
+#pragma unroll
+                for (int k = 0; k < kPer / 2; ++k) {
+                  x[2 * k] += f * v[w][k].x;
+                  x[2 * k + 1] += f * v[w][k].y;
+                }
+              }
+            }
+          }
+          write_row(c, a, l, b, h, rt * Q + r, nq, d0, x, mm, s);
+        }
       }
     }
-    load_values();
+
+    // ---- the next head ----
+    at += end - begin;
+    if (at >= hi) break;
+    begin = 0;
+    if (++head == heads) {
+      head = 0;
+      do {
+        if (++b == c.B) {
+          b = 0;
+          ++l;
+        }
+        steps = steps_of(c, a, b, &unused);
+      } while (steps == 0);
+    }
+    __syncthreads();  // the parts become the rings again
   }
-
-  // ---- join the warps ----
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float s = sum[nt][i];
-      s += __shfl_xor_sync(0xffffffffu, s, 4);
-      s += __shfl_xor_sync(0xffffffffu, s, 8);
-      s += __shfl_xor_sync(0xffffffffu, s, 16);
-      const int r = nt * 8 + 2 * q4 + i;
-      if (g == 0) {
-        s_m[warp][r] = m[nt][i];
-        s_l[warp][r] = s;
-      }
-      // this lane's values: tile t has d = 2 (g MT + t) in c0/c1 and one more in c2/c3
-#pragma unroll
-      for (int t = 0; t < MT; t += 2)
-        *reinterpret_cast<float4*>(&s_o[warp][r][2 * (g * MT + t)]) =
-            make_float4(o[nt][t][i], o[nt][t][2 + i], o[nt][t + 1][i], o[nt][t + 1][2 + i]);
-    }
   if (bad) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
-  __syncthreads();
+}
 
-  // a thread has kPer neighbouring values of a row
-  constexpr int kPer = 8;
-  constexpr int TPR = D / kPer;  // threads of a row
-  const size_t slot_floats = static_cast<size_t>(kRowTile) * (D + 2);
-  float* mine = sp.part + static_cast<size_t>(blockIdx.x) * slot_floats;
-  for (int i = threadIdx.x; i < Q * TPR; i += kThreads) {
-    const int r = i / TPR, d0 = (i % TPR) * kPer;
-    if (r >= rows) continue;
-    float mm = s_m[0][r];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
-    const float ref = mm == -INFINITY ? 0.f : mm;
-    float x[kPer], s = 0.f;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) x[k] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(s_m[w][r] - ref);
-      s += f * s_l[w][r];
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) x[k] += f * s_o[w][r][d0 + k];
-    }
-    if (parts > 1) {
-      float* to = mine + r * (D + 2);
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) to[2 + d0 + k] = x[k];
-      if (d0 == 0) {
-        to[0] = mm;
-        to[1] = s;
-      }
-    } else {
-      const int rr = rt * Q + r;
-      const int hq = h * a.G + rr / nq, j = rr % nq;
-      const float inv = s == 0.f ? 0.f : 1.f / s;
-      *reinterpret_cast<uint4*>(a.out.at(l, b, hq, j) + d0) =
-          make_uint4(bf16x2(x[0] * inv, x[1] * inv), bf16x2(x[2] * inv, x[3] * inv),
-                     bf16x2(x[4] * inv, x[5] * inv), bf16x2(x[6] * inv, x[7] * inv));
-      if (a.lse && d0 == 0)
-        a.lse[((static_cast<size_t>(l) * c.B + b) * c.H * a.G + hq) * a.n + j] =
-            (mm + __log2f(s)) * 0.6931471805599453f;
-    }
+template <int D, int FMT, int NT, int W>
+cudaError_t launch_few(const Cache& c, const AttendArgs& a, const Split& sp, cudaStream_t s) {
+  constexpr int smem = smem_bytes<D, NT, W>();
+  auto* kernel = attend_few_kernel<D, FMT, NT, W>;
+  // beyond 48 KB a kernel has to be told so, once per device
+  static std::atomic<uint64_t> told{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(told.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) told.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  if (parts == 1) return;
-
-  // ---- join the parts: the last CTA to arrive, in the order of the parts ----
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) s_last = atomicAdd(&sp.arrived[ur], 1) == parts - 1;
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  if (threadIdx.x == 0) sp.arrived[ur] = 0;  // ready for the next call
-  const float* first = sp.part + static_cast<size_t>(ur) * sp.per_unit * slot_floats;
-  for (int i = threadIdx.x; i < Q * TPR; i += kThreads) {
-    const int r = i / TPR, d0 = (i % TPR) * kPer;
-    if (r >= rows) continue;
-    const float* from = first + r * (D + 2);
-    float mm = -INFINITY;
-    for (int w = 0; w < parts; ++w) mm = fmaxf(mm, __ldcg(from + w * slot_floats));
-    const float ref = mm == -INFINITY ? 0.f : mm;
-    float x[kPer], s = 0.f;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) x[k] = 0.f;
-    for (int w = 0; w < parts; ++w) {
-      const float* pw = from + w * slot_floats;
-      const float f = ex2(__ldcg(pw) - ref);
-      s += f * __ldcg(pw + 1);
-#pragma unroll
-      for (int k = 0; k < kPer; k += 2) {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(pw + 2 + d0 + k));
-        x[k] += f * v.x;
-        x[k + 1] += f * v.y;
-      }
-    }
-    const int rr = rt * Q + r;
-    const int hq = h * a.G + rr / nq, j = rr % nq;
-    const float inv = s == 0.f ? 0.f : 1.f / s;
-    *reinterpret_cast<uint4*>(a.out.at(l, b, hq, j) + d0) =
-        make_uint4(bf16x2(x[0] * inv, x[1] * inv), bf16x2(x[2] * inv, x[3] * inv),
-                   bf16x2(x[4] * inv, x[5] * inv), bf16x2(x[6] * inv, x[7] * inv));
-    if (a.lse && d0 == 0)
-      a.lse[((static_cast<size_t>(l) * c.B + b) * c.H * a.G + hq) * a.n + j] =
-          (mm + __log2f(s)) * 0.6931471805599453f;
-  }
+  const int grid = min(a.num_sms * (kSmWarps / W), kMaxCtas);
+  kernel<<<grid, 32 * W, smem, s>>>(c, a, sp, make_div(c.bs));
+  return cudaGetLastError();
 }
 
 template <int D, int FMT>
 cudaError_t launch_few(const Cache& c, const AttendArgs& a, cudaStream_t s) {
-  const int R = a.G * a.n;
-  const int nt = R > 8 ? 2 : 1;
+  const int R = a.G * a.n, nt = R > 8 ? 2 : 1;
   Split sp;
   sp.row_tiles = (R + 8 * nt - 1) / (8 * nt);
-  const long long heads = static_cast<long long>(c.L) * c.B * c.H * sp.row_tiles;
-  // split sequences while the heads leave CTAs' places free
-  const long long places = static_cast<long long>(a.num_sms) * (nt == 1 ? 4 : 3);
-  const int tiles = static_cast<int>((static_cast<long long>(c.max_blocks) * c.bs + kTile - 1) / kTile);
-  long long per = heads < 2 * places ? 2 * places / heads : 1;
-  per = per < (tiles + kMinTiles - 1) / kMinTiles ? per : (tiles + kMinTiles - 1) / kMinTiles;
-  while (per > 1 && per * heads > kMaxParts) --per;
-  sp.per_unit = static_cast<int>(per < 1 ? 1 : per);
   sp.arrived = static_cast<int*>(a.workspace);
-  sp.part = reinterpret_cast<float*>(sp.arrived + kMaxParts);
-  const int grid = static_cast<int>(heads * sp.per_unit);
-  auto* kernel = nt == 1 ? attend_few_kernel<D, FMT, 1> : attend_few_kernel<D, FMT, 2>;
-  kernel<<<grid, kThreads, 0, s>>>(c, a, sp, make_div(c.bs));
-  return cudaGetLastError();
+  sp.part = reinterpret_cast<float*>(sp.arrived + kMaxCtas);
+  // One large CTA per SM where a head would otherwise be cut into more parts than
+  // are quickly joined; else small ones, whose beginnings and ends overlap.
+  const long long heads = static_cast<long long>(c.L) * c.B * c.H * sp.row_tiles;
+  const bool large = heads * 16 < static_cast<long long>(a.num_sms) * (kSmWarps / 4);
+  if (nt == 1)
+    return large ? launch_few<D, FMT, 1, 12>(c, a, sp, s) : launch_few<D, FMT, 1, 4>(c, a, sp, s);
+  return large ? launch_few<D, FMT, 2, 12>(c, a, sp, s) : launch_few<D, FMT, 2, 4>(c, a, sp, s);
 }
 
 }  // namespace
@@ -531,7 +692,8 @@ cudaError_t launch_attend(const Cache& c, int format, const AttendArgs& a, cudaS
 }  // namespace cache8
 
 size_t cache8_attend_workspace(int d) {
-  return cache8::kMaxParts * (sizeof(int) + static_cast<size_t>(cache8::kRowTile) * (d + 2) * 4);
+  using namespace cache8;
+  return kMaxCtas * (sizeof(int) + 2 * static_cast<size_t>(kRowTile) * (d + 2) * sizeof(float));
 }
 
 }  // namespace kvc
