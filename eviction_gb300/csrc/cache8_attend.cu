@@ -29,11 +29,12 @@
 // passes it by 2^8 (fp16 has the room), which turns the reduction over lanes into
 // one vote per 32 tokens.
 //
-// Work is the list of all heads' steps of 32 tokens, one after another; every CTA
-// takes an equal stretch of it, whatever the lengths are, and walks the heads that
-// it meets.  A head that lies in one stretch is finished there; the parts of one
-// that does not go to the workspace, and the last CTA of it to finish joins them in
-// order (the result does not depend on which one that is).
+// Work is the list of all heads' steps of 32 tokens, one after another.  Many heads:
+// small CTAs, three on an SM, take equal stretches of the list, whatever the lengths
+// are, and walk the heads that they meet.  Few heads: one large CTA per SM takes a
+// part of one head.  A head within one CTA is finished there; the parts of one that
+// is not go to the workspace, and the last CTA of it to finish joins them in order
+// (the result does not depend on which one that is).
 #include <atomic>
 
 #include "cache8.cuh"
@@ -48,6 +49,7 @@ constexpr int kStages = 2;
 constexpr int kSmWarps = 12;     // warps of an SM, by registers and shared memory
 constexpr int kMaxCtas = 512;    // CTAs of a call
 constexpr float kSlack = 8.f;    // log2 of how far a weight may pass 1
+constexpr int kMinRounds = 3;    // steps of a CTA's warps at least, before a head is cut
 
 // Division by the block size: floor(t / bs) = umulhi(t, mul) >> shift for
 // 0 <= t < 2^31 (bs > 1).
@@ -121,6 +123,15 @@ __device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
   }
 }
 
+// Values in the order of the second product's A operand: from four codes of each of
+// two tokens, pairs (token x, token y) of codes 0 and 1 (HIGH: 2 and 3).  (int8 codes
+// left biased, with the bias taken off the sums, saved a tenth of the instructions
+// and lost columns much smaller than their block's largest value.)
+template <int FMT, bool HIGH>
+__device__ __forceinline__ void value_pairs(uint32_t x, uint32_t y, uint32_t& even, uint32_t& odd) {
+  halves<FMT>(__byte_perm(x, y, HIGH ? 0x7362 : 0x5140), even, odd);
+}
+
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -148,27 +159,9 @@ constexpr int smem_bytes() {
   return ring > parts ? ring : parts;
 }
 
-// Inclusive scan over a CTA of W warps; every thread gets the total too.
-template <int W>
-__device__ __forceinline__ long long scan(long long v, long long* sums, long long* total) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += t;
-  }
-  if (lane == 31) sums[warp] = v;
-  __syncthreads();
-  long long before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    if (w < warp) before += sums[w];
-    all += sums[w];
-  }
-  __syncthreads();
-  *total = all;
-  return v + before;
-}
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+__device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 
 // Steps of one head of sequence b; 0 for one that has no queries or is refused.
 __device__ __forceinline__ int steps_of(const Cache& c, const AttendArgs& a, int b, bool* bad) {
@@ -210,62 +203,101 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
   extern __shared__ __align__(128) uint8_t smem[];
   auto s_o = reinterpret_cast<float(*)[Q][OS]>(smem);  // after a head's loop, the warps' parts
   __shared__ float s_m[W][Q], s_l[W][Q];
-  __shared__ long long s_scan[W];
-  __shared__ int s_seq, s_last;
-  __shared__ long long s_off;
+  __shared__ int s_last;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, q4 = lane % 4;
-  bool bad = false;
+  bool bad = false, unused = false;
 
-  // ---- this CTA's stretch [lo, hi) of all steps, and the head that it begins in ----
+  // ---- this CTA's work: steps [begin, ...) of a head, `left` steps in all ----
+  // (every warp computes it for itself; all counts are below 2^31, checked on the host)
   const int heads = c.H * sp.row_tiles;  // of one sequence and layer
-  long long layer_steps, at;
-  {
-    long long mine = 0;
-    for (int b = threadIdx.x; b < c.B; b += kThreads) mine += steps_of(c, a, b, &bad);
-    if (blockIdx.x != 0) bad = false;  // one report is enough
-    scan<W>(mine, s_scan, &layer_steps);
-    layer_steps *= heads;
+  int own_steps[2] = {0, 0};             // of the first 64 sequences, by lane
+  int all = 0, most = 0;
+  for (int b0 = 0; b0 < c.B; b0 += 32) {
+    const int n = b0 + lane < c.B ? steps_of(c, a, b0 + lane, &bad) : 0;
+    if (b0 == 0) own_steps[0] = n;
+    if (b0 == 32) own_steps[1] = n;
+    all += n;
+    most = max(most, n);
   }
-  const long long total = layer_steps * c.L;
-  const long long n_cta = min(static_cast<long long>(gridDim.x), (total + W - 1) / W);
-  if (blockIdx.x >= n_cta) {
-    if (bad) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
-    return;
-  }
-  auto first_of = [&](long long cta) { return total * cta / n_cta; };
-  const long long lo = first_of(blockIdx.x), hi = first_of(blockIdx.x + 1);
-  int l = static_cast<int>(lo / layer_steps);
-  {
-    const long long want = lo % layer_steps;
-    long long before = 0;  // of earlier chunks of sequences
-    for (int b0 = 0; b0 < c.B; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      bool unused = false;
-      const long long n = b < c.B ? static_cast<long long>(steps_of(c, a, b, &unused)) * heads : 0;
-      long long chunk;
-      const long long end = before + scan<W>(n, s_scan, &chunk);
-      if (n > 0 && want >= end - n && want < end) {
-        s_seq = b;
-        s_off = want - (end - n);
+  all = warp_sum(all);
+  if (blockIdx.x == 0 && bad) atomicOr(c.status, KVC_STATUS_BAD_INDEX);  // one report is enough
+  bad = false;
+  // the sum over sequences of f(steps)
+  auto steps_at = [&](int b0) {
+    return b0 == 0 ? own_steps[0] : b0 == 32 ? own_steps[1]
+           : b0 + lane < c.B ? steps_of(c, a, b0 + lane, &unused) : 0;
+  };
+  auto sum_over = [&](auto f) {
+    int v = 0;
+    for (int b0 = 0; b0 < c.B; b0 += 32) v += f(steps_at(b0));
+    return warp_sum(v);
+  };
+  // the sequence in which place `at` of the sum over sequences of heads * f(steps)
+  // lies, and the place within it
+  auto find = [&](int at, auto f, int* in) {
+    int before = 0;
+    for (int b0 = 0;; b0 += 32) {
+      const int n = heads * f(steps_at(b0));
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      const int chunk = __shfl_sync(0xffffffffu, incl, 31);
+      if (at < before + chunk || b0 + 32 >= c.B) {
+        const int place = __ffs(__ballot_sync(0xffffffffu, at < before + incl)) - 1;
+        *in = at - before - __shfl_sync(0xffffffffu, incl - n, place);
+        return b0 + place;
       }
       before += chunk;
-      if (want < before) break;
     }
+  };
+  const int n_cta = gridDim.x, total = all * heads * c.L;
+  if (total == 0) return;
+  int chunk = max(div_up(total, n_cta), kMinRounds * W);
+  int l, b, head, begin, left;
+  if constexpr (W == kSmWarps) {
+    // parts of at most `chunk` steps, so many that the grid has a CTA for each: with
+    // n_cta / (heads in all) parts of the longest head that is so; the even share
+    // and one in between are tried first
+    const int seqs = sum_over([](int n) { return n > 0; }) * heads * c.L;
+    const int safe = max(div_up(__reduce_max_sync(0xffffffffu, most), max(n_cta / seqs, 1)), chunk);
+    int parts_all = 0;  // of a layer
+    for (int i = 0; i < 3; ++i) {
+      parts_all = heads * sum_over([&](int n) { return div_up(n, chunk); });
+      if (parts_all * c.L <= n_cta) break;
+      chunk = i == 0 ? (chunk + safe + 1) / 2 : safe;
+    }
+    if (static_cast<int>(blockIdx.x) >= parts_all * c.L) return;
+    l = blockIdx.x / parts_all;
+    int in;
+    b = find(blockIdx.x % parts_all, [&](int n) { return div_up(n, chunk); }, &in);
+    const int steps = steps_of(c, a, b, &unused), parts = div_up(steps, chunk);
+    head = in / parts;
+    begin = in % parts * chunk;
+    left = min(chunk, steps - begin);
+  } else {
+    const int lo = blockIdx.x * chunk;
+    if (static_cast<long long>(blockIdx.x) * chunk >= total) return;
+    left = min(chunk, total - lo);
+    l = lo / (all * heads);
+    int in;
+    b = find(lo % (all * heads), [](int n) { return n; }, &in);
+    const int steps = steps_of(c, a, b, &unused);
+    head = in / steps;
+    begin = in % steps;
   }
-  __syncthreads();
-  int b = s_seq;
-  at = lo;
-  bool unused = false;
   int steps = steps_of(c, a, b, &unused);  // of a head of this sequence
-  int head = static_cast<int>(s_off / steps), begin = static_cast<int>(s_off % steps);
 
   uint8_t* ring = smem + warp * (kStages * St::kBytes);
   const uint32_t ring_addr = smem_u32(ring);
 
+  int at = blockIdx.x * chunk;  // place in the list
   for (;;) {
     const int h = head / sp.row_tiles, rt = head % sp.row_tiles;
-    const int end = static_cast<int>(min(static_cast<long long>(steps), begin + (hi - at)));
+    const int end = min(steps, begin + left);
     const int len = c.seq_len[b];
     const int nq = a.n_q ? a.n_q[b] : a.n;
     const int rows = min(a.G * nq - rt * Q, Q);  // of this tile: r = rt * Q + 0..rows-1
@@ -414,12 +446,11 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
       const float* k_scales = reinterpret_cast<const float*>(st + St::kKeyScales);
       const float* v_scales = reinterpret_cast<const float*>(st + St::kValueScales);
       float back[4];  // 2^-e, 0 for an absent token
-      const bool whole = t0 + kTile <= len - nq + 1;  // every query sees the step
-      bool up = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float ks = k_scales[g + 8 * i], vs = v_scales[g + 8 * i];
         const int e = static_cast<int>(__float_as_uint(vs) >> 23) - 127;
+        // (an absent token has zeros for key and scales: its logit becomes -inf)
         const float ef = vs == 0.f ? -INFINITY : static_cast<float>(e);
         back[i] = vs == 0.f ? 0.f : exp2_int(-e);
 #pragma unroll
@@ -427,12 +458,26 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float& x = z[i / 2][nt][(i % 2) * 2 + j];
-            // (an absent token's product is 0: its key and scale are)
             x = fmaf(x, ks * qscale[nt][j], ef);
-            if (vs == 0.f || (!whole && t0 + g + 8 * i > limit[nt][j])) x = -INFINITY;
-            up = up || x > m[nt][j] + kSlack;
           }
       }
+      if (t0 + kTile > len - nq + 1) {  // not every query sees all of the step
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (t0 + g + 8 * i > limit[nt][j]) z[i / 2][nt][(i % 2) * 2 + j] = -INFINITY;
+      }
+      bool up = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float x = fmaxf(fmaxf(z[0][nt][j], z[0][nt][2 + j]), fmaxf(z[1][nt][j], z[1][nt][2 + j]));
+          up = up || x > m[nt][j] + kSlack;
+        }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -485,17 +530,18 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
           }
         }
 #pragma unroll
-        for (int j = 0; j < MT / 2; ++j)
+        for (int j = 0; j < MT / 2; ++j) {
+          uint32_t a0, a1, a2, a3;
+          value_pairs<FMT, false>(vr[0][j], vr[1][j], a0, a1);
+          value_pairs<FMT, false>(vr[2][j], vr[3][j], a2, a3);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t sel = i == 0 ? 0x5140 : 0x7362;
-            uint32_t a0, a1, a2, a3;
-            halves<FMT>(__byte_perm(vr[0][j], vr[1][j], sel), a0, a1);
-            halves<FMT>(__byte_perm(vr[2][j], vr[3][j], sel), a2, a3);
+          for (int nt = 0; nt < NT; ++nt) mma(o[nt][2 * j], a0, a1, a2, a3, p[kt][nt][0], p[kt][nt][1]);
+          value_pairs<FMT, true>(vr[0][j], vr[1][j], a0, a1);
+          value_pairs<FMT, true>(vr[2][j], vr[3][j], a2, a3);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma(o[nt][2 * j + i], a0, a1, a2, a3, p[kt][nt][0], p[kt][nt][1]);
-          }
+          for (int nt = 0; nt < NT; ++nt)
+            mma(o[nt][2 * j + 1], a0, a1, a2, a3, p[kt][nt][0], p[kt][nt][1]);
+        }
       }
       __syncwarp();  // every lane has read the stage before it is filled again
     }
@@ -556,23 +602,28 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
 
     // ---- join the parts of a head: the last CTA of it to arrive ----
     if (!whole_head && rows > 0) {
-      // the CTAs that have a stretch of this head: the one with its first step to the
-      // one with its last
-      const long long head_lo = at - begin, head_hi = head_lo + steps;
-      auto owner = [&](long long step_at) {
-        long long k = step_at * n_cta / total;  // first_of(k) <= step_at up to rounding
-        while (first_of(k + 1) <= step_at) ++k;
-        while (first_of(k) > step_at) --k;
-        return static_cast<int>(k);
-      };
-      const int c0 = owner(head_lo), c1 = owner(head_hi - 1), n_part = c1 - c0 + 1;
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) s_last = atomicAdd(&sp.arrived[c0], 1) == n_part - 1;
+      // the CTAs c0 .. c0 + n_part - 1 have this head
+      int c0, n_part;
+      if constexpr (W == kSmWarps) {
+        c0 = blockIdx.x - begin / chunk;
+        n_part = div_up(steps, chunk);
+      } else {
+        const int head_lo = at - begin;
+        c0 = head_lo / chunk;
+        n_part = (head_lo + steps - 1) / chunk - c0 + 1;
+      }
+      __syncthreads();  // the part is written, by all threads
+      if (threadIdx.x == 0) {
+        int seen;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                     : "=r"(seen)
+                     : "l"(sp.arrived + c0)
+                     : "memory");
+        s_last = seen == n_part - 1;
+        if (s_last) sp.arrived[c0] = 0;  // ready for the next call
+      }
       __syncthreads();
       if (s_last) {
-        __threadfence();
-        if (threadIdx.x == 0) sp.arrived[c0] = 0;  // ready for the next call
         // the first CTA's part of a head that begins in it, then the others'
         auto part_of = [&](int i) {
           return sp.part + (2 * static_cast<size_t>(c0 + i) + (i == 0 ? 1 : 0)) * kSlot;
@@ -584,7 +635,7 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
 #pragma unroll
           for (int k = 0; k < kPer; ++k) x[k] = 0.f;
           // a few parts at a time, all their loads in flight together
-          constexpr int kBatch = 4;
+          constexpr int kBatch = 6;
           for (int w0 = 0; w0 < n_part; w0 += kBatch) {
             float2 ml[kBatch], v[kBatch][kPer / 2];
             float top = mm;
@@ -626,8 +677,9 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
     }
 
     // ---- the next head ----
+    left -= end - begin;
+    if (W == kSmWarps || left == 0) break;
     at += end - begin;
-    if (at >= hi) break;
     begin = 0;
     if (++head == heads) {
       head = 0;

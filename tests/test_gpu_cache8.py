@@ -222,6 +222,20 @@ def test_attend_long(fmt, H, G, bs, lens, n):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("B,H,longest,n", [(100, 2, 300, 1), (70, 1, 900, 2), (33, 1, 60, 20), (3, 1, 6000, 1)])
+def test_attend_many_and_uneven_sequences(fmt, B, H, longest, n):
+    """Heads cut anywhere: lengths from nothing to the longest, some sequences without queries."""
+    p = Pair(1, B, H, 64, 16, -(-longest // 16), fmt, window=32, seed=B)
+    lens = p.rng.integers(0, longest + 1, B) * (p.rng.random(B) < 0.8)
+    lens[0], lens[-1] = longest, 1
+    p.fill(lens.tolist())
+    p.attend(n)
+    n_q = p.rng.integers(0, n + 1, B)
+    n_q[:3] = 0
+    p.attend(n, n_q=n_q)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("n", [1, 40])
 def test_attend_scales_far_apart(fmt, n):
     """Blocks whose value scales lie 2^60 apart, and sharp softmaxes."""
