@@ -234,11 +234,11 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
     return warp_sum(v);
   };
   // the sequence in which place `at` of the sum over sequences of heads * f(steps)
-  // lies, and the place within it
-  auto find = [&](int at, auto f, int* in) {
+  // lies, the place within it and the sequence's steps
+  auto find = [&](int at, auto f, int* in, int* steps) {
     int before = 0;
     for (int b0 = 0;; b0 += 32) {
-      const int n = heads * f(steps_at(b0));
+      const int own = steps_at(b0), n = heads * f(own);
       int incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
       if (at < before + chunk || b0 + 32 >= c.B) {
         const int place = __ffs(__ballot_sync(0xffffffffu, at < before + incl)) - 1;
         *in = at - before - __shfl_sync(0xffffffffu, incl - n, place);
+        *steps = __shfl_sync(0xffffffffu, own, place);
         return b0 + place;
       }
       before += chunk;
@@ -257,13 +258,15 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
   const int n_cta = gridDim.x, total = all * heads * c.L;
   if (total == 0) return;
   int chunk = max(div_up(total, n_cta), kMinRounds * W);
-  int l, b, head, begin, left;
+  int l, b, head, begin, left, steps;  // (steps of a head of sequence b)
   if constexpr (W == kSmWarps) {
     // parts of at most `chunk` steps, so many that the grid has a CTA for each: with
-    // n_cta / (heads in all) parts of the longest head that is so; the even share
-    // and one in between are tried first
+    // n_cta / (heads in all) parts of the longest head that is so; where lengths
+    // differ, the even share and one in between may do and are tried first
+    most = __reduce_max_sync(0xffffffffu, most);
     const int seqs = sum_over([](int n) { return n > 0; }) * heads * c.L;
-    const int safe = max(div_up(__reduce_max_sync(0xffffffffu, most), max(n_cta / seqs, 1)), chunk);
+    const int safe = max(div_up(most, max(n_cta / seqs, 1)), kMinRounds * W);
+    if (seqs * most == total) chunk = safe;
     int parts_all = 0;  // of a layer
     for (int i = 0; i < 3; ++i) {
       parts_all = heads * sum_over([&](int n) { return div_up(n, chunk); });
@@ -273,8 +276,8 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
     if (static_cast<int>(blockIdx.x) >= parts_all * c.L) return;
     l = blockIdx.x / parts_all;
     int in;
-    b = find(blockIdx.x % parts_all, [&](int n) { return div_up(n, chunk); }, &in);
-    const int steps = steps_of(c, a, b, &unused), parts = div_up(steps, chunk);
+    b = find(blockIdx.x % parts_all, [&](int n) { return div_up(n, chunk); }, &in, &steps);
+    const int parts = div_up(steps, chunk);
     head = in / parts;
     begin = in % parts * chunk;
     left = min(chunk, steps - begin);
@@ -284,13 +287,10 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
     left = min(chunk, total - lo);
     l = lo / (all * heads);
     int in;
-    b = find(lo % (all * heads), [](int n) { return n; }, &in);
-    const int steps = steps_of(c, a, b, &unused);
+    b = find(lo % (all * heads), [](int n) { return n; }, &in, &steps);
     head = in / steps;
     begin = in % steps;
   }
-  int steps = steps_of(c, a, b, &unused);  // of a head of this sequence
-
   uint8_t* ring = smem + warp * (kStages * St::kBytes);
   const uint32_t ring_addr = smem_u32(ring);
 
@@ -340,30 +340,38 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
       copies_commit();
     };
 
+    // ---- queries: row g of each 8-row tile, in the order of the key reads ----
+    // row r is head r / nq of the group, query r % nq; the loads start before the first
+    // step's, which wait for the table
     int step = rows > 0 ? begin + warp : end;
     int blk = block_of(step);
     int next = block_of(step + W);
+    uint4 raw[NT][KV][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = rt * Q + nt * 8 + g;
+      const bool there = nt * 8 + g < rows;
+      const uint16_t* qp = a.q.at(l, b, h * a.G + (there ? r / nq : 0), there ? r % nq : 0);
+#pragma unroll
+      for (int k = 0; k < KV; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          raw[nt][k][i] = there ? __ldg(reinterpret_cast<const uint4*>(qp + (k * 4 + q4) * 16 + i * 8))
+                                : make_uint4(0, 0, 0, 0);
+    }
     fetch(step, blk, 0);
     int stage = 0;
-
-    // ---- queries: row g of each 8-row tile, in the order of the key reads ----
-    // row r is head r / nq of the group, query r % nq
     uint32_t qf[NT][KV * 4][2];
     float qscale[NT][2];  // of rows 2 q4, 2 q4 + 1: scale log2(e) 2^e
     int limit[NT][2];     // last token that they see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = rt * Q + nt * 8 + g;
-      const bool there = nt * 8 + g < rows;
-      uint4 w[KV][2];
+      const auto& w = raw[nt];
       float mx = 0.f;
-      const uint16_t* qp = a.q.at(l, b, h * a.G + (there ? r / nq : 0), there ? r % nq : 0);
 #pragma unroll
       for (int k = 0; k < KV; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          w[k][i] = there ? __ldg(reinterpret_cast<const uint4*>(qp + (k * 4 + q4) * 16 + i * 8))
-                          : make_uint4(0, 0, 0, 0);
           const uint32_t x[4] = {w[k][i].x, w[k][i].y, w[k][i].z, w[k][i].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j)
