@@ -35,9 +35,7 @@
 // part of one head.  A head within one CTA is finished there; the parts of one that
 // is not go to the workspace, and the last CTA of it to finish joins them in order
 // (the result does not depend on which one that is).
-#include <atomic>
-
-#include "cache8.cuh"
+#include "cache8_attend.cuh"
 
 namespace kvc {
 namespace cache8 {
@@ -47,25 +45,9 @@ constexpr int kTile = 32;        // tokens of one step of a warp
 constexpr int kRowTile = 16;     // query rows of a stretch at most
 constexpr int kStages = 2;
 constexpr int kSmWarps = 12;     // warps of an SM, by registers and shared memory
-constexpr int kMaxCtas = 512;    // CTAs of a call
+constexpr int kMaxCtas = kCounters;  // CTAs of a call
 constexpr float kSlack = 8.f;    // log2 of how far a weight may pass 1
 constexpr int kMinRounds = 3;    // steps of a CTA's warps at least, before a head is cut
-
-// Division by the block size: floor(t / bs) = umulhi(t, mul) >> shift for
-// 0 <= t < 2^31 (bs > 1).
-struct Div {
-  uint32_t mul;
-  int shift, bs;
-  __device__ __forceinline__ int div(int t) const {
-    return mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(t), mul) >> shift) : t;
-  }
-};
-Div make_div(int bs) {
-  if (bs == 1) return {0, 0, 1};
-  int s = 0;
-  while ((1 << s) < bs) ++s;  // 2^(s-1) < bs <= 2^s
-  return {static_cast<uint32_t>((1ull << (31 + s)) / bs + 1), s - 1, bs};
-}
 
 struct Split {
   int row_tiles;  // of a head
@@ -102,27 +84,6 @@ struct Stage {
   }
 };
 
-// Codes as signed integers, biased to 0..255, behind the exponent of 1024: the
-// fp16 number 1024 + u, from which 1152 leaves the value.
-__device__ __forceinline__ uint32_t unbias(uint32_t h) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
-  return r;
-}
-
-// Four codes to two half2: (0, 1), (2, 3).
-template <int FMT>
-__device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (FMT == KVC_CACHE8_E4M3) {
-    lo = e4m3_to_half2(w);
-    hi = e4m3_to_half2(w >> 16);
-  } else {
-    w ^= 0x80808080u;
-    lo = unbias(__byte_perm(w, 0x64646464u, 0x4140));
-    hi = unbias(__byte_perm(w, 0x64646464u, 0x4342));
-  }
-}
-
 // Values in the order of the second product's A operand: from four codes of each of
 // two tokens, pairs (token x, token y) of codes 0 and 1 (HIGH: 2 and 3).  (int8 codes
 // left biased, with the bias taken off the sums, saved a tenth of the instructions
@@ -147,12 +108,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t half2_of(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
-
 template <int D, int NT, int W>
 constexpr int smem_bytes() {
   const int ring = W * kStages * Stage<D>::kBytes, parts = W * 8 * NT * (D + 4) * 4;
@@ -160,8 +115,6 @@ constexpr int smem_bytes() {
 }
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
-
-__device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 
 // Steps of one head of sequence b; 0 for one that has no queries or is refused.
 __device__ __forceinline__ int steps_of(const Cache& c, const AttendArgs& a, int b, bool* bad) {
@@ -173,21 +126,6 @@ __device__ __forceinline__ int steps_of(const Cache& c, const AttendArgs& a, int
     return 0;
   }
   return nq == 0 ? 0 : max((len + kTile - 1) / kTile, 1);
-}
-
-// Write kPer values of a row and, with the first ones, its lse.
-constexpr int kPer = 8;
-__device__ __forceinline__ void write_row(const Cache& c, const AttendArgs& a, int l, int b, int h,
-                                          int r, int nq, int d0, const float (&x)[kPer], float m,
-                                          float sum) {
-  const int hq = h * a.G + r / nq, j = r % nq;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  *reinterpret_cast<uint4*>(a.out.at(l, b, hq, j) + d0) =
-      make_uint4(bf16x2(x[0] * inv, x[1] * inv), bf16x2(x[2] * inv, x[3] * inv),
-                 bf16x2(x[4] * inv, x[5] * inv), bf16x2(x[6] * inv, x[7] * inv));
-  if (a.lse && d0 == 0)
-    a.lse[((static_cast<size_t>(l) * c.B + b) * c.H * a.G + hq) * a.n + j] =
-        (m + __log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int D, int FMT, int NT, int W>
@@ -708,16 +646,9 @@ template <int D, int FMT, int NT, int W>
 cudaError_t launch_few(const Cache& c, const AttendArgs& a, const Split& sp, cudaStream_t s) {
   constexpr int smem = smem_bytes<D, NT, W>();
   auto* kernel = attend_few_kernel<D, FMT, NT, W>;
-  // beyond 48 KB a kernel has to be told so, once per device
   static std::atomic<uint64_t> told{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_smem(kernel, smem, told);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(told.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) told.fetch_or(1ull << dev, std::memory_order_relaxed);
-  }
   const int grid = min(a.num_sms * (kSmWarps / W), kMaxCtas);
   kernel<<<grid, 32 * W, smem, s>>>(c, a, sp, make_div(c.bs));
   return cudaGetLastError();
@@ -729,7 +660,7 @@ cudaError_t launch_few(const Cache& c, const AttendArgs& a, cudaStream_t s) {
   Split sp;
   sp.row_tiles = (R + 8 * nt - 1) / (8 * nt);
   sp.arrived = static_cast<int*>(a.workspace);
-  sp.part = reinterpret_cast<float*>(sp.arrived + kMaxCtas);
+  sp.part = reinterpret_cast<float*>(sp.arrived + kCounters);
   // One large CTA per SM where a head would otherwise be cut into more parts than
   // are quickly joined; else small ones, whose beginnings and ends overlap.
   const long long heads = static_cast<long long>(c.L) * c.B * c.H * sp.row_tiles;
@@ -741,7 +672,11 @@ cudaError_t launch_few(const Cache& c, const AttendArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+// Above this many query rows a head's work is bound by arithmetic: the other kernel.
+constexpr int kFewRows = 32;
+
 cudaError_t launch_attend(const Cache& c, int format, const AttendArgs& a, cudaStream_t s) {
+  if (a.G * a.n > kFewRows) return launch_attend_many(c, format, a, s);
   if (c.d == 64)
     return format == KVC_CACHE8_E4M3 ? launch_few<64, KVC_CACHE8_E4M3>(c, a, s)
                                      : launch_few<64, KVC_CACHE8_INT8>(c, a, s);
@@ -753,7 +688,9 @@ cudaError_t launch_attend(const Cache& c, int format, const AttendArgs& a, cudaS
 
 size_t cache8_attend_workspace(int d) {
   using namespace cache8;
-  return kMaxCtas * (sizeof(int) + 2 * static_cast<size_t>(kRowTile) * (d + 2) * sizeof(float));
+  const size_t few = kMaxCtas * 2 * static_cast<size_t>(kRowTile) * (d + 2) * sizeof(float);
+  const size_t many = attend_many_parts_bytes(d);
+  return kCounters * sizeof(int) + (few > many ? few : many);
 }
 
 }  // namespace kvc

@@ -1,0 +1,680 @@
+// cache8_attend_many.cu -- attention over the 8-bit paged cache for many queries
+// (a prompt in pieces, the window of an event): 128 query rows a CTA on the
+// 5th-generation tensor cores (tcgen05 + TMEM).
+//
+//   out_r = sum_t w_rt v_t / sum_t w_rt,  w_rt = exp(scale q_r . k_t)
+//
+// Row r of a KV head is query r % nq of its group's head r / nq.  Per 128 tokens:
+//   converters (4 warps)  codes from global memory to fp16 tiles in shared memory,
+//                         in the swizzled layout of the MMA operands.  Keys carry
+//                         their block's scale relative to the tile's largest (a
+//                         power of two: exact, down to fp16's last step); values are
+//                         the codes themselves;
+//   MMA (1 thread)        S = Q K^T (128 x 128, in TMEM), then O += P V with P read
+//                         from TMEM, where it takes the place of S;
+//   softmax (4 warps)     one thread a row: p = 2^(x - m), x = z + e with 2^e the
+//                         value scale of the token's block (so that P needs no scale
+//                         and stays within fp16 whatever the blocks' scales are), the
+//                         sum of 2^-e p in fp32, P to TMEM as fp16.
+// The reference m of a row lies below its maximum: weights may reach 2^15 (fp16 has
+// the room) before m moves, and a new m leaves them at 2^8.  The maximum itself comes
+// with the TMEM load (tcgen05.ld.red) where the whole tile is seen and its blocks'
+// value scales are within 2^8 of each other: scores' maximum plus the largest e is
+// then at most 2^8 too high.  Else it is taken over the masked logits.
+//
+// The arithmetic bounds this: 4 R d operations a token, 1024 cycles of the tensor
+// pipe per 128 x 128 tile of d = 128.  S and P share columns, so that one CTA's
+// softmax and MMAs take turns; two CTAs on an SM (half of TMEM and shared memory
+// each) fill each other's gaps, and a CTA's beginning and end as well.
+//
+// Heads and row tiles that do not fill the GPU have their tokens cut into parts; the
+// last CTA of a row tile to finish joins them in order.  Every wait is bounded.
+#include "cache8_attend.cuh"
+
+namespace kvc {
+namespace cache8 {
+namespace {
+
+constexpr int kRows = 128, kTokens = 128;
+constexpr int kSoftmaxWarps = 4, kConvertWarps = 4, kMmaWarp = 8;
+constexpr int kThreads = 32 * 9;
+constexpr int kTmemCols = 256;    // S / P: 128, O: up to 128
+constexpr int kMaxParts = 320;    // CTAs of a call that cuts heads
+constexpr float kRoom = 15.f, kStart = 8.f;  // log2 of the weights' limit and of a new m's
+constexpr float kSpread = 8.f;
+
+struct Parts {
+  int per_tile;   // CTAs of a row tile
+  int row_tiles;  // of a head
+  float* part;    // [kMaxParts][D + 2][kRows]: reference, sum, values
+  int* arrived;   // [kCounters] zero between calls
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kTile = kTokens * D * 2;
+  static constexpr int kV = 0, kK = kTile, kQ = 2 * kTile, kMeta = 3 * kTile;
+  static constexpr int kE = kMeta, kBack = kE + 2 * kTokens * 4, kInfo = kBack + 2 * kTokens * 4,
+                       kRed = kInfo + 2 * 16, kBars = kRed + 2 * 4 * 16, kMisc = kBars + 16 * 8;
+  static constexpr int kBytes = kMisc + 32 + 1024;  // and 1024 for the alignment
+};
+
+// What a tile's converters tell the softmax warps.
+struct TileInfo {
+  float k_ref;    // the scale that the tile's keys are relative to
+  float e_max;    // largest log2 value scale
+  int plain;      // no token is absent and the value scales are within 2^kSpread
+  int uniform;    // and all the same
+};
+
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Instruction descriptor, kind::f16: A = B = fp16, D = fp32; B with N contiguous
+// (bit 16) where mn_major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool mn_major) {
+  return (1u << 4) | (mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// B operand with N contiguous: rows (K) of 128 bytes = 64 values of N, swizzled in
+// groups of 8 rows 1024 bytes apart; the next 64 values of N `block` bytes on.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr, uint32_t block) {
+  uint64_t desc = sw128_desc(addr);
+  desc &= ~(static_cast<uint64_t>(0x3FFF) << 16);
+  return desc | static_cast<uint64_t>(block >> 4) << 16;
+}
+
+// D += A B with A in tensor memory.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// All lanes wait converged and agree on the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          uint32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
+
+// All lanes' shared-memory writes, then one arrival for the warp.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// 2^e as both halves of a pair of fp16, 0 below its last step (e <= 0).
+__device__ __forceinline__ uint32_t exp2_half2(int e) {
+  const uint32_t h = e >= -14 ? (15 + e) << 10 : e >= -24 ? 1u << (24 + e) : 0u;
+  return h * 0x00010001u;
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads, 2)
+    attend_many_kernel(Cache c, AttendArgs a, Parts sp, Div by_bs) {
+#if defined(__CUDA_ARCH__) && (__CUDA_ARCH__ >= 1000)
+  using Sm = Smem<D>;
+  constexpr int DB = D / 64;  // 64-value blocks (128 bytes) of a row
+  constexpr int kBlock = kTokens * 128;  // bytes of one block of all rows
+  constexpr uint32_t kOutCol = 128;      // O's first TMEM column
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* s_e = reinterpret_cast<float*>(smem + Sm::kE);        // [2][kTokens]
+  float* s_back = reinterpret_cast<float*>(smem + Sm::kBack);  // [2][kTokens] 2^-e
+  TileInfo* s_info = reinterpret_cast<TileInfo*>(smem + Sm::kInfo);
+  int4* s_red = reinterpret_cast<int4*>(smem + Sm::kRed);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kBars);
+  uint64_t *q_full = bars, *k_full = bars + 1, *k_empty = bars + 2, *v_full = bars + 3,
+           *v_empty = bars + 4, *s_full = bars + 5, *p_full = bars + 6, *o_full = bars + 7,
+           *m_full = bars + 8, *m_empty = bars + 10, *r_full = bars + 12, *done = bars + 13;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sm::kMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + Sm::kMisc + 4);
+  int* s_last = reinterpret_cast<int*>(smem + Sm::kMisc + 8);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  // ---- this CTA's row tile and tokens ----
+  const int part = blockIdx.x % sp.per_tile;
+  const int ur = blockIdx.x / sp.per_tile;
+  const int rt = ur % sp.row_tiles;
+  const int u = ur / sp.row_tiles;
+  const int h = u % c.H, b = (u / c.H) % c.B, l = u / (c.H * c.B);
+  bool bad = false;
+  const int len = length_of(c, b, &bad);
+  const int nq = a.n_q ? a.n_q[b] : a.n;
+  if (bad || nq < 0 || nq > a.n) {
+    if (threadIdx.x == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
+    return;
+  }
+  const int rows = min(a.G * nq - rt * kRows, kRows);
+  if (rows <= 0) return;
+  // the last token that one of the rows sees
+  const int r0 = rt * kRows, r1 = r0 + rows - 1;
+  const int last_q = r0 / nq == r1 / nq ? r1 % nq : nq - 1;
+  const int kv_end = max(len - nq + last_q + 1, 0);
+  const int all_tiles = div_up(kv_end, kTokens);
+  const int per = max(div_up(all_tiles, sp.per_tile), 2);
+  const int parts = max(div_up(all_tiles, per), 1);
+  if (part >= parts) return;
+  const int tile0 = part * per, n_tiles = min(per, all_tiles - tile0);
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, kSoftmaxWarps);
+    mbar_init(k_full, kConvertWarps);
+    mbar_init(k_empty, 1);
+    mbar_init(v_full, kConvertWarps);
+    mbar_init(v_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, kSoftmaxWarps);
+    mbar_init(o_full, 1);
+    mbar_init(r_full, kConvertWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m_full[i], kConvertWarps);
+      mbar_init(&m_empty[i], kSoftmaxWarps);
+    }
+    mbar_init(done, 1);
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < kSoftmaxWarps) {
+    // ------------------------------------------------------------ softmax
+    const int row = threadIdx.x, r = r0 + row;
+    const bool there = row < rows;
+    const int hq = h * a.G + (there ? r / nq : 0), j = there ? r % nq : 0;
+    const uint32_t my_tmem = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    // the query row as fp16, its largest magnitude scaled to [1, 2)
+    float qf;
+    {
+      const uint4* q = reinterpret_cast<const uint4*>(a.q.at(l, b, hq, j));
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = there ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
+      }
+      const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      const float down = exp2_int(-e);
+      qf = a.scale_log2 * exp2_int(e);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = there ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(smem + Sm::kQ + (i / 8) * kBlock + row * 128 +
+                                  (((i % 8) ^ (row % 8)) << 4)) =
+            make_uint4(half2_of(bf16_lo(v.x) * down, bf16_hi(v.x) * down),
+                       half2_of(bf16_lo(v.y) * down, bf16_hi(v.y) * down),
+                       half2_of(bf16_lo(v.z) * down, bf16_hi(v.z) * down),
+                       half2_of(bf16_lo(v.w) * down, bf16_hi(v.w) * down));
+      }
+      fence_async_shared();
+      warp_arrive(q_full);
+    }
+    const int limit = len - nq + j;     // last token that this row sees
+    float m = -INFINITY, sum = 0.f;     // reference and sum of 2^-e p
+    bool ok = true;
+    for (int i = 0; i < n_tiles; ++i) {
+      const int t0 = (tile0 + i) * kTokens, st = i & 1;
+      const uint32_t parity = (i >> 1) & 1;
+      if (!warp_wait(&m_full[st], parity, abort, c.status) ||
+          !warp_wait(s_full, i & 1, abort, c.status)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const TileInfo info = s_info[st];
+      const float* e_col = s_e + st * kTokens;
+      const float* back_col = s_back + st * kTokens;
+      const float f = qf * info.k_ref;
+      const bool whole = info.plain && t0 + kTokens <= len - nq + 1;  // the same for all rows
+      // ---- the maximum, or a bound of it ----
+      float top = -INFINITY;
+      if (whole) {
+#pragma unroll
+        for (int k = 0; k < kTokens / 32; ++k) {
+          uint32_t v[32];
+          float mx;
+          tmem_ld32_max(my_tmem + k * 32, v, mx);
+          tmem_ld_wait();
+          top = fmaxf(top, mx);
+        }
+        top = fmaf(top, f, info.e_max);
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < kTokens / 32; ++k) {
+          uint32_t v[32];
+          tmem_ld32(my_tmem + k * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const float z = fmaf(__uint_as_float(v[x]), f, e_col[k * 32 + x]);
+            if (t0 + k * 32 + x <= limit) top = fmaxf(top, z);
+          }
+        }
+      }
+      // ---- a new reference: what is there is scaled to it ----
+      const bool raise = top > m + kRoom;
+      if (__any_sync(0xffffffffu, raise)) {
+        const float next = raise ? top - kStart : m;
+        const float scale = raise ? ex2(m - next) : 1.f;
+        m = next;
+        sum *= scale;
+        if (i > 0) {
+          if (!warp_wait(o_full, (i - 1) & 1, abort, c.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t v[32];
+            tmem_ld32(my_tmem + kOutCol + k * 32, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * scale);
+            tmem_st32(my_tmem + kOutCol + k * 32, v);
+          }
+          tmem_st_wait();
+        }
+      }
+      // ---- weights: S's columns become P's ----
+      const float ref = m == -INFINITY ? 0.f : m;
+      if (whole && info.uniform) {
+        const float2 ff = make_float2(f, f), off = make_float2(info.e_max - ref, info.e_max - ref);
+        float2 part_sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kTokens / 32; ++k) {
+          uint32_t v[32], p[16];
+          tmem_ld32(my_tmem + k * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float2 z = fma2(make_float2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])),
+                            ff, off);
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+            part_sum = add2(part_sum, z);
+            p[x] = half2_of(z.x, z.y);
+          }
+          tmem_st16(my_tmem + k * 16, p);
+        }
+        sum = fmaf(part_sum.x + part_sum.y, back_col[0], sum);
+      } else {
+        const float2 ff = make_float2(f, f), off = make_float2(-ref, -ref);
+        float2 part_sum = make_float2(0.f, 0.f);
+        const int seen = whole ? kTokens : limit - t0 + 1;  // columns that this row sees
+#pragma unroll 1
+        for (int k = 0; k < kTokens / 32; ++k) {
+          uint32_t v[32], p[16];
+          tmem_ld32(my_tmem + k * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 16; x += 2) {
+            const float4 e4 = *reinterpret_cast<const float4*>(e_col + k * 32 + 2 * x);
+            const float4 b4 = *reinterpret_cast<const float4*>(back_col + k * 32 + 2 * x);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int at = 2 * (x + y);
+              float2 z = fma2(make_float2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), ff,
+                              y ? make_float2(e4.z, e4.w) : make_float2(e4.x, e4.y));
+              z = add2(z, off);
+              z.x = k * 32 + at < seen ? ex2(z.x) : 0.f;
+              z.y = k * 32 + at + 1 < seen ? ex2(z.y) : 0.f;
+              part_sum = fma2(z, y ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y), part_sum);
+              p[x + y] = half2_of(z.x, z.y);
+            }
+          }
+          tmem_st16(my_tmem + k * 16, p);
+        }
+        sum += part_sum.x + part_sum.y;
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(p_full);
+      if (lane == 0) mbar_arrive(&m_empty[st]);
+    }
+    // ---- the result ----
+    if (ok && n_tiles > 0) ok = warp_wait(o_full, (n_tiles - 1) & 1, abort, c.status);
+    if (ok) {
+      tc_fence_after();
+      float* slot = sp.part + static_cast<size_t>(blockIdx.x) * ((D + 2) * kRows) + row;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t v[32];
+        if (n_tiles > 0) {
+          tmem_ld32(my_tmem + kOutCol + k * 32, v);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) v[x] = 0;
+        }
+        if (there && parts == 1) {
+          uint4* out = reinterpret_cast<uint4*>(a.out.at(l, b, hq, j) + k * 32);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float y[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) y[z] = __uint_as_float(v[8 * x + z]) * inv;
+            out[x] = make_uint4(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]), bf16x2(y[4], y[5]),
+                                bf16x2(y[6], y[7]));
+          }
+        } else if (there) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) slot[(2 + k * 32 + x) * kRows] = __uint_as_float(v[x]);
+        }
+        __syncwarp();
+      }
+      if (there && parts == 1 && a.lse)
+        a.lse[((static_cast<size_t>(l) * c.B + b) * c.H * a.G + hq) * a.n + j] =
+            (m + __log2f(sum)) * 0.6931471805599453f;
+      if (there && parts > 1) {
+        slot[0] = m;
+        slot[kRows] = sum;
+      }
+    }
+  } else if (warp < kSoftmaxWarps + kConvertWarps) {
+    // ------------------------------------------------------------ converters
+    // This lane: rows (tokens) row_in + 32 i, 16-byte chunks q4 + 4 j of them.
+    const int cw = warp - kSoftmaxWarps, q4 = lane % 4;
+    const int row_in = cw * 8 + lane / 4;
+    const uint8_t* kp = c.pool[0] + block_row(c, l, 0, h) * D;
+    const uint8_t* vp = c.pool[1] + block_row(c, l, 0, h) * D;
+    const float* ksp = c.scale[0] + scale_at(c, l, 0, h);
+    const float* vsp = c.scale[1] + scale_at(c, l, 0, h);
+    const int32_t* table = c.table + static_cast<size_t>(b) * c.max_blocks;
+    int blk[4], row[4], ke[4], ve[4];
+    uint4 kc[4][DB], vc[4][DB];
+    auto lookup = [&](int i) {  // the tile's blocks
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int t = (tile0 + i) * kTokens + row_in + 32 * k;
+        blk[k] = i < n_tiles && t < len ? __ldg(table + by_bs.div(t)) : -1;
+      }
+    };
+    auto load = [&](int i) {  // rows, scales and keys of the tile whose blocks are known
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int t = (tile0 + i) * kTokens + row_in + 32 * k;
+        row[k] = -1;
+        ke[k] = ve[k] = -1000;
+        if (i < n_tiles && t < len) {
+          if (blk[k] < 0 || blk[k] >= c.n_blocks) {
+            bad = true;
+          } else {
+            row[k] = blk[k] * c.H * by_bs.bs + (t - by_bs.div(t) * by_bs.bs);
+            const size_t sc = static_cast<size_t>(blk[k]) * c.H;
+            ke[k] = static_cast<int>(__float_as_uint(__ldg(ksp + sc)) >> 23) - 127;
+            ve[k] = static_cast<int>(__float_as_uint(__ldg(vsp + sc)) >> 23) - 127;
+          }
+        }
+      }
+    };
+    auto load_codes = [&](const uint8_t* pool, uint4 (&to)[4][DB]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int x = 0; x < DB; ++x)
+          to[k][x] = row[k] >= 0 ? __ldg(reinterpret_cast<const uint4*>(
+                                       pool + static_cast<size_t>(row[k]) * D + (q4 + 4 * x) * 16))
+                                 : make_uint4(0, 0, 0, 0);
+    };
+    // 16 codes of a row, times 2^down, to their place in a tile
+    auto store = [&](uint8_t* tile, int r, int x, uint4 codes, bool scaled, uint32_t factor) {
+      const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) halves<FMT>(w[k], o[2 * k], o[2 * k + 1]);
+      if (scaled) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = mul_half2(o[k], factor);
+      }
+      uint8_t* at = tile + x * kBlock + r * 128;
+      *reinterpret_cast<uint4*>(at + (((2 * q4) ^ (r % 8)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(at + (((2 * q4 + 1) ^ (r % 8)) << 4)) =
+          make_uint4(o[4], o[5], o[6], o[7]);
+    };
+    lookup(0);
+    load(0);
+    load_codes(kp, kc);
+    for (int i = 0; i < n_tiles; ++i) {
+      const int st = i & 1;
+      load_codes(vp, vc);
+      lookup(i + 1);
+      // ---- the tile's scales ----
+      int k_max = -1000, v_max = -1000, v_min = 1000, absent = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        k_max = max(k_max, ke[k]);
+        v_max = max(v_max, ve[k]);
+        v_min = min(v_min, ve[k]);
+        absent |= row[k] < 0;
+      }
+      k_max = __reduce_max_sync(0xffffffffu, k_max);
+      v_max = __reduce_max_sync(0xffffffffu, v_max);
+      v_min = __reduce_min_sync(0xffffffffu, v_min);
+      absent = __any_sync(0xffffffffu, absent);
+      if (!warp_wait(&m_empty[st], ((i >> 1) & 1) ^ 1, abort, c.status)) break;
+      // (two buffers: a warp writes one again after all have read the other)
+      if (lane == 0) s_red[st * kConvertWarps + cw] = make_int4(k_max, v_max, v_min, absent);
+      warp_arrive(r_full);
+      if (!warp_wait(r_full, i & 1, abort, c.status)) break;
+#pragma unroll
+      for (int k = 0; k < kConvertWarps; ++k) {
+        const int4 o = s_red[st * kConvertWarps + k];
+        k_max = max(k_max, o.x);
+        v_max = max(v_max, o.y);
+        v_min = min(v_min, o.z);
+        absent |= o.w;
+      }
+      if (q4 == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s_e[st * kTokens + row_in + 32 * k] = row[k] < 0 ? -INFINITY : static_cast<float>(ve[k]);
+          s_back[st * kTokens + row_in + 32 * k] = row[k] < 0 ? 0.f : exp2_int(-ve[k]);
+        }
+      }
+      if (lane == 0 && cw == 0) {
+        TileInfo info;
+        info.k_ref = exp2_int(max(k_max, -126));
+        info.e_max = static_cast<float>(v_max);
+        info.plain = !absent && v_max - v_min <= static_cast<int>(kSpread);
+        info.uniform = v_max == v_min;
+        s_info[st] = info;
+      }
+      warp_arrive(&m_full[st]);
+      // ---- keys ----
+      uint32_t factor[4];
+      bool scaled = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        factor[k] = exp2_half2(max(ke[k] - k_max, -1000));
+        scaled = scaled || ke[k] != k_max;
+      }
+      scaled = __any_sync(0xffffffffu, scaled);
+      if (!warp_wait(k_empty, (i & 1) ^ 1, abort, c.status)) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int x = 0; x < DB; ++x)
+          store(smem + Sm::kK, row_in + 32 * k, x, kc[k][x], scaled, factor[k]);
+      fence_async_shared();
+      warp_arrive(k_full);
+      load(i + 1);
+      load_codes(kp, kc);
+      // ---- values ----
+      if (!warp_wait(v_empty, (i & 1) ^ 1, abort, c.status)) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int x = 0; x < DB; ++x) store(smem + Sm::kV, row_in + 32 * k, x, vc[k][x], false, 0);
+      fence_async_shared();
+      warp_arrive(v_full);
+    }
+    if (bad) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
+  } else {
+    // ------------------------------------------------------------ MMA issuer
+    // (all lanes wait converged; lane 0 issues)
+    const uint32_t base = smem_u32(smem);
+    bool ok = n_tiles > 0 && warp_wait(q_full, 0, abort, c.status);
+    for (int i = 0; ok && i < n_tiles; ++i) {
+      // (S takes P's columns: the last product has to be done with them)
+      if (!warp_wait(k_full, i & 1, abort, c.status) ||
+          (i > 0 && !warp_wait(o_full, (i - 1) & 1, abort, c.status)))
+        break;
+      tc_fence_after();
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_f16(kRows, kTokens, false);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * kBlock + (k % 4) * 32;
+          mma_bf16(tmem, sw128_desc(base + Sm::kQ + off), sw128_desc(base + Sm::kK + off), idesc,
+                   k > 0 ? 1u : 0u);
+        }
+        mma_commit(k_empty);
+        mma_commit(s_full);
+      }
+      __syncwarp();
+      if (!warp_wait(v_full, i & 1, abort, c.status) || !warp_wait(p_full, i & 1, abort, c.status))
+        break;
+      tc_fence_after();
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_f16(kRows, D, true);
+#pragma unroll
+        for (int k = 0; k < kTokens / 16; ++k)
+          mma_f16_ts(tmem + kOutCol, tmem + k * 8,
+                     sw128_desc_mn(base + Sm::kV + k * 2048, kBlock), idesc,
+                     i > 0 || k > 0 ? 1u : 0u);
+        mma_commit(v_empty);
+        mma_commit(o_full);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) mma_commit(done);
+    __syncwarp();
+    volatile int never = 0;  // also after an abort: what was issued ends
+    mbar_wait(done, 0, &never, c.status);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if (parts == 1) return;
+
+  // ---- join the parts: the last CTA to arrive, in the order of the parts ----
+  // (also after an abort, so that the count is whole again)
+  if (threadIdx.x == 0) {
+    int seen;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                 : "=r"(seen)
+                 : "l"(sp.arrived + ur)
+                 : "memory");
+    *s_last = seen == parts - 1;
+    if (seen == parts - 1) sp.arrived[ur] = 0;  // ready for the next call
+  }
+  __syncthreads();
+  if (!*s_last) return;
+  constexpr size_t kSlot = (D + 2) * kRows;
+  const float* first = sp.part + static_cast<size_t>(ur) * sp.per_tile * kSlot;
+  // a thread takes 8 values of a row
+  for (int x = threadIdx.x; x < kRows * (D / kPer); x += kThreads) {
+    const int row = x % kRows, d0 = x / kRows * kPer;
+    if (row >= rows) continue;
+    const float* from = first + row;
+    float mm = -INFINITY, y[kPer], s = 0.f;
+    for (int w = 0; w < parts; ++w) mm = fmaxf(mm, __ldcg(from + w * kSlot));
+    const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) y[k] = 0.f;
+#pragma unroll 2
+    for (int w = 0; w < parts; ++w) {
+      const float* pw = from + w * kSlot;
+      const float f = ex2(__ldcg(pw) - ref);
+      s += f * __ldcg(pw + kRows);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) y[k] += f * __ldcg(pw + (2 + d0 + k) * kRows);
+    }
+    write_row(c, a, l, b, h, r0 + row, nq, d0, y, mm, s);
+  }
+#endif
+}
+
+template <int D, int FMT>
+cudaError_t launch_many(const Cache& c, const AttendArgs& a, cudaStream_t s) {
+  auto* kernel = attend_many_kernel<D, FMT>;
+  static std::atomic<uint64_t> told{0};
+  const cudaError_t e = allow_smem(kernel, Smem<D>::kBytes, told);
+  if (e != cudaSuccess) return e;
+  Parts sp;
+  sp.row_tiles = (a.G * a.n + kRows - 1) / kRows;
+  sp.arrived = static_cast<int*>(a.workspace);
+  sp.part = reinterpret_cast<float*>(sp.arrived + kCounters);
+  const long long tiles = static_cast<long long>(c.L) * c.B * c.H * sp.row_tiles;
+  long long per = min(2 * a.num_sms, kMaxParts) / tiles;
+  sp.per_tile = static_cast<int>(per < 1 ? 1 : per);
+  kernel<<<static_cast<int>(tiles * sp.per_tile), kThreads, Smem<D>::kBytes, s>>>(c, a, sp,
+                                                                                  make_div(c.bs));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attend_many(const Cache& c, int format, const AttendArgs& a, cudaStream_t s) {
+  if (c.d == 64)
+    return format == KVC_CACHE8_E4M3 ? launch_many<64, KVC_CACHE8_E4M3>(c, a, s)
+                                     : launch_many<64, KVC_CACHE8_INT8>(c, a, s);
+  return format == KVC_CACHE8_E4M3 ? launch_many<128, KVC_CACHE8_E4M3>(c, a, s)
+                                   : launch_many<128, KVC_CACHE8_INT8>(c, a, s);
+}
+
+size_t attend_many_parts_bytes(int d) {
+  return kMaxParts * static_cast<size_t>(d + 2) * kRows * sizeof(float);
+}
+
+}  // namespace cache8
+}  // namespace kvc
