@@ -5,22 +5,24 @@
 //   out_r = sum_t w_rt v_t / sum_t w_rt,  w_rt = exp(scale q_r . k_t)
 //
 // Row r of a KV head is query r % nq of its group's head r / nq.  Per 128 tokens:
-//   converters (4 warps)  codes from global memory to fp16 tiles in shared memory,
-//                         in the swizzled layout of the MMA operands.  Keys carry
-//                         their block's scale relative to the tile's largest (a
-//                         power of two: exact, down to fp16's last step); values are
-//                         the codes themselves;
+//   converters (4 warps)  codes from global memory to fp16 tiles in shared memory, in
+//                         the swizzled layout of the MMA operands, one tile ahead.
+//                         Keys carry their block's scale relative to the tile's
+//                         largest, values relative to the largest so far (powers of
+//                         two: exact, down to fp16's last step);
 //   MMA (1 thread)        S = Q K^T (128 x 128, in TMEM), then O += P V with P read
 //                         from TMEM, where it takes the place of S;
-//   softmax (4 warps)     one thread a row: p = 2^(x - m), x = z + e with 2^e the
-//                         value scale of the token's block (so that P needs no scale
-//                         and stays within fp16 whatever the blocks' scales are), the
-//                         sum of 2^-e p in fp32, P to TMEM as fp16.
+//   softmax (4 warps)     one thread a row: p = 2^(z - m), their sum in fp32, P to TMEM
+//                         as fp16.  The first of these warps also issues the MMAs: it
+//                         would wait for them anyway.
 // The reference m of a row lies below its maximum: weights may reach 2^15 (fp16 has
-// the room) before m moves, and a new m leaves them at 2^8.  The maximum itself comes
-// with the TMEM load (tcgen05.ld.red) where the whole tile is seen and its blocks'
-// value scales are within 2^8 of each other: scores' maximum plus the largest e is
-// then at most 2^8 too high.  Else it is taken over the masked logits.
+// the room) before m moves, and a new m leaves them at 2^8.  The maximum comes with the
+// TMEM load (tcgen05.ld.red).  Half of a row stays in registers between the maximum
+// and the exponentials, the other half is loaded again.
+// Where the value scales 2^e of a tile are more than 2^8 below the largest so far, 2^v,
+// fp16 would lose the values: such a tile's values are the bare codes, and its logits
+// x = z + e - v carry the scale, with 2^(v - e) p in the sum.  That path takes masks and
+// absent tokens as well (e = -inf).
 //
 // The arithmetic bounds this: 4 R d operations a token, 1024 cycles of the tensor
 // pipe per 128 x 128 tile of d = 128.  S and P share columns, so that one CTA's
@@ -36,12 +38,12 @@ namespace cache8 {
 namespace {
 
 constexpr int kRows = 128, kTokens = 128;
-constexpr int kSoftmaxWarps = 4, kConvertWarps = 4, kMmaWarp = 8;
-constexpr int kThreads = 32 * 9;
+constexpr int kSoftmaxWarps = 4, kConvertWarps = 4;
+constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps);
 constexpr int kTmemCols = 256;    // S / P: 128, O: up to 128
 constexpr int kMaxParts = 320;    // CTAs of a call that cuts heads
 constexpr float kRoom = 15.f, kStart = 8.f;  // log2 of the weights' limit and of a new m's
-constexpr float kSpread = 8.f;
+constexpr int kSpread = 8;  // log2 of how far below the largest value scale stays plain
 
 struct Parts {
   int per_tile;   // CTAs of a row tile
@@ -61,10 +63,10 @@ struct Smem {
 
 // What a tile's converters tell the softmax warps.
 struct TileInfo {
-  float k_ref;    // the scale that the tile's keys are relative to
-  float e_max;    // largest log2 value scale
-  int plain;      // no token is absent and the value scales are within 2^kSpread
-  int uniform;    // and all the same
+  float k_ref;  // the scale that the tile's keys are relative to
+  int v_ref;    // log2 of the scale that its values are relative to (never falls)
+  int plain;    // no token is absent and no value scale is 2^kSpread below that
+  int unused;
 };
 
 __device__ __forceinline__ void fence_async_shared() {
@@ -106,16 +108,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     *abort = 0;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
+  if (warp == 0) tmem_alloc(tmem_slot, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -229,11 +229,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     float qf;
     {
       const uint4* q = reinterpret_cast<const uint4*>(a.q.at(l, b, hq, j));
+      uint4 v[D / 8];
       float mx = 0.f;
 #pragma unroll
+      for (int i = 0; i < D / 8; ++i) v[i] = there ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
       for (int i = 0; i < D / 8; ++i) {
-        const uint4 v = there ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
@@ -242,25 +244,64 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float down = exp2_int(-e);
       qf = a.scale_log2 * exp2_int(e);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 v = there ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < D / 8; ++i)
         *reinterpret_cast<uint4*>(smem + Sm::kQ + (i / 8) * kBlock + row * 128 +
                                   (((i % 8) ^ (row % 8)) << 4)) =
-            make_uint4(half2_of(bf16_lo(v.x) * down, bf16_hi(v.x) * down),
-                       half2_of(bf16_lo(v.y) * down, bf16_hi(v.y) * down),
-                       half2_of(bf16_lo(v.z) * down, bf16_hi(v.z) * down),
-                       half2_of(bf16_lo(v.w) * down, bf16_hi(v.w) * down));
-      }
+            make_uint4(half2_of(bf16_lo(v[i].x) * down, bf16_hi(v[i].x) * down),
+                       half2_of(bf16_lo(v[i].y) * down, bf16_hi(v[i].y) * down),
+                       half2_of(bf16_lo(v[i].z) * down, bf16_hi(v[i].z) * down),
+                       half2_of(bf16_lo(v[i].w) * down, bf16_hi(v[i].w) * down));
       fence_async_shared();
       warp_arrive(q_full);
     }
+    // the first warp issues the products (all lanes wait converged, lane 0 issues)
+    const uint32_t base = smem_u32(smem);
+    auto issue_scores = [&](int i) {  // S = Q K^T of tile i
+      // (S takes P's columns: the last product has to be done with them)
+      if (!warp_wait(k_full, i & 1, abort, c.status) ||
+          (i > 0 && !warp_wait(o_full, (i - 1) & 1, abort, c.status)))
+        return false;
+      tc_fence_after();
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_f16(kRows, kTokens, false);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k / 4) * kBlock + (k % 4) * 32;
+          mma_bf16(tmem, sw128_desc(base + Sm::kQ + off), sw128_desc(base + Sm::kK + off), idesc,
+                   k > 0 ? 1u : 0u);
+        }
+        mma_commit(k_empty);
+        mma_commit(s_full);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto issue_output = [&](int i) {  // O += P V of tile i
+      if (!warp_wait(v_full, i & 1, abort, c.status) || !warp_wait(p_full, i & 1, abort, c.status))
+        return false;
+      tc_fence_after();
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_f16(kRows, D, true);
+#pragma unroll
+        for (int k = 0; k < kTokens / 16; ++k)
+          mma_f16_ts(tmem + kOutCol, tmem + k * 8,
+                     sw128_desc_mn(base + Sm::kV + k * 2048, kBlock), idesc,
+                     i > 0 || k > 0 ? 1u : 0u);
+        mma_commit(v_empty);
+        mma_commit(o_full);
+      }
+      __syncwarp();
+      return true;
+    };
     const int limit = len - nq + j;     // last token that this row sees
-    float m = -INFINITY, sum = 0.f;     // reference and sum of 2^-e p
+    float m = -INFINITY, sum = 0.f;     // reference and sum of the weights
+    int v_ref = 0;
     bool ok = true;
-    for (int i = 0; i < n_tiles; ++i) {
+    if (warp == 0 && n_tiles > 0)
+      ok = warp_wait(q_full, 0, abort, c.status) && issue_scores(0);
+    for (int i = 0; ok && i < n_tiles; ++i) {
       const int t0 = (tile0 + i) * kTokens, st = i & 1;
-      const uint32_t parity = (i >> 1) & 1;
-      if (!warp_wait(&m_full[st], parity, abort, c.status) ||
+      if (!warp_wait(&m_full[st], (i >> 1) & 1, abort, c.status) ||
           !warp_wait(s_full, i & 1, abort, c.status)) {
         ok = false;
         break;
@@ -270,67 +311,67 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float* e_col = s_e + st * kTokens;
       const float* back_col = s_back + st * kTokens;
       const float f = qf * info.k_ref;
-      const bool whole = info.plain && t0 + kTokens <= len - nq + 1;  // the same for all rows
-      // ---- the maximum, or a bound of it ----
-      float top = -INFINITY;
-      if (whole) {
-#pragma unroll
-        for (int k = 0; k < kTokens / 32; ++k) {
-          uint32_t v[32];
-          float mx;
-          tmem_ld32_max(my_tmem + k * 32, v, mx);
-          tmem_ld_wait();
-          top = fmaxf(top, mx);
-        }
-        top = fmaf(top, f, info.e_max);
+      const bool fast = info.plain && t0 + kTokens <= len - nq + 1;  // seen by all rows
+      uint32_t va[32], vb[32];
+      float top;
+      if (fast) {
+        float m0, m1;
+        tmem_ld32_max(my_tmem + 64, va, m0);
+        tmem_ld32_max(my_tmem + 96, vb, m1);
+        tmem_ld_wait();
+        top = fmaxf(m0, m1);
+        tmem_ld32_max(my_tmem, va, m0);
+        tmem_ld32_max(my_tmem + 32, vb, m1);
+        tmem_ld_wait();
+        top = fmaxf(top, fmaxf(m0, m1)) * f;
       } else {
+        top = -INFINITY;
 #pragma unroll 1
         for (int k = 0; k < kTokens / 32; ++k) {
-          uint32_t v[32];
-          tmem_ld32(my_tmem + k * 32, v);
+          tmem_ld32(my_tmem + k * 32, va);
           tmem_ld_wait();
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
-            const float z = fmaf(__uint_as_float(v[x]), f, e_col[k * 32 + x]);
+            const float z = fmaf(__uint_as_float(va[x]), f, e_col[k * 32 + x]);
             if (t0 + k * 32 + x <= limit) top = fmaxf(top, z);
           }
         }
       }
-      // ---- a new reference: what is there is scaled to it ----
+      // ---- new references: what is there is scaled to them ----
       const bool raise = top > m + kRoom;
-      if (__any_sync(0xffffffffu, raise)) {
+      const bool shift = i > 0 && info.v_ref != v_ref;
+      if (__any_sync(0xffffffffu, raise || shift)) {
         const float next = raise ? top - kStart : m;
-        const float scale = raise ? ex2(m - next) : 1.f;
+        const float keep = raise ? ex2(m - next) : 1.f;
         m = next;
-        sum *= scale;
+        sum *= keep;
         if (i > 0) {
+          const float scale = keep * ex2(static_cast<float>(v_ref - info.v_ref));
           if (!warp_wait(o_full, (i - 1) & 1, abort, c.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
+          uint32_t v[16];
 #pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t v[32];
-            tmem_ld32(my_tmem + kOutCol + k * 32, v);
+          for (int k = 0; k < D / 16; ++k) {
+            tmem_ld16(my_tmem + kOutCol + k * 16, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * scale);
-            tmem_st32(my_tmem + kOutCol + k * 32, v);
+            for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * scale);
+            tmem_st16(my_tmem + kOutCol + k * 16, v);
           }
           tmem_st_wait();
         }
       }
+      v_ref = info.v_ref;
       // ---- weights: S's columns become P's ----
       const float ref = m == -INFINITY ? 0.f : m;
-      if (whole && info.uniform) {
-        const float2 ff = make_float2(f, f), off = make_float2(info.e_max - ref, info.e_max - ref);
-        float2 part_sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kTokens / 32; ++k) {
-          uint32_t v[32], p[16];
-          tmem_ld32(my_tmem + k * 32, v);
-          tmem_ld_wait();
+      const float2 ff = make_float2(f, f), off = make_float2(-ref, -ref);
+      float2 part_sum = make_float2(0.f, 0.f);
+      if (fast) {
+        auto weights = [&](const uint32_t (&v)[32], uint32_t to) {
+          uint32_t p[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             float2 z = fma2(make_float2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])),
@@ -340,17 +381,22 @@ __global__ void __launch_bounds__(kThreads, 2)
             part_sum = add2(part_sum, z);
             p[x] = half2_of(z.x, z.y);
           }
-          tmem_st16(my_tmem + k * 16, p);
-        }
-        sum = fmaf(part_sum.x + part_sum.y, back_col[0], sum);
+          tmem_st16(to, p);
+        };
+        // columns 0-63 are in registers, and P takes no others before 64-127 are read
+        weights(va, my_tmem);
+        tmem_ld32(my_tmem + 64, va);
+        weights(vb, my_tmem + 16);
+        tmem_ld32(my_tmem + 96, vb);
+        tmem_ld_wait();
+        weights(va, my_tmem + 32);
+        weights(vb, my_tmem + 48);
       } else {
-        const float2 ff = make_float2(f, f), off = make_float2(-ref, -ref);
-        float2 part_sum = make_float2(0.f, 0.f);
-        const int seen = whole ? kTokens : limit - t0 + 1;  // columns that this row sees
+        const int seen = limit - t0 + 1;  // columns that this row sees
 #pragma unroll 1
         for (int k = 0; k < kTokens / 32; ++k) {
-          uint32_t v[32], p[16];
-          tmem_ld32(my_tmem + k * 32, v);
+          uint32_t p[16];
+          tmem_ld32(my_tmem + k * 32, va);
           tmem_ld_wait();
 #pragma unroll
           for (int x = 0; x < 16; x += 2) {
@@ -359,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const int at = 2 * (x + y);
-              float2 z = fma2(make_float2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), ff,
+              float2 z = fma2(make_float2(__uint_as_float(va[at]), __uint_as_float(va[at + 1])), ff,
                               y ? make_float2(e4.z, e4.w) : make_float2(e4.x, e4.y));
               z = add2(z, off);
               z.x = k * 32 + at < seen ? ex2(z.x) : 0.f;
@@ -370,19 +416,27 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           tmem_st16(my_tmem + k * 16, p);
         }
-        sum += part_sum.x + part_sum.y;
       }
+      sum += part_sum.x + part_sum.y;
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(p_full);
       if (lane == 0) mbar_arrive(&m_empty[st]);
+      if (warp == 0) ok = issue_output(i) && (i + 1 == n_tiles || issue_scores(i + 1));
+    }
+    if (warp == 0) {
+      if (lane == 0) mma_commit(done);
+      __syncwarp();
+      volatile int never = 0;  // also after an abort: what was issued ends
+      mbar_wait(done, 0, &never, c.status);
     }
     // ---- the result ----
     if (ok && n_tiles > 0) ok = warp_wait(o_full, (n_tiles - 1) & 1, abort, c.status);
     if (ok) {
       tc_fence_after();
       float* slot = sp.part + static_cast<size_t>(blockIdx.x) * ((D + 2) * kRows) + row;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float unit = exp2_int(v_ref);
+      const float inv = sum == 0.f ? 0.f : unit / sum;
 #pragma unroll 1
       for (int k = 0; k < D / 32; ++k) {
         uint32_t v[32];
@@ -405,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         } else if (there) {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) slot[(2 + k * 32 + x) * kRows] = __uint_as_float(v[x]);
+          for (int x = 0; x < 32; ++x) slot[(2 + k * 32 + x) * kRows] = __uint_as_float(v[x]) * unit;
         }
         __syncwarp();
       }
@@ -417,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         slot[kRows] = sum;
       }
     }
-  } else if (warp < kSoftmaxWarps + kConvertWarps) {
+  } else {
     // ------------------------------------------------------------ converters
     // This lane: rows (tokens) row_in + 32 i, 16-byte chunks q4 + 4 j of them.
     const int cw = warp - kSoftmaxWarps, q4 = lane % 4;
@@ -427,8 +481,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float* ksp = c.scale[0] + scale_at(c, l, 0, h);
     const float* vsp = c.scale[1] + scale_at(c, l, 0, h);
     const int32_t* table = c.table + static_cast<size_t>(b) * c.max_blocks;
-    int blk[4], row[4], ke[4], ve[4];
+    int blk[4], row[4];
+    uint32_t ks[4], vs[4];  // scales as they are in memory
     uint4 kc[4][DB], vc[4][DB];
+    int v_ref = -1000;      // largest value exponent so far
     auto lookup = [&](int i) {  // the tile's blocks
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -436,20 +492,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         blk[k] = i < n_tiles && t < len ? __ldg(table + by_bs.div(t)) : -1;
       }
     };
-    auto load = [&](int i) {  // rows, scales and keys of the tile whose blocks are known
+    auto resolve = [&](int i) {  // rows and scales of the tile whose blocks are known
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int t = (tile0 + i) * kTokens + row_in + 32 * k;
         row[k] = -1;
-        ke[k] = ve[k] = -1000;
+        ks[k] = vs[k] = 0;
         if (i < n_tiles && t < len) {
           if (blk[k] < 0 || blk[k] >= c.n_blocks) {
             bad = true;
           } else {
             row[k] = blk[k] * c.H * by_bs.bs + (t - by_bs.div(t) * by_bs.bs);
             const size_t sc = static_cast<size_t>(blk[k]) * c.H;
-            ke[k] = static_cast<int>(__float_as_uint(__ldg(ksp + sc)) >> 23) - 127;
-            ve[k] = static_cast<int>(__float_as_uint(__ldg(vsp + sc)) >> 23) - 127;
+            ks[k] = __float_as_uint(__ldg(ksp + sc));
+            vs[k] = __float_as_uint(__ldg(vsp + sc));
           }
         }
       }
@@ -478,21 +534,28 @@ __global__ void __launch_bounds__(kThreads, 2)
       *reinterpret_cast<uint4*>(at + (((2 * q4 + 1) ^ (r % 8)) << 4)) =
           make_uint4(o[4], o[5], o[6], o[7]);
     };
+    // a tile's codes are loaded while the last one's are stored, its blocks and scales
+    // one step before
     lookup(0);
-    load(0);
+    resolve(0);
     load_codes(kp, kc);
+    load_codes(vp, vc);
+    lookup(1);
     for (int i = 0; i < n_tiles; ++i) {
       const int st = i & 1;
-      load_codes(vp, vc);
-      lookup(i + 1);
       // ---- the tile's scales ----
-      int k_max = -1000, v_max = -1000, v_min = 1000, absent = 0;
+      int ke[4], ve[4], k_max = -1000, v_max = -1000, v_min = 1000, absent = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        ke[k] = static_cast<int>(ks[k] >> 23) - 127;
+        ve[k] = static_cast<int>(vs[k] >> 23) - 127;
+        if (row[k] < 0) {
+          absent = 1;
+          continue;
+        }
         k_max = max(k_max, ke[k]);
         v_max = max(v_max, ve[k]);
         v_min = min(v_min, ve[k]);
-        absent |= row[k] < 0;
       }
       k_max = __reduce_max_sync(0xffffffffu, k_max);
       v_max = __reduce_max_sync(0xffffffffu, v_max);
@@ -511,99 +574,68 @@ __global__ void __launch_bounds__(kThreads, 2)
         v_min = min(v_min, o.z);
         absent |= o.w;
       }
+      k_max = max(k_max, -126);
+      v_ref = max(max(v_ref, v_max), -126);
+      const bool plain = !absent && v_ref - v_min <= kSpread;
       if (q4 == 0) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          s_e[st * kTokens + row_in + 32 * k] = row[k] < 0 ? -INFINITY : static_cast<float>(ve[k]);
-          s_back[st * kTokens + row_in + 32 * k] = row[k] < 0 ? 0.f : exp2_int(-ve[k]);
+          const bool bare = !plain && row[k] >= 0;
+          s_e[st * kTokens + row_in + 32 * k] =
+              row[k] < 0 ? -INFINITY : bare ? static_cast<float>(ve[k] - v_ref) : 0.f;
+          s_back[st * kTokens + row_in + 32 * k] =
+              row[k] < 0 ? 0.f : bare ? exp2_int(min(v_ref - ve[k], 126)) : 1.f;
         }
       }
       if (lane == 0 && cw == 0) {
         TileInfo info;
-        info.k_ref = exp2_int(max(k_max, -126));
-        info.e_max = static_cast<float>(v_max);
-        info.plain = !absent && v_max - v_min <= static_cast<int>(kSpread);
-        info.uniform = v_max == v_min;
+        info.k_ref = exp2_int(k_max);
+        info.v_ref = v_ref;
+        info.plain = plain;
+        info.unused = 0;
         s_info[st] = info;
       }
       warp_arrive(&m_full[st]);
-      // ---- keys ----
-      uint32_t factor[4];
-      bool scaled = false;
+      // ---- keys and values, relative to those scales ----
+      uint32_t k_factor[4], v_factor[4];
+      bool k_scaled = false, v_scaled = false;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        factor[k] = exp2_half2(max(ke[k] - k_max, -1000));
-        scaled = scaled || ke[k] != k_max;
+        k_factor[k] = exp2_half2(min(ke[k] - k_max, 0));
+        v_factor[k] = exp2_half2(min(ve[k] - v_ref, 0));
+        k_scaled = k_scaled || ke[k] != k_max;
+        v_scaled = v_scaled || (plain && ve[k] != v_ref);
       }
-      scaled = __any_sync(0xffffffffu, scaled);
+      k_scaled = __any_sync(0xffffffffu, k_scaled);
+      v_scaled = __any_sync(0xffffffffu, v_scaled);
       if (!warp_wait(k_empty, (i & 1) ^ 1, abort, c.status)) break;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int x = 0; x < DB; ++x)
-          store(smem + Sm::kK, row_in + 32 * k, x, kc[k][x], scaled, factor[k]);
+          store(smem + Sm::kK, row_in + 32 * k, x, kc[k][x], k_scaled, k_factor[k]);
       fence_async_shared();
       warp_arrive(k_full);
-      load(i + 1);
+      resolve(i + 1);
       load_codes(kp, kc);
-      // ---- values ----
+      lookup(i + 2);
       if (!warp_wait(v_empty, (i & 1) ^ 1, abort, c.status)) break;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int x = 0; x < DB; ++x) store(smem + Sm::kV, row_in + 32 * k, x, vc[k][x], false, 0);
+        for (int x = 0; x < DB; ++x)
+          store(smem + Sm::kV, row_in + 32 * k, x, vc[k][x], v_scaled, v_factor[k]);
       fence_async_shared();
       warp_arrive(v_full);
+      load_codes(vp, vc);
     }
     if (bad) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
-  } else {
-    // ------------------------------------------------------------ MMA issuer
-    // (all lanes wait converged; lane 0 issues)
-    const uint32_t base = smem_u32(smem);
-    bool ok = n_tiles > 0 && warp_wait(q_full, 0, abort, c.status);
-    for (int i = 0; ok && i < n_tiles; ++i) {
-      // (S takes P's columns: the last product has to be done with them)
-      if (!warp_wait(k_full, i & 1, abort, c.status) ||
-          (i > 0 && !warp_wait(o_full, (i - 1) & 1, abort, c.status)))
-        break;
-      tc_fence_after();
-      if (lane == 0) {
-        constexpr uint32_t idesc = idesc_f16(kRows, kTokens, false);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k / 4) * kBlock + (k % 4) * 32;
-          mma_bf16(tmem, sw128_desc(base + Sm::kQ + off), sw128_desc(base + Sm::kK + off), idesc,
-                   k > 0 ? 1u : 0u);
-        }
-        mma_commit(k_empty);
-        mma_commit(s_full);
-      }
-      __syncwarp();
-      if (!warp_wait(v_full, i & 1, abort, c.status) || !warp_wait(p_full, i & 1, abort, c.status))
-        break;
-      tc_fence_after();
-      if (lane == 0) {
-        constexpr uint32_t idesc = idesc_f16(kRows, D, true);
-#pragma unroll
-        for (int k = 0; k < kTokens / 16; ++k)
-          mma_f16_ts(tmem + kOutCol, tmem + k * 8,
-                     sw128_desc_mn(base + Sm::kV + k * 2048, kBlock), idesc,
-                     i > 0 || k > 0 ? 1u : 0u);
-        mma_commit(v_empty);
-        mma_commit(o_full);
-      }
-      __syncwarp();
-    }
-    if (lane == 0) mma_commit(done);
-    __syncwarp();
-    volatile int never = 0;  // also after an abort: what was issued ends
-    mbar_wait(done, 0, &never, c.status);
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
   if (parts == 1) return;
 
   // ---- join the parts: the last CTA to arrive, in the order of the parts ----
