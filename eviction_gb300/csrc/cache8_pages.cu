@@ -3,14 +3,18 @@
 // sequences up (free).
 //
 // The tables are a few thousand integers, so their work is latency: one CTA does
-// each call, with its lists in shared memory.  A call either does everything or
-// changes nothing, so every index is checked before the first write.  The order in
-// which blocks leave and enter the stack is fixed (list order, then block order),
-// which makes the tables reproducible: counts go through atomics, whose order
-// does not matter for integers, and places come from prefix sums.
+// each call, and what counts is how many loads wait for one another.  A thread
+// keeps its sequence and its first kKeep table entries in registers from the checks
+// to the writes; entries past those (of calls over kKeep * 1024) are read again.  A
+// call either does everything or changes nothing, so every index is checked before
+// the first write that cannot be taken back.  The order in which blocks leave and
+// enter the stack is fixed (list order, then block order), which makes the tables
+// reproducible: counts go through atomics, whose order does not matter for
+// integers, and places come from prefix sums.
 //
 // fork copies the rows of the started blocks in a second launch over all layers
-// and heads, which skips its work when the first one refused.
+// (one CTA per new sequence and layer), which skips its work when the first one
+// refused.
 #include "cache8.cuh"
 
 namespace kvc {
@@ -57,31 +61,43 @@ __device__ __forceinline__ int blocks_for(int tokens, int bs) {
   return tokens / bs + (tokens % bs ? 1 : 0);
 }
 
+constexpr int kKeep = 4;  // table entries a thread keeps
+
+// Where entry e (of all lists of a pass, one after another) lies: list k of those
+// that end at ends[], place col in it.
+struct Place {
+  int k, col;
+};
+__device__ __forceinline__ Place place_of(const int* ends, int e) {
+  const int k = owner(ends, kSeqs, e);
+  return {k, e - (k ? ends[k - 1] : 0)};
+}
+
 // ---- grow ----
 
-__global__ void __launch_bounds__(kThreads) grow_kernel(Cache c, const int32_t* n_new) {
+__global__ void __launch_bounds__(kThreads, 1) grow_kernel(Cache c, const int32_t* n_new) {
   __shared__ int ends[kSeqs], have[kSeqs];
   const int t = threadIdx.x;
   const int top = *c.free_top;
   bool bad = top < 0 || top > c.n_blocks;
   long long need_all = 0;  // of this thread's sequences
+  int len = 0, n = 0;      // of its first one
   for (int b = t; b < c.B; b += kThreads) {
-    const int len = length_of(c, b, &bad), n = n_new[b];
-    if (n < 0 || static_cast<long long>(len) + n > static_cast<long long>(c.max_blocks) * c.bs) {
+    const int bl = length_of(c, b, &bad), bn = n_new[b];
+    if (b == t) len = bl, n = bn;
+    if (bn < 0 || static_cast<long long>(bl) + bn > static_cast<long long>(c.max_blocks) * c.bs) {
       bad = true;
       continue;
     }
-    need_all += blocks_for(len + n, c.bs) - blocks_for(len, c.bs);
-    if (n > 0 && len % c.bs) {  // the started block has to be this sequence's alone
-      const int blk = block_at(c, b, len / c.bs);
+    need_all += blocks_for(bl + bn, c.bs) - blocks_for(bl, c.bs);
+    if (bn > 0 && bl % c.bs) {  // the started block has to be this sequence's alone
+      const int blk = block_at(c, b, bl / c.bs);
       bad = bad || blk < 0 || c.ref_count[blk] != 1;
     }
   }
-  // a thread's own need may be larger than the stack: cap it before the int scan
-  int need = 0;
-  const int mine = static_cast<int>(min(need_all, static_cast<long long>(c.n_blocks) + 1));
   const bool any_bad = __syncthreads_or(bad);
-  // the sum of kThreads capped needs can pass 2^31: scan in 64 bits by halves
+  // a sum of needs can pass 2^31: each capped above the stack's size, then in halves
+  const int mine = static_cast<int>(min(need_all, static_cast<long long>(c.n_blocks) + 1));
   int lo_total, hi_total;
   block_scan(mine & 0xffff, &lo_total);
   block_scan(mine >> 16, &hi_total);
@@ -92,8 +108,19 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(Cache c, const int32_t* 
   }
   const int base = top - static_cast<int>(all);
   // what the stack gives has to be blocks that nobody holds
+  int taken[kKeep];
   bad = false;
-  for (int e = t; e < static_cast<int>(all); e += kThreads) {
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    const int e = t + i * kThreads;
+    taken[i] = e < all ? c.free_list[base + e] : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    if (t + i * kThreads < all)
+      bad = bad || taken[i] < 0 || taken[i] >= c.n_blocks || c.ref_count[taken[i]] != 0;
+  }
+  for (int e = t + kKeep * kThreads; e < all; e += kThreads) {
     const int blk = c.free_list[base + e];
     bad = bad || blk < 0 || blk >= c.n_blocks || c.ref_count[blk] != 0;
   }
@@ -101,26 +128,30 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(Cache c, const int32_t* 
     if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
     return;
   }
-  int from = base;
+  int from = 0;
   for (int b0 = 0; b0 < c.B; b0 += kSeqs) {
     const int b = b0 + t;
-    need = 0;
-    if (b < c.B) {
-      const int len = c.seq_len[b], n = n_new[b];
-      have[t] = blocks_for(len, c.bs);
-      need = blocks_for(len + n, c.bs) - have[t];
-      if (n) c.seq_len[b] = len + n;
+    if (b0 > 0) {
+      len = b < c.B ? c.seq_len[b] : 0;
+      n = b < c.B ? n_new[b] : 0;
     }
+    have[t] = blocks_for(len, c.bs);
     int total;
-    ends[t] = block_scan(need, &total);
+    ends[t] = block_scan(blocks_for(len + n, c.bs) - have[t], &total);
+    if (n) c.seq_len[b] = len + n;
     __syncthreads();
-    for (int e = t; e < total; e += kThreads) {
-      const int i = owner(ends, kSeqs, e);
-      const int k = e - (i ? ends[i - 1] : 0);
-      const int blk = c.free_list[from + e];
-      c.table[static_cast<size_t>(b0 + i) * c.max_blocks + have[i] + k] = blk;
+    auto give = [&](int e, int blk) {
+      const Place p = place_of(ends, e);
+      c.table[static_cast<size_t>(b0 + p.k) * c.max_blocks + have[p.k] + p.col] = blk;
       c.ref_count[blk] = 1;
+    };
+    if (b0 == 0) {
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if (t + i * kThreads < total) give(t + i * kThreads, taken[i]);
     }
+    for (int e = b0 == 0 ? t + kKeep * kThreads : t; e < total; e += kThreads)
+      give(e, c.free_list[base + from + e]);
     from += total;
     __syncthreads();
   }
@@ -129,34 +160,70 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(Cache c, const int32_t* 
 
 // ---- free ----
 
-// Calls f(key, block) for every table entry of the listed sequences; keys ascend
-// with list and block order (-1 for a thread without an entry).  The sequences
-// are checked and marked.  Whole CTA; `ends` is scratch of kSeqs ints.
+constexpr int kMarkBits = 1 << 16;  // sequences that the marks in shared memory cover
+
+// Whether a sequence number is listed twice, or is in `others` too (may be null).
+// Whole CTA; the numbers are in range.
+__device__ bool listed_twice(const Cache& c, int n, const int32_t* seqs, const int32_t* others,
+                             uint32_t* marks) {
+  bool twice = false;
+  for (int base = 0; base < c.B; base += kMarkBits) {
+    const int words = (min(c.B - base, kMarkBits) + 31) / 32;
+    for (int i = threadIdx.x; i < words; i += kThreads) marks[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const int s = seqs[i] - base;
+      if (s >= 0 && s < kMarkBits)
+        twice = (atomicOr(&marks[s / 32], 1u << (s % 32)) >> (s % 32) & 1u) || twice;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; others && i < n; i += kThreads) {
+      const int s = others[i] - base;
+      if (s >= 0 && s < kMarkBits) twice = (marks[s / 32] >> (s % 32) & 1u) || twice;
+    }
+    __syncthreads();
+  }
+  return __syncthreads_or(twice);
+}
+
+// Calls f(key, number, entry) for every table entry of the listed sequences, 0 <=
+// number < kKeep for a thread's first ones; keys ascend with list and block order, and
+// are -1 for a thread without an entry.  Whole CTA; `ends` is scratch of kSeqs ints.
 template <class F>
 __device__ void for_entries(const Cache& c, int n, const int32_t* seqs, int* ends, F f) {
   for (int i0 = 0; i0 < n; i0 += kSeqs) {
     const int i = i0 + threadIdx.x;
-    const int held = i < n ? blocks_for(c.seq_len[seqs[i]] & 0x7fffffff, c.bs) : 0;
+    const int held = i < n ? blocks_for(c.seq_len[seqs[i]], c.bs) : 0;
     int total;
     __syncthreads();
     ends[threadIdx.x] = block_scan(held, &total);
     __syncthreads();
-    for (int e0 = 0; e0 < total; e0 += kThreads) {
-      const int e = e0 + threadIdx.x;
-      int k = -1, col = 0;
+    // (f may hold barriers: every thread calls it, at one place)
+    auto one = [&](int e, int number) {
+      int key = -1;
+      int32_t* at = nullptr;
       if (e < total) {
-        k = owner(ends, kSeqs, e);
-        col = e - (k ? ends[k - 1] : 0);
+        const Place p = place_of(ends, e);
+        key = (i0 + p.k) * c.max_blocks + p.col;
+        at = c.table + static_cast<size_t>(seqs[i0 + p.k]) * c.max_blocks + p.col;
       }
-      f(k < 0 ? -1 : (i0 + k) * c.max_blocks + col,
-        k < 0 ? nullptr : c.table + static_cast<size_t>(seqs[i0 + k]) * c.max_blocks + col);
+      f(key, number, at);
+    };
+    int e0 = 0;
+    if (i0 == 0) {
+#pragma unroll
+      for (int k = 0; k < kKeep; ++k)
+        if (k * kThreads < total) one(k * kThreads + threadIdx.x, k);
+      e0 = kKeep * kThreads;
     }
+    for (; e0 < total; e0 += kThreads) one(e0 + threadIdx.x, kKeep);
   }
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads) free_kernel(Cache c, int n, const int32_t* seqs) {
+__global__ void __launch_bounds__(kThreads, 1) free_kernel(Cache c, int n, const int32_t* seqs) {
   __shared__ int ends[kSeqs];
+  __shared__ uint32_t marks[kMarkBits / 32];
   const int t = threadIdx.x;
   const int top = *c.free_top;
   bool bad = top < 0 || top > c.n_blocks;
@@ -167,73 +234,89 @@ __global__ void __launch_bounds__(kThreads) free_kernel(Cache c, int n, const in
     else
       length_of(c, s, &bad);
   }
+  if (__syncthreads_or(bad) || listed_twice(c, n, seqs, nullptr, marks)) {
+    if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
+    return;
+  }
+  int kept[kKeep];   // this thread's first entries (blocks)
+  for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
+    if (key < 0) return;
+    const int blk = *at;
+    if (number < kKeep) kept[number] = blk;
+    bad = bad || blk < 0 || blk >= c.n_blocks;
+  });
   if (__syncthreads_or(bad)) {
     if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
     return;
   }
-  // mark the listed sequences (sign bit of the length): one marked twice is listed twice
-  for (int i = t; i < n; i += kThreads)
-    bad = bad || atomicOr(&c.seq_len[seqs[i]], static_cast<int>(0x80000000u)) < 0;
-  if (!__syncthreads_or(bad)) {
-    for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
+  auto block = [&](int number, const int32_t* at) { return number < kKeep ? kept[number] : *at; };
+  // one holder fewer; the count before says whether the block is free now (1), was
+  // shared (more), or had more holders than were counted (less)
+  int before[kKeep];
+  bool shared = false;
+  for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
+    if (key < 0) return;
+    const int was = atomicSub(&c.ref_count[block(number, at)], 1);
+    if (number < kKeep) before[number] = was;
+    bad = bad || was < 1;
+    shared = shared || was > 1 || number >= kKeep;
+  });
+  auto put_back = [&] {
+    for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
+      if (key >= 0) atomicAdd(&c.ref_count[block(number, at)], 1);
+    });
+    if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
+  };
+  if (__syncthreads_or(bad)) {
+    put_back();
+    return;
+  }
+  // An entry whose block nobody holds now pushes it: the last one in the list, where
+  // several have the same block.  (There is one entry alone if none was shared.)
+  const bool any_shared = __syncthreads_or(shared);
+  if (any_shared) {
+    for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
       if (key < 0) return;
-      const int blk = *at;
-      bad = bad || blk < 0 || blk >= c.n_blocks;
+      int* count = &c.ref_count[block(number, at)];
+      if (*count <= 0) atomicMin(count, -1 - key);  // zero, or another entry's mark
     });
   }
-  if (__syncthreads_or(bad)) {
-    for (int i = t; i < n; i += kThreads) atomicAnd(&c.seq_len[seqs[i]], 0x7fffffff);
-    if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
-    return;
-  }
-  for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
-    if (key >= 0) atomicSub(&c.ref_count[*at], 1);
+  auto pushes = [&](int key, int number, const int32_t* at) {
+    if (key < 0) return false;
+    return any_shared ? c.ref_count[block(number, at)] == -1 - key : before[number] == 1;
+  };
+  int mine = 0, all;
+  for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
+    if (number < kKeep) {
+      const bool push = pushes(key, number, at);
+      before[number] = push;  // (known from here on)
+      mine += push;
+    } else {
+      mine += pushes(key, number, at);
+    }
   });
-  // a count below zero: more holders than were counted; put everything back
-  for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
-    if (key >= 0) bad = bad || c.ref_count[*at] < 0;
-  });
-  if (__syncthreads_or(bad)) {
-    for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
-      if (key >= 0) atomicAdd(&c.ref_count[*at], 1);
-    });
-    for (int i = t; i < n; i += kThreads) atomicAnd(&c.seq_len[seqs[i]], 0x7fffffff);
-    if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
-    return;
-  }
-  // a block that nobody holds: its count becomes -1 - (its last key in the list)
-  for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
-    if (key >= 0 && c.ref_count[*at] <= 0) atomicMin(&c.ref_count[*at], -1 - key);
-  });
-  int pushes = 0, all;
-  for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
-    if (key >= 0) pushes += c.ref_count[*at] == -1 - key;
-  });
-  block_scan(pushes, &all);
+  block_scan(mine, &all);
   if (all > c.n_blocks - top) {  // more blocks than there are: the stack was wrong
-    for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
-      if (key >= 0 && c.ref_count[*at] < 0) c.ref_count[*at] = 0;
+    for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
+      if (key >= 0 && c.ref_count[block(number, at)] < 0) c.ref_count[block(number, at)] = 0;
     });
-    for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
-      if (key >= 0) atomicAdd(&c.ref_count[*at], 1);
-    });
-    for (int i = t; i < n; i += kThreads) atomicAnd(&c.seq_len[seqs[i]], 0x7fffffff);
-    if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
+    put_back();
     return;
   }
   int to = top;
-  for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
-    const int blk = key >= 0 ? *at : 0;
-    const bool push = key >= 0 && c.ref_count[blk] == -1 - key;
+  for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
+    const bool push = number < kKeep ? key >= 0 && before[number] : pushes(key, number, at);
     int total;
     const int place = to + block_scan(push, &total) - 1;
-    if (push) c.free_list[place] = blk;
+    if (push) c.free_list[place] = block(number, at);
     to += total;
   });
-  for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
+  for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
     if (key < 0) return;
-    const int blk = *at;
-    if (c.ref_count[blk] < 0) c.ref_count[blk] = 0;
+    if (any_shared) {
+      int* count = &c.ref_count[block(number, at)];
+      if (*count < 0) *count = 0;
+    }
     *at = -1;
   });
   for (int i = t; i < n; i += kThreads) c.seq_len[seqs[i]] = 0;
@@ -242,14 +325,15 @@ __global__ void __launch_bounds__(kThreads) free_kernel(Cache c, int n, const in
 
 // ---- fork ----
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1)
     fork_kernel(Cache c, int n, const int32_t* src, const int32_t* dst) {
   __shared__ int ends[kSeqs], part[kSeqs];
+  __shared__ uint32_t marks[kMarkBits / 32];
   const int t = threadIdx.x;
   if (t == 0) *c.err = 0;
   const int top = *c.free_top;
   bool bad = top < 0 || top > c.n_blocks;
-  int started = 0;
+  int started = 0, first_len = 0;
   for (int i = t; i < n; i += kThreads) {
     const int s = src[i], d = dst[i];
     if (s < 0 || s >= c.B || d < 0 || d >= c.B) {
@@ -257,16 +341,17 @@ __global__ void __launch_bounds__(kThreads)
       continue;
     }
     const int len = length_of(c, s, &bad);
+    if (i == t) first_len = len;
     started += len % c.bs ? 1 : 0;
     bad = bad || c.seq_len[d] != 0;
   }
   int all;
   block_scan(started, &all);
   bool full = false;
-  if (!__syncthreads_or(bad)) {
-    // mark the new sequences: one marked twice is listed twice
-    for (int i = t; i < n; i += kThreads)
-      bad = bad || atomicExch(&c.seq_len[dst[i]], static_cast<int>(0x80000000u)) != 0;
+  // a new sequence listed twice, or also as a source (which can only be an empty one)
+  bad = __syncthreads_or(bad);
+  if (!bad) bad = listed_twice(c, n, dst, src, marks);
+  if (!bad) {
     full = all > top;
     if (!full) {
       for (int e = t; e < all; e += kThreads) {
@@ -274,26 +359,20 @@ __global__ void __launch_bounds__(kThreads)
         bad = bad || blk < 0 || blk >= c.n_blocks || c.ref_count[blk] != 0;
       }
     }
-    __syncthreads();
     for (int i0 = 0; i0 < n; i0 += kSeqs) {
       const int i = i0 + t;
-      const int len = i < n ? c.seq_len[src[i]] : 0;
-      bad = bad || len < 0;  // marked: a source that is also new
+      const int len = i0 == 0 ? first_len : i < n ? c.seq_len[src[i]] : 0;
       int total;
-      ends[t] = block_scan(blocks_for(max(len, 0), c.bs), &total);
+      ends[t] = block_scan(blocks_for(len, c.bs), &total);
       __syncthreads();
       for (int e = t; e < total; e += kThreads) {
-        const int k = owner(ends, kSeqs, e);
-        const int blk = block_at(c, src[i0 + k], e - (k ? ends[k - 1] : 0));
+        const Place p = place_of(ends, e);
+        const int blk = block_at(c, src[i0 + p.k], p.col);
         bad = bad || blk < 0 || c.ref_count[blk] < 1;
       }
       __syncthreads();
     }
     bad = __syncthreads_or(bad);
-    if (bad || full)
-      for (int i = t; i < n; i += kThreads) c.seq_len[dst[i]] = 0;
-  } else {
-    bad = true;
   }
   if (bad || full) {
     if (t == 0) {
@@ -305,52 +384,70 @@ __global__ void __launch_bounds__(kThreads)
   int from = top - all;
   for (int i0 = 0; i0 < n; i0 += kSeqs) {
     const int i = i0 + t;
-    const int len = i < n ? c.seq_len[src[i]] : 0;
+    const int len = i0 == 0 ? first_len : i < n ? c.seq_len[src[i]] : 0;
     int total, fresh;
     ends[t] = block_scan(blocks_for(len, c.bs), &total);
     const int after = block_scan(len % c.bs ? 1 : 0, &fresh);
     part[t] = len % c.bs ? from + after - 1 : -1;  // where the stack has this one's block
     __syncthreads();
     for (int e = t; e < total; e += kThreads) {
-      const int k = owner(ends, kSeqs, e);
-      const int col = e - (k ? ends[k - 1] : 0);
+      const Place p = place_of(ends, e);
       int blk;
-      if (part[k] >= 0 && e == ends[k] - 1) {
-        blk = c.free_list[part[k]];
+      if (part[p.k] >= 0 && e == ends[p.k] - 1) {
+        blk = c.free_list[part[p.k]];
         c.ref_count[blk] = 1;
       } else {
-        blk = c.table[static_cast<size_t>(src[i0 + k]) * c.max_blocks + col];
+        blk = c.table[static_cast<size_t>(src[i0 + p.k]) * c.max_blocks + p.col];
         atomicAdd(&c.ref_count[blk], 1);
       }
-      c.table[static_cast<size_t>(dst[i0 + k]) * c.max_blocks + col] = blk;
+      c.table[static_cast<size_t>(dst[i0 + p.k]) * c.max_blocks + p.col] = blk;
     }
+    if (i < n) c.seq_len[dst[i]] = len;  // a dst is never a src
     from += fresh;
     __syncthreads();
   }
-  for (int i = t; i < n; i += kThreads) c.seq_len[dst[i]] = c.seq_len[src[i]];  // src is never a dst
   if (t == 0) *c.free_top = top - all;
 }
 
-constexpr int kCopyThreads = 128;
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 8;
 
-// One CTA: the started block of one new sequence, in one layer and head, of keys
-// (blockIdx.z 0) or values.
+// One CTA: the started block of one new sequence in one layer, all heads, keys and
+// values.
 __global__ void __launch_bounds__(kCopyThreads)
-    fork_copy_kernel(Cache c, const int32_t* src, const int32_t* dst) {
+    fork_copy_kernel(Cache c, int layer0, const int32_t* src, const int32_t* dst) {
   if (*c.err) return;  // refused
-  const int h = blockIdx.x % c.H, l = blockIdx.x / c.H;
-  const int s = src[blockIdx.y], d = dst[blockIdx.y];
+  const int l = layer0 + blockIdx.y;
+  const int s = src[blockIdx.x], d = dst[blockIdx.x];
   const int len = c.seq_len[d];
   const int rows = len % c.bs;
   if (rows == 0) return;
   const int from = block_at(c, s, len / c.bs), to = block_at(c, d, len / c.bs);
   if (from < 0 || to < 0) return;
-  const int vec = c.d / 16;
-  const uint4* x = reinterpret_cast<const uint4*>(c.pool[blockIdx.z]) + block_row(c, l, from, h) * vec;
-  uint4* y = reinterpret_cast<uint4*>(c.pool[blockIdx.z]) + block_row(c, l, to, h) * vec;
-  for (int i = threadIdx.x; i < rows * vec; i += kCopyThreads) y[i] = x[i];
-  if (threadIdx.x == 0)
-    c.scale[blockIdx.z][scale_at(c, l, to, h)] = c.scale[blockIdx.z][scale_at(c, l, from, h)];
+  const int vec = c.d / 16, head = rows * vec;  // 16-byte vectors of a row, of a head's rows
+  const size_t x0 = block_row(c, l, from, 0) * vec, y0 = block_row(c, l, to, 0) * vec;
+  const int stride = c.bs * vec;
+  for (int i = threadIdx.x; i < head; i += kCopyThreads) {
+    for (int k0 = 0; k0 < 2 * c.H; k0 += kCopyUnroll) {
+      uint4 v[kCopyUnroll];
+#pragma unroll
+      for (int k = 0; k < kCopyUnroll; ++k) {
+        const int hk = k0 + k, hh = hk < c.H ? hk : hk - c.H;
+        const uint4* pool = reinterpret_cast<const uint4*>(hk < c.H ? c.pool[0] : c.pool[1]);
+        if (hk < 2 * c.H) v[k] = pool[x0 + hh * stride + i];
+      }
+#pragma unroll
+      for (int k = 0; k < kCopyUnroll; ++k) {
+        const int hk = k0 + k, hh = hk < c.H ? hk : hk - c.H;
+        uint4* pool = reinterpret_cast<uint4*>(hk < c.H ? c.pool[0] : c.pool[1]);
+        if (hk < 2 * c.H) pool[y0 + hh * stride + i] = v[k];
+      }
+    }
+  }
+  for (int i = threadIdx.x; i < 2 * c.H; i += kCopyThreads) {
+    float* scale = i < c.H ? c.scale[0] : c.scale[1];
+    scale[scale_at(c, l, to, i % c.H)] = scale[scale_at(c, l, from, i % c.H)];
+  }
 }
 
 }  // namespace
@@ -369,11 +466,11 @@ cudaError_t launch_fork(const Cache& c, int n, const int32_t* src, const int32_t
                         cudaStream_t s) {
   fork_kernel<<<1, kThreads, 0, s>>>(c, n, src, dst);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  for (int i = 0; i < n; i += 65535)  // gridDim.y is at most 65535
-    fork_copy_kernel<<<dim3(c.L * c.H, min(65535, n - i), 2), kCopyThreads, 0, s>>>(c, src + i,
-                                                                                   dst + i);
-  return cudaGetLastError();
+  for (int l = 0; l < c.L && e == cudaSuccess; l += 65535) {  // gridDim.y is at most 65535
+    fork_copy_kernel<<<dim3(n, min(65535, c.L - l)), kCopyThreads, 0, s>>>(c, l, src, dst);
+    e = cudaGetLastError();
+  }
+  return e;
 }
 
 }  // namespace cache8

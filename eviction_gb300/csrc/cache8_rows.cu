@@ -96,11 +96,6 @@ __global__ void __launch_bounds__(32 * kWarps)
   const int i = start / c.bs + ib;
   if (nn == 0 || static_cast<long long>(i) * c.bs >= len) return;
   const int first = i * c.bs;
-  const int blk = block_at(c, b, i);
-  if (blk < 0) {
-    if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
-    return;
-  }
   const int lo = max(first, start), hi = min(len, first + c.bs);
   const Rows& src = blockIdx.y ? v_new : k_new;
   const uint16_t* x = src.at(static_cast<int>(l), b, h, lo - start);
@@ -115,6 +110,14 @@ __global__ void __launch_bounds__(32 * kWarps)
     const int idx = lane + 32 * s;
     keep[s] = idx < total ? load(idx) : make_uint4(0, 0, 0, 0);
   }
+  // (the block and its old scale are looked up while the rows are on their way)
+  const int blk = block_at(c, b, i);
+  if (blk < 0) {
+    if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
+    return;
+  }
+  float* scale_ptr = c.scale[blockIdx.y] + scale_at(c, static_cast<int>(l), blk, h);
+  const float old = lo > first ? *scale_ptr : 0.f;
 #pragma unroll
   for (int s = 0; s < kKeep; ++s) m = max_abs8(keep[s], m);
   for (int idx = lane + 32 * kKeep; idx < total; idx += 32) m = max_abs8(load(idx), m);
@@ -126,10 +129,8 @@ __global__ void __launch_bounds__(32 * kWarps)
     m = warp_max_half(m);
   }
   float scale = exp2_int(scale_exp<FMT>(__uint_as_float(m << 16)));
-  float* scale_ptr = c.scale[blockIdx.y] + scale_at(c, static_cast<int>(l), blk, h);
   uint8_t* rows = c.pool[blockIdx.y] + block_row(c, static_cast<int>(l), blk, h) * D;
   if (lo > first) {  // older rows: the scale only grows, and they follow it
-    const float old = *scale_ptr;
     if (old >= scale) {
       scale = old;
     } else {
@@ -223,29 +224,52 @@ __global__ void __launch_bounds__(kGatherThreads)
 
 // ---- compact ----
 
-constexpr int kKeepCodes = 4;  // 16-byte chunks of codes a lane keeps
+constexpr int kKeepRows = 16;  // rows whose codes a warp keeps in registers
 
-// Largest finite |code| of 16.
+// Bytes 2 k and 2 k + 1 as two signed 16-bit integers.
+template <int K>
+__device__ __forceinline__ uint32_t signed_pair(uint32_t four) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(four), "n"(K == 0 ? 0x9180 : 0xb3a2));
+  return r;
+}
+
+// Largest |code| of 16 finite ones: integers order e4m3 magnitudes as well.
 template <int FMT>
 __device__ __forceinline__ float max_code16(uint4 v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float m = 0.f;
+  if constexpr (FMT == KVC_CACHE8_E4M3) {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(__vmaxu2(m, w[i] & 0x007f007fu), (w[i] >> 8) & 0x007f007fu);
     float x[4];
-    decode4<FMT>(w[i], x);
+    decode4<FMT>(max(m & 0xffffu, m >> 16), x);
+    return x[0];
+  } else {
+    uint32_t hi = 0, lo = 0;  // pairs of 16 bits: largest and smallest
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(x[j]));  // a NaN code does not count
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = signed_pair<0>(w[i]), b = signed_pair<1>(w[i]);
+      hi = __vmaxs2(hi, __vmaxs2(a, b));
+      lo = __vmins2(lo, __vmins2(a, b));
+    }
+    const int most = max(static_cast<int16_t>(hi & 0xffffu), static_cast<int16_t>(hi >> 16));
+    const int least = min(static_cast<int16_t>(lo & 0xffffu), static_cast<int16_t>(lo >> 16));
+    return static_cast<float>(max(most, -least));
   }
-  return m;
 }
 
-// One warp: one new block of one head, keys (blockIdx.y 0) or values.
+// One warp: one new block of one head, keys and values.  A lane looks up a row (its
+// kept index, its block, the scales), which the warp then shares: three loads that wait
+// for one another before 4 KB are on their way.
 template <int D, int FROM, int TO>
 __global__ void __launch_bounds__(32 * kWarps)
     compact_kernel(Cache c, Cache to, CompactArgs a, int per_unit) {
-  constexpr int CH = D / 16;
+  constexpr int CH = D / 16;                     // 16-byte chunks of a row
+  constexpr int RPI = 32 / CH;                   // rows of one load of the warp
+  constexpr int KEEP = kKeepRows / RPI;
   const int lane = threadIdx.x % 32;
+  const int ch = lane % CH;
   const long long task = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
   const long long u = task / per_unit;
   const int jb = static_cast<int>(task % per_unit);
@@ -253,6 +277,11 @@ __global__ void __launch_bounds__(32 * kWarps)
   const int b = static_cast<int>((u / c.H) % c.B);
   const int l = static_cast<int>(u / (static_cast<long long>(c.H) * c.B));
   if (l >= c.L) return;
+  const int j0 = jb * to.bs;
+  const int32_t* kept = a.kept + u * a.budget;
+  // (read before the checks below: the index arrays do not depend on them)
+  int slot = j0 + lane < a.budget && lane < to.bs ? kept[j0 + lane] : -1;
+  const int new_blk = block_at(to, b, jb);
   bool bad = false;
   const int len = length_of(c, b, &bad);
   const int nk = a.n_kept[u];
@@ -261,77 +290,108 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
     return;
   }
-  const int j0 = jb * to.bs;
   const int pad = a.pad[b];
-  const int32_t* kept = a.kept + u * a.budget;
-  if (a.credit_out && blockIdx.y == 0) {
-    for (int j = j0 + lane; j < min(j0 + to.bs, a.budget); j += 32) {
-      const int slot = j < nk ? kept[j] : -1;
-      a.credit_out[u * a.budget + j] =
-          slot >= 0 && slot < a.T ? a.credit_post[u * a.T + slot] : 0.f;
-    }
-  }
   const int rows = min(nk - j0, to.bs);
-  if (rows <= 0) return;
-  const int new_blk = block_at(to, b, jb);
-  if (new_blk < 0) {
-    if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
-    return;
-  }
-  const uint4* pool = reinterpret_cast<const uint4*>(c.pool[blockIdx.y]);
-  const float* scales = c.scale[blockIdx.y];
-  // a chunk of row r and its scale; zeros for an index outside the sequence
-  auto load = [&](int idx, uint4* v, float* s) {
-    const int slot = kept[j0 + idx / CH];
+  // the row of 32 that this lane looks after: its place in the pools (rows of d codes
+  // from the layer's first, of this head) and its scales; -1 outside the sequence
+  const size_t base = block_row(c, l, 0, h);
+  const size_t scale_base = scale_at(c, l, 0, h);
+  int row;
+  float ks, vs;
+  auto look_up = [&](int r0) {
+    const int r = r0 + lane;
+    row = -1;
+    ks = vs = 0.f;
+    if (r >= rows) return;
     const long long pos = static_cast<long long>(slot) - pad;
-    *v = make_uint4(0, 0, 0, 0);
-    *s = 0.f;
-    if (pos < 0 || pos >= len || slot < 0 || slot >= a.T) {
-      bad = true;
-      return;
-    }
-    const int blk = block_at(c, b, static_cast<int>(pos) / c.bs);
+    const bool in = pos >= 0 && pos < len && slot >= 0 && slot < a.T;
+    const int blk = in ? block_at(c, b, static_cast<int>(pos) / c.bs) : -1;
     if (blk < 0) {
       bad = true;
       return;
     }
-    *v = __ldg(pool + (block_row(c, l, blk, h) + static_cast<int>(pos) % c.bs) * CH + idx % CH);
-    *s = __ldg(scales + scale_at(c, l, blk, h));
+    row = blk * c.H * c.bs + static_cast<int>(pos) % c.bs;  // below 2^31: checked on the host
+    const size_t sc = scale_base + static_cast<size_t>(blk) * c.H;
+    ks = __ldg(c.scale[0] + sc);
+    vs = __ldg(c.scale[1] + sc);
   };
-  const int total = rows * CH;
-  uint4 keep[kKeepCodes];
-  float ks[kKeepCodes];
-  float m = 0.f;
+  look_up(0);
+  if (a.credit_out) {
+    for (int j = j0 + lane; j < min(j0 + to.bs, a.budget); j += 32) {
+      const int s = j < nk ? (j < j0 + 32 ? slot : kept[j]) : -1;
+      a.credit_out[u * a.budget + j] = s >= 0 && s < a.T ? a.credit_post[u * a.T + s] : 0.f;
+    }
+  }
+  if (rows <= 0) return;
+  if (new_blk < 0) {
+    if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
+    return;
+  }
+  // chunk ch of row r (r0 + 0..31 are looked up) of pool w
+  auto load = [&](int w, int r) {
+    const int from = __shfl_sync(0xffffffffu, row, r % 32);
+    return from >= 0 ? __ldg(reinterpret_cast<const uint4*>(c.pool[w]) + (base + from) * CH + ch)
+                     : make_uint4(0, 0, 0, 0);
+  };
+  uint4 kk[KEEP], kv[KEEP];
 #pragma unroll
-  for (int s = 0; s < kKeepCodes; ++s) {
-    const int idx = lane + 32 * s;
-    keep[s] = make_uint4(0, 0, 0, 0);
-    ks[s] = 0.f;
-    if (idx < total) load(idx, &keep[s], &ks[s]);
-  }
+  for (int i = 0; i < KEEP; ++i) kk[i] = load(0, i * RPI + lane / CH);
 #pragma unroll
-  for (int s = 0; s < kKeepCodes; ++s) m = fmaxf(m, max_code16<FROM>(keep[s]) * ks[s]);
-  for (int idx = lane + 32 * kKeepCodes; idx < total; idx += 32) {
-    uint4 v;
-    float s;
-    load(idx, &v, &s);
-    m = fmaxf(m, max_code16<FROM>(v) * s);
-  }
-  const float scale = exp2_int(scale_exp<TO>(warp_max(m)));
-  const float inv = 1.f / scale;  // exact
-  uint4* out = reinterpret_cast<uint4*>(to.pool[blockIdx.y]) + block_row(to, l, new_blk, h) * CH;
+  for (int i = 0; i < KEEP; ++i) kv[i] = load(1, i * RPI + lane / CH);
+  float km = 0.f, vm = 0.f;
 #pragma unroll
-  for (int s = 0; s < kKeepCodes; ++s) {
-    const int idx = lane + 32 * s;
-    if (idx < total) out[idx] = recode16<FROM, TO>(keep[s], ks[s] * inv);
+  for (int i = 0; i < KEEP; ++i) {
+    const int r = i * RPI + lane / CH;
+    km = fmaxf(km, max_code16<FROM>(kk[i]) * __shfl_sync(0xffffffffu, ks, r));
+    vm = fmaxf(vm, max_code16<FROM>(kv[i]) * __shfl_sync(0xffffffffu, vs, r));
   }
-  for (int idx = lane + 32 * kKeepCodes; idx < total; idx += 32) {
-    uint4 v;
-    float s;
-    load(idx, &v, &s);
-    out[idx] = recode16<FROM, TO>(v, s * inv);
+  // the other rows of larger blocks (read again below, from L2)
+  auto more = [&](auto f) {
+    for (int r0 = 0; r0 < rows; r0 += 32) {
+      if (r0 > 0) {
+        slot = r0 + lane < rows ? kept[j0 + r0 + lane] : -1;
+        look_up(r0);
+      }
+      for (int r = r0 == 0 ? kKeepRows : r0; r < min(rows, r0 + 32); r += RPI) {
+        const int mine = r + lane / CH;
+        const uint4 k = load(0, mine), v = load(1, mine);
+        f(mine, k, v, __shfl_sync(0xffffffffu, ks, mine % 32), __shfl_sync(0xffffffffu, vs, mine % 32));
+      }
+    }
+  };
+  if (rows > kKeepRows)
+    more([&](int, uint4 k, uint4 v, float s, float t) {
+      km = fmaxf(km, max_code16<FROM>(k) * s);
+      vm = fmaxf(vm, max_code16<FROM>(v) * t);
+    });
+  if (rows > 32) {  // back to the first rows' scales
+    slot = kept[j0 + lane];
+    look_up(0);
   }
-  if (lane == 0) to.scale[blockIdx.y][scale_at(to, l, new_blk, h)] = scale;
+  const float k_scale = exp2_int(scale_exp<TO>(warp_max(km)));
+  const float v_scale = exp2_int(scale_exp<TO>(warp_max(vm)));
+  const float k_inv = 1.f / k_scale, v_inv = 1.f / v_scale;  // exact
+  const size_t out = block_row(to, l, new_blk, h) * CH + ch;
+  uint4* ko = reinterpret_cast<uint4*>(to.pool[0]) + out;
+  uint4* vo = reinterpret_cast<uint4*>(to.pool[1]) + out;
+  auto store = [&](int r, uint4 k, uint4 v, float s, float t) {
+    if (r >= rows) return;
+    // (a row whose scale stays keeps its codes)
+    ko[r * CH] = FROM == TO && s == k_scale ? k : recode16<FROM, TO>(k, s * k_inv);
+    vo[r * CH] = FROM == TO && t == v_scale ? v : recode16<FROM, TO>(v, t * v_inv);
+  };
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    const int r = i * RPI + lane / CH;
+    const float s = __shfl_sync(0xffffffffu, ks, r), t = __shfl_sync(0xffffffffu, vs, r);
+    store(r, kk[i], kv[i], s, t);
+  }
+  if (rows > kKeepRows) more(store);
+  if (lane == 0) {
+    const size_t sc = scale_at(to, l, new_blk, h);
+    to.scale[0][sc] = k_scale;
+    to.scale[1][sc] = v_scale;
+  }
   if (bad) report(c, KVC_STATUS_BAD_INDEX);
 }
 
@@ -369,7 +429,7 @@ template <int D>
 static cudaError_t launch_compact_d(const Cache& c, int from, const Cache& to, int to_format,
                                     const CompactArgs& a, cudaStream_t s) {
   const int per_unit = (a.budget + to.bs - 1) / to.bs;
-  const dim3 grid(ctas(static_cast<long long>(c.L) * c.B * c.H * per_unit), 2);
+  const int grid = ctas(static_cast<long long>(c.L) * c.B * c.H * per_unit);
   constexpr int E = KVC_CACHE8_E4M3, I = KVC_CACHE8_INT8;
   auto* kernel = from == E ? (to_format == E ? compact_kernel<D, E, E> : compact_kernel<D, E, I>)
                            : (to_format == E ? compact_kernel<D, I, E> : compact_kernel<D, I, I>);
