@@ -186,9 +186,9 @@ __device__ bool listed_twice(const Cache& c, int n, const int32_t* seqs, const i
   return __syncthreads_or(twice);
 }
 
-// Calls f(key, number, entry) for every table entry of the listed sequences, 0 <=
-// number < kKeep for a thread's first ones; keys ascend with list and block order, and
-// are -1 for a thread without an entry.  Whole CTA; `ends` is scratch of kSeqs ints.
+// Calls f(key, entry) for every table entry of the listed sequences; keys ascend with
+// list and block order, and are -1 for a thread without an entry.  Whole CTA; `ends`
+// is scratch of kSeqs ints.
 template <class F>
 __device__ void for_entries(const Cache& c, int n, const int32_t* seqs, int* ends, F f) {
   for (int i0 = 0; i0 < n; i0 += kSeqs) {
@@ -198,32 +198,24 @@ __device__ void for_entries(const Cache& c, int n, const int32_t* seqs, int* end
     __syncthreads();
     ends[threadIdx.x] = block_scan(held, &total);
     __syncthreads();
-    // (f may hold barriers: every thread calls it, at one place)
-    auto one = [&](int e, int number) {
+    for (int e0 = 0; e0 < total; e0 += kThreads) {
+      // (f may hold barriers: every thread calls it, at one place)
       int key = -1;
       int32_t* at = nullptr;
-      if (e < total) {
-        const Place p = place_of(ends, e);
+      if (e0 + static_cast<int>(threadIdx.x) < total) {
+        const Place p = place_of(ends, e0 + threadIdx.x);
         key = (i0 + p.k) * c.max_blocks + p.col;
         at = c.table + static_cast<size_t>(seqs[i0 + p.k]) * c.max_blocks + p.col;
       }
-      f(key, number, at);
-    };
-    int e0 = 0;
-    if (i0 == 0) {
-#pragma unroll
-      for (int k = 0; k < kKeep; ++k)
-        if (k * kThreads < total) one(k * kThreads + threadIdx.x, k);
-      e0 = kKeep * kThreads;
+      f(key, at);
     }
-    for (; e0 < total; e0 += kThreads) one(e0 + threadIdx.x, kKeep);
   }
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads, 1) free_kernel(Cache c, int n, const int32_t* seqs) {
-  __shared__ int ends[kSeqs];
-  __shared__ uint32_t marks[kMarkBits / 32];
+// Any number of sequences and entries; the entries are read again in each step.
+__device__ __noinline__ void free_many(const Cache& c, int n, const int32_t* seqs, int* ends,
+                                       uint32_t* marks) {
   const int t = threadIdx.x;
   const int top = *c.free_top;
   bool bad = top < 0 || top > c.n_blocks;
@@ -238,32 +230,19 @@ __global__ void __launch_bounds__(kThreads, 1) free_kernel(Cache c, int n, const
     if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
     return;
   }
-  int kept[kKeep];   // this thread's first entries (blocks)
-  for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
-    if (key < 0) return;
-    const int blk = *at;
-    if (number < kKeep) kept[number] = blk;
-    bad = bad || blk < 0 || blk >= c.n_blocks;
+  for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
+    if (key >= 0) bad = bad || *at < 0 || *at >= c.n_blocks;
   });
   if (__syncthreads_or(bad)) {
     if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
     return;
   }
-  auto block = [&](int number, const int32_t* at) { return number < kKeep ? kept[number] : *at; };
-  // one holder fewer; the count before says whether the block is free now (1), was
-  // shared (more), or had more holders than were counted (less)
-  int before[kKeep];
-  bool shared = false;
-  for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
-    if (key < 0) return;
-    const int was = atomicSub(&c.ref_count[block(number, at)], 1);
-    if (number < kKeep) before[number] = was;
-    bad = bad || was < 1;
-    shared = shared || was > 1 || number >= kKeep;
+  for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
+    if (key >= 0) bad = atomicSub(&c.ref_count[*at], 1) < 1 || bad;
   });
   auto put_back = [&] {
-    for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
-      if (key >= 0) atomicAdd(&c.ref_count[block(number, at)], 1);
+    for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
+      if (key >= 0) atomicAdd(&c.ref_count[*at], 1);
     });
     if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
   };
@@ -271,56 +250,145 @@ __global__ void __launch_bounds__(kThreads, 1) free_kernel(Cache c, int n, const
     put_back();
     return;
   }
-  // An entry whose block nobody holds now pushes it: the last one in the list, where
-  // several have the same block.  (There is one entry alone if none was shared.)
-  const bool any_shared = __syncthreads_or(shared);
-  if (any_shared) {
-    for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
-      if (key < 0) return;
-      int* count = &c.ref_count[block(number, at)];
-      if (*count <= 0) atomicMin(count, -1 - key);  // zero, or another entry's mark
-    });
-  }
-  auto pushes = [&](int key, int number, const int32_t* at) {
-    if (key < 0) return false;
-    return any_shared ? c.ref_count[block(number, at)] == -1 - key : before[number] == 1;
-  };
+  // a block that nobody holds: its count becomes -1 - (its last key in the list)
+  for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
+    if (key >= 0 && __ldcg(&c.ref_count[*at]) <= 0) atomicMin(&c.ref_count[*at], -1 - key);
+  });
   int mine = 0, all;
-  for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
-    if (number < kKeep) {
-      const bool push = pushes(key, number, at);
-      before[number] = push;  // (known from here on)
-      mine += push;
-    } else {
-      mine += pushes(key, number, at);
-    }
+  for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
+    if (key >= 0) mine += __ldcg(&c.ref_count[*at]) == -1 - key;
   });
   block_scan(mine, &all);
   if (all > c.n_blocks - top) {  // more blocks than there are: the stack was wrong
-    for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
-      if (key >= 0 && c.ref_count[block(number, at)] < 0) c.ref_count[block(number, at)] = 0;
+    for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
+      if (key >= 0 && __ldcg(&c.ref_count[*at]) < 0) c.ref_count[*at] = 0;
     });
     put_back();
     return;
   }
   int to = top;
-  for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
-    const bool push = number < kKeep ? key >= 0 && before[number] : pushes(key, number, at);
+  for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
+    const bool push = key >= 0 && __ldcg(&c.ref_count[*at]) == -1 - key;
     int total;
     const int place = to + block_scan(push, &total) - 1;
-    if (push) c.free_list[place] = block(number, at);
+    if (push) c.free_list[place] = *at;
     to += total;
   });
-  for_entries(c, n, seqs, ends, [&](int key, int number, int32_t* at) {
+  for_entries(c, n, seqs, ends, [&](int key, int32_t* at) {
     if (key < 0) return;
-    if (any_shared) {
-      int* count = &c.ref_count[block(number, at)];
-      if (*count < 0) *count = 0;
-    }
+    if (__ldcg(&c.ref_count[*at]) < 0) c.ref_count[*at] = 0;
     *at = -1;
   });
   for (int i = t; i < n; i += kThreads) c.seq_len[seqs[i]] = 0;
   if (t == 0) *c.free_top = to;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) free_kernel(Cache c, int n, const int32_t* seqs) {
+  __shared__ int ends[kSeqs], numbers[kSeqs];
+  __shared__ uint32_t marks[kMarkBits / 32];
+  if (n > kSeqs || c.B > kMarkBits) {
+    free_many(c, n, seqs, ends, marks);
+    return;
+  }
+  // one thread, one sequence; then one thread, up to kKeep entries, in registers
+  const int t = threadIdx.x;
+  const int s = t < n ? seqs[t] : 0;
+  const int top = *c.free_top;
+  for (int i = t; i < (c.B + 31) / 32; i += kThreads) marks[i] = 0;
+  bool bad = top < 0 || top > c.n_blocks || s < 0 || s >= c.B;
+  const int len = t < n && !bad ? length_of(c, s, &bad) : 0;
+  numbers[t] = s;
+  __syncthreads();
+  if (t < n && !bad) bad = atomicOr(&marks[s / 32], 1u << (s % 32)) >> (s % 32) & 1u;
+  int total;
+  ends[t] = block_scan(blocks_for(len, c.bs), &total);
+  if (__syncthreads_or(bad)) {
+    if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
+    return;
+  }
+  if (total > kKeep * kThreads) {
+    __syncthreads();
+    free_many(c, n, seqs, ends, marks);
+    return;
+  }
+  int at[kKeep], key[kKeep], blk[kKeep], was[kKeep];
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    key[i] = -1;
+    if (t + i * kThreads < total) {
+      const Place p = place_of(ends, t + i * kThreads);
+      at[i] = numbers[p.k] * c.max_blocks + p.col;  // below 2^31: checked on the host
+      key[i] = p.k * c.max_blocks + p.col;
+      blk[i] = c.table[at[i]];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (key[i] >= 0) bad = bad || blk[i] < 0 || blk[i] >= c.n_blocks;
+  if (__syncthreads_or(bad)) {
+    if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
+    return;
+  }
+  // one holder fewer; the count before says whether the block is free now (1), was
+  // shared (more), or had more holders than were counted (less)
+  bool shared = false;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) was[i] = key[i] >= 0 ? atomicSub(&c.ref_count[blk[i]], 1) : 2;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    bad = bad || was[i] < 1;
+    shared = shared || (key[i] >= 0 && was[i] > 1);
+  }
+  bad = __syncthreads_or(bad);
+  // An entry whose block nobody holds now pushes it: the last one in the list, where
+  // several of the list shared it (an entry that saw a count above 1 knows).
+  if (!bad && __syncthreads_or(shared)) {
+    bool twice = false;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      if (key[i] >= 0 && was[i] > 1) twice = twice || __ldcg(&c.ref_count[blk[i]]) == 0;
+    if (__syncthreads_or(twice)) {
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if (key[i] >= 0 && __ldcg(&c.ref_count[blk[i]]) <= 0) atomicMin(&c.ref_count[blk[i]], -1 - key[i]);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if (key[i] >= 0) was[i] = __ldcg(&c.ref_count[blk[i]]) == -1 - key[i] ? 1 : 2;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if (was[i] == 1) c.ref_count[blk[i]] = 0;
+      __syncthreads();
+    }
+  }
+  // places on the stack: entries i * kThreads + t in this order, two counts at a time
+  int push[kKeep], place[kKeep], all = 0;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) push[i] = key[i] >= 0 && was[i] == 1;
+#pragma unroll
+  for (int i = 0; i < kKeep; i += 2) {
+    int both;
+    const int incl = block_scan(push[i] | push[i + 1] << 16, &both);
+    place[i] = all + (incl & 0xffff) - 1;
+    all += both & 0xffff;
+    place[i + 1] = all + (incl >> 16) - 1;
+    all += both >> 16;
+  }
+  if (bad || all > c.n_blocks - top) {  // a stack with more blocks than there are was wrong
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      if (key[i] >= 0) atomicAdd(&c.ref_count[blk[i]], 1);
+    if (t == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    if (push[i]) c.free_list[top + place[i]] = blk[i];
+    if (key[i] >= 0) c.table[at[i]] = -1;
+  }
+  if (t < n) c.seq_len[s] = 0;
+  if (t == 0) *c.free_top = top + all;
 }
 
 // ---- fork ----
@@ -351,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // a new sequence listed twice, or also as a source (which can only be an empty one)
   bad = __syncthreads_or(bad);
   if (!bad) bad = listed_twice(c, n, dst, src, marks);
+  int kept[kKeep];  // blocks of this thread's first entries
   if (!bad) {
     full = all > top;
     if (!full) {
@@ -365,7 +434,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       int total;
       ends[t] = block_scan(blocks_for(len, c.bs), &total);
       __syncthreads();
-      for (int e = t; e < total; e += kThreads) {
+      if (i0 == 0) {
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k) {
+          kept[k] = -1;
+          if (t + k * kThreads < total) {
+            const Place p = place_of(ends, t + k * kThreads);
+            kept[k] = block_at(c, src[p.k], p.col);
+            bad = bad || kept[k] < 0;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kKeep; ++k)
+          if (kept[k] >= 0) bad = c.ref_count[kept[k]] < 1 || bad;
+      }
+      for (int e = i0 == 0 ? t + kKeep * kThreads : t; e < total; e += kThreads) {
         const Place p = place_of(ends, e);
         const int blk = block_at(c, src[i0 + p.k], p.col);
         bad = bad || blk < 0 || c.ref_count[blk] < 1;
@@ -390,18 +473,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int after = block_scan(len % c.bs ? 1 : 0, &fresh);
     part[t] = len % c.bs ? from + after - 1 : -1;  // where the stack has this one's block
     __syncthreads();
-    for (int e = t; e < total; e += kThreads) {
+    auto give = [&](int e, int blk) {  // entry e: a source's block, or a new one for its started one
       const Place p = place_of(ends, e);
-      int blk;
       if (part[p.k] >= 0 && e == ends[p.k] - 1) {
         blk = c.free_list[part[p.k]];
         c.ref_count[blk] = 1;
       } else {
-        blk = c.table[static_cast<size_t>(src[i0 + p.k]) * c.max_blocks + p.col];
+        if (blk < 0) blk = c.table[static_cast<size_t>(src[i0 + p.k]) * c.max_blocks + p.col];
         atomicAdd(&c.ref_count[blk], 1);
       }
       c.table[static_cast<size_t>(dst[i0 + p.k]) * c.max_blocks + p.col] = blk;
+    };
+    if (i0 == 0) {
+#pragma unroll
+      for (int k = 0; k < kKeep; ++k)
+        if (t + k * kThreads < total) give(t + k * kThreads, kept[k]);
     }
+    for (int e = i0 == 0 ? t + kKeep * kThreads : t; e < total; e += kThreads) give(e, -1);
     if (i < n) c.seq_len[dst[i]] = len;  // a dst is never a src
     from += fresh;
     __syncthreads();

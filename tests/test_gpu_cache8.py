@@ -472,6 +472,26 @@ def test_pages_match_model(bs, B, M):
     assert {("grow", 0), ("fork", 0), ("free", 0)} <= seen
 
 
+@pytest.mark.parametrize("B,M,bs", [(40, 300, 1), (1300, 6, 2)])
+def test_pages_of_large_calls(B, M, bs):
+    """More entries than a thread keeps, more sequences than threads; shared blocks freed together."""
+    p = Pair(1, B, 1, 64, bs, M, "int8", n_blocks=B * M // 2 + 50, seed=B)
+    half = B // 2
+    lens = np.zeros(B, int)
+    lens[:half] = p.rng.integers(0, M * bs // 2, half)
+    assert p.grow(lens) == 0
+    src, dst = p.rng.integers(0, half, B - half), half + p.rng.permutation(B - half)
+    for want, call, args in ((p.ref.fork, p.h.cache8_fork, (src, dst)),
+                             (p.ref.free, p.h.cache8_free, (p.rng.permutation(B)[:B - 3],)),
+                             (p.ref.free, p.h.cache8_free, (np.r_[p.rng.permutation(B), 5],)),
+                             (p.ref.free, p.h.cache8_free, (p.rng.permutation(B),))):
+        code = want(*args)
+        call(p.c, *[_ints(a) for a in args])
+        assert p.h.device_status() == code
+        p.same()
+    assert p.ref.top == p.ref.N
+
+
 def test_pages_refusals_change_nothing():
     p = Pair(1, 6, 1, 64, 16, 4, "e4m3", n_blocks=12)
     p.fill([20, 40, 0, 0, 16, 0])
