@@ -48,7 +48,7 @@ struct CompactArgs {
 cudaError_t launch_grow(const Cache& c, const int32_t* n_new, cudaStream_t s);
 cudaError_t launch_free(const Cache& c, int n, const int32_t* seqs, cudaStream_t s);
 cudaError_t launch_fork(const Cache& c, int n, const int32_t* src, const int32_t* dst,
-                        cudaStream_t s);
+                        int num_sms, cudaStream_t s);
 cudaError_t launch_append(const Cache& c, int format, const Rows& k, const Rows& v, int n,
                           const int32_t* n_new, cudaStream_t s);
 cudaError_t launch_gather(const Cache& c, int format, int T, uint16_t* k_out, uint16_t* v_out,

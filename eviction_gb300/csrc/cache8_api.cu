@@ -260,7 +260,7 @@ int kvc_cache8_fork(kvc_handle* h, const kvc_cache8* c, int n, const int32_t* sr
     KVC_REQUIRE_INTS(src);
     KVC_REQUIRE_INTS(dst);
     return run(h, kvc::kKernelCache8Fork, "cache8 fork", stream, [&](cudaStream_t s) {
-      return kvc::cache8::launch_fork(view(h, *c), n, src, dst, s);
+      return kvc::cache8::launch_fork(view(h, *c), n, src, dst, h->num_sms, s);
     });
   });
 }

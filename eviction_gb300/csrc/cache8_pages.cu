@@ -12,9 +12,8 @@
 // reproducible: counts go through atomics, whose order does not matter for
 // integers, and places come from prefix sums.
 //
-// fork copies the rows of the started blocks in a second launch over all layers
-// (one CTA per new sequence and layer), which skips its work when the first one
-// refused.
+// fork copies the rows of the started blocks in a second launch over all layers,
+// which skips its work when the first one refused.
 #include "cache8.cuh"
 
 namespace kvc {
@@ -500,41 +499,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;
 
-// One CTA: the started block of one new sequence in one layer, all heads, keys and
-// values.
-__global__ void __launch_bounds__(kCopyThreads)
-    fork_copy_kernel(Cache c, int layer0, const int32_t* src, const int32_t* dst) {
-  if (*c.err) return;  // refused
-  const int l = layer0 + blockIdx.y;
+// One CTA: the started block of one new sequence in some layers, all heads, keys and
+// values.  (Finding the blocks takes four loads that wait for one another: so many
+// layers a CTA that all are resident at once.)
+__global__ void __launch_bounds__(kCopyThreads, 3)
+    fork_copy_kernel(Cache c, int layers, const int32_t* src, const int32_t* dst) {
   const int s = src[blockIdx.x], d = dst[blockIdx.x];
+  if (*c.err) return;  // refused: the numbers may be out of range
   const int len = c.seq_len[d];
   const int rows = len % c.bs;
   if (rows == 0) return;
   const int from = block_at(c, s, len / c.bs), to = block_at(c, d, len / c.bs);
   if (from < 0 || to < 0) return;
   const int vec = c.d / 16, head = rows * vec;  // 16-byte vectors of a row, of a head's rows
-  const size_t x0 = block_row(c, l, from, 0) * vec, y0 = block_row(c, l, to, 0) * vec;
   const int stride = c.bs * vec;
-  for (int i = threadIdx.x; i < head; i += kCopyThreads) {
-    for (int k0 = 0; k0 < 2 * c.H; k0 += kCopyUnroll) {
-      uint4 v[kCopyUnroll];
-#pragma unroll
-      for (int k = 0; k < kCopyUnroll; ++k) {
-        const int hk = k0 + k, hh = hk < c.H ? hk : hk - c.H;
-        const uint4* pool = reinterpret_cast<const uint4*>(hk < c.H ? c.pool[0] : c.pool[1]);
-        if (hk < 2 * c.H) v[k] = pool[x0 + hh * stride + i];
-      }
-#pragma unroll
-      for (int k = 0; k < kCopyUnroll; ++k) {
-        const int hk = k0 + k, hh = hk < c.H ? hk : hk - c.H;
-        uint4* pool = reinterpret_cast<uint4*>(hk < c.H ? c.pool[0] : c.pool[1]);
-        if (hk < 2 * c.H) pool[y0 + hh * stride + i] = v[k];
+  const int l0 = blockIdx.y * layers, l1 = min(c.L, l0 + layers);
+  for (int l = l0; l < l1; ++l) {
+    const size_t x0 = block_row(c, l, from, 0) * vec, y0 = block_row(c, l, to, 0) * vec;
+    for (int i = threadIdx.x; i < head; i += kCopyThreads) {
+      for (int k0 = 0; k0 < 2 * c.H; k0 += kCopyUnroll) {
+        uint4 v[kCopyUnroll];
+  #pragma unroll
+        for (int k = 0; k < kCopyUnroll; ++k) {
+          const int hk = k0 + k, hh = hk < c.H ? hk : hk - c.H;
+          const uint4* pool = reinterpret_cast<const uint4*>(hk < c.H ? c.pool[0] : c.pool[1]);
+          if (hk < 2 * c.H) v[k] = pool[x0 + hh * stride + i];
+        }
+  #pragma unroll
+        for (int k = 0; k < kCopyUnroll; ++k) {
+          const int hk = k0 + k, hh = hk < c.H ? hk : hk - c.H;
+          uint4* pool = reinterpret_cast<uint4*>(hk < c.H ? c.pool[0] : c.pool[1]);
+          if (hk < 2 * c.H) pool[y0 + hh * stride + i] = v[k];
+        }
       }
     }
-  }
-  for (int i = threadIdx.x; i < 2 * c.H; i += kCopyThreads) {
-    float* scale = i < c.H ? c.scale[0] : c.scale[1];
-    scale[scale_at(c, l, to, i % c.H)] = scale[scale_at(c, l, from, i % c.H)];
+    for (int i = threadIdx.x; i < 2 * c.H; i += kCopyThreads) {
+      float* scale = i < c.H ? c.scale[0] : c.scale[1];
+      scale[scale_at(c, l, to, i % c.H)] = scale[scale_at(c, l, from, i % c.H)];
+    }
   }
 }
 
@@ -551,14 +553,15 @@ cudaError_t launch_free(const Cache& c, int n, const int32_t* seqs, cudaStream_t
 }
 
 cudaError_t launch_fork(const Cache& c, int n, const int32_t* src, const int32_t* dst,
-                        cudaStream_t s) {
+                        int num_sms, cudaStream_t s) {
   fork_kernel<<<1, kThreads, 0, s>>>(c, n, src, dst);
   cudaError_t e = cudaGetLastError();
-  for (int l = 0; l < c.L && e == cudaSuccess; l += 65535) {  // gridDim.y is at most 65535
-    fork_copy_kernel<<<dim3(n, min(65535, c.L - l)), kCopyThreads, 0, s>>>(c, l, src, dst);
-    e = cudaGetLastError();
-  }
-  return e;
+  if (e != cudaSuccess) return e;
+  // three CTAs an SM, and gridDim.y is at most 65535
+  const long long share = static_cast<long long>(n) * c.L / (3 * num_sms);
+  const int layers = static_cast<int>(max(max(share, static_cast<long long>(c.L) / 65535 + 1), 1ll));
+  fork_copy_kernel<<<dim3(n, (c.L + layers - 1) / layers), kCopyThreads, 0, s>>>(c, layers, src, dst);
+  return cudaGetLastError();
 }
 
 }  // namespace cache8

@@ -76,14 +76,13 @@ __global__ void __launch_bounds__(32 * kWarps)
     append_kernel(Cache c, Rows k_new, Rows v_new, int n, int per_seq, const int32_t* n_new) {
   constexpr int CH = D / 8;  // 16-byte chunks of a bf16 row
   const int lane = threadIdx.x % 32;
-  const long long task = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
+  const uint32_t task = blockIdx.x * kWarps + threadIdx.x / 32;
   // heads fastest: the rows of a token-major source then lie side by side
-  const int h = static_cast<int>(task % c.H);
-  const long long t1 = task / c.H;
-  const int ib = static_cast<int>(t1 % per_seq);
-  const long long t2 = t1 / per_seq;
-  const int b = static_cast<int>(t2 % c.B);
-  const long long l = t2 / c.B;
+  const int h = task % c.H;
+  const uint32_t t1 = task / c.H;
+  const int ib = t1 % per_seq;
+  const uint32_t t2 = t1 / per_seq;
+  const int b = t2 % c.B, l = t2 / c.B;
   if (l >= c.L) return;
   const int nn = n_new[b];
   bool bad = false;
@@ -97,11 +96,12 @@ __global__ void __launch_bounds__(32 * kWarps)
   if (nn == 0 || static_cast<long long>(i) * c.bs >= len) return;
   const int first = i * c.bs;
   const int lo = max(first, start), hi = min(len, first + c.bs);
-  const Rows& src = blockIdx.y ? v_new : k_new;
-  const uint16_t* x = src.at(static_cast<int>(l), b, h, lo - start);
+  const bool values = blockIdx.y != 0;
+  const uint16_t* x = values ? v_new.at(l, b, h, lo - start) : k_new.at(l, b, h, lo - start);
+  const long long stride = values ? v_new.token : k_new.token;
   const int total = (hi - lo) * CH;
   auto load = [&](int idx) {
-    return __ldg(reinterpret_cast<const uint4*>(x + (idx / CH) * src.token + (idx % CH) * 8));
+    return __ldg(reinterpret_cast<const uint4*>(x + (idx / CH) * stride + (idx % CH) * 8));
   };
   uint4 keep[kKeep];
   uint32_t m = 0;
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
     return;
   }
-  float* scale_ptr = c.scale[blockIdx.y] + scale_at(c, static_cast<int>(l), blk, h);
+  float* scale_ptr = (values ? c.scale[1] : c.scale[0]) + scale_at(c, l, blk, h);
   const float old = lo > first ? *scale_ptr : 0.f;
 #pragma unroll
   for (int s = 0; s < kKeep; ++s) m = max_abs8(keep[s], m);
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     m = warp_max_half(m);
   }
   float scale = exp2_int(scale_exp<FMT>(__uint_as_float(m << 16)));
-  uint8_t* rows = c.pool[blockIdx.y] + block_row(c, static_cast<int>(l), blk, h) * D;
+  uint8_t* rows = (values ? c.pool[1] : c.pool[0]) + block_row(c, l, blk, h) * D;
   if (lo > first) {  // older rows: the scale only grows, and they follow it
     if (old >= scale) {
       scale = old;
@@ -263,22 +263,20 @@ __device__ __forceinline__ float max_code16(uint4 v) {
 // kept index, its block, the scales), which the warp then shares: three loads that wait
 // for one another before 4 KB are on their way.
 template <int D, int FROM, int TO>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, 6)
     compact_kernel(Cache c, Cache to, CompactArgs a, int per_unit) {
   constexpr int CH = D / 16;                     // 16-byte chunks of a row
   constexpr int RPI = 32 / CH;                   // rows of one load of the warp
   constexpr int KEEP = kKeepRows / RPI;
   const int lane = threadIdx.x % 32;
   const int ch = lane % CH;
-  const long long task = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
-  const long long u = task / per_unit;
-  const int jb = static_cast<int>(task % per_unit);
-  const int h = static_cast<int>(u % c.H);
-  const int b = static_cast<int>((u / c.H) % c.B);
-  const int l = static_cast<int>(u / (static_cast<long long>(c.H) * c.B));
+  const uint32_t task = blockIdx.x * kWarps + threadIdx.x / 32;
+  const uint32_t u = task / per_unit;
+  const int jb = task % per_unit;
+  const int h = u % c.H, b = (u / c.H) % c.B, l = u / (c.H * c.B);
   if (l >= c.L) return;
   const int j0 = jb * to.bs;
-  const int32_t* kept = a.kept + u * a.budget;
+  const int32_t* kept = a.kept + static_cast<size_t>(u) * a.budget;
   // (read before the checks below: the index arrays do not depend on them)
   int slot = j0 + lane < a.budget && lane < to.bs ? kept[j0 + lane] : -1;
   const int new_blk = block_at(to, b, jb);
@@ -319,7 +317,8 @@ __global__ void __launch_bounds__(32 * kWarps)
   if (a.credit_out) {
     for (int j = j0 + lane; j < min(j0 + to.bs, a.budget); j += 32) {
       const int s = j < nk ? (j < j0 + 32 ? slot : kept[j]) : -1;
-      a.credit_out[u * a.budget + j] = s >= 0 && s < a.T ? a.credit_post[u * a.T + s] : 0.f;
+      a.credit_out[static_cast<size_t>(u) * a.budget + j] =
+          s >= 0 && s < a.T ? a.credit_post[static_cast<size_t>(u) * a.T + s] : 0.f;
     }
   }
   if (rows <= 0) return;
