@@ -127,6 +127,59 @@ __device__ __forceinline__ void decode4(uint32_t four, float (&x)[4]) {
   }
 }
 
+// Codes as signed integers, biased to 0..255, behind the exponent of 1024: the
+// fp16 number 1024 + u, from which 1152 leaves the value.
+__device__ __forceinline__ uint32_t unbias(uint32_t h) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
+  return r;
+}
+
+// Four codes to two half2: (0, 1), (2, 3).
+template <int FMT>
+__device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == KVC_CACHE8_E4M3) {
+    lo = e4m3_to_half2(w);
+    hi = e4m3_to_half2(w >> 16);
+  } else {
+    w ^= 0x80808080u;
+    lo = unbias(__byte_perm(w, 0x64646464u, 0x4140));
+    hi = unbias(__byte_perm(w, 0x64646464u, 0x4342));
+  }
+}
+
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// 2^e as both halves of a pair of fp16, e <= 15; 0 below its last step.
+__device__ __forceinline__ uint32_t exp2_half2(int e) {
+  const uint32_t h = e >= -14 ? (15 + e) << 10 : e >= -24 ? 1u << (24 + e) : 0u;
+  return h * 0x00010001u;
+}
+
+// Pairs (0, 1) and (2, 3) of fp16 values, at most the largest code, to four codes.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes_of(uint32_t lo, uint32_t hi) {
+  if constexpr (FMT == KVC_CACHE8_E4M3) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\tmov.b32 %0, {a, b};\n\t}"
+        : "=r"(r)
+        : "r"(lo), "r"(hi));
+    return r;
+  } else {
+    // plus 1.5 2^10: steps of 1 there, so that the sum rounds to the nearest integer
+    // (ties to even), whose low byte it ends in
+    uint32_t a, b;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(a) : "r"(lo), "r"(0x66006600u));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(b) : "r"(hi), "r"(0x66006600u));
+    return __byte_perm(a, b, 0x6420);
+  }
+}
+
 // The block that holds entry i of sequence b, or -1 if it is out of range.
 __device__ __forceinline__ int block_at(const Cache& c, int b, int i) {
   if (i < 0 || i >= c.max_blocks) return -1;

@@ -45,27 +45,6 @@ cudaError_t allow_smem(Kernel* kernel, int smem, std::atomic<uint64_t>& told) {
 cudaError_t launch_attend_many(const Cache& c, int format, const AttendArgs& a, cudaStream_t s);
 size_t attend_many_parts_bytes(int d);
 
-// Codes as signed integers, biased to 0..255, behind the exponent of 1024: the
-// fp16 number 1024 + u, from which 1152 leaves the value.
-__device__ __forceinline__ uint32_t unbias(uint32_t h) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
-  return r;
-}
-
-// Four codes to two half2: (0, 1), (2, 3).
-template <int FMT>
-__device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (FMT == KVC_CACHE8_E4M3) {
-    lo = e4m3_to_half2(w);
-    hi = e4m3_to_half2(w >> 16);
-  } else {
-    w ^= 0x80808080u;
-    lo = unbias(__byte_perm(w, 0x64646464u, 0x4140));
-    hi = unbias(__byte_perm(w, 0x64646464u, 0x4342));
-  }
-}
-
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));

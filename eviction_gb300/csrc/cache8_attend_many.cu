@@ -135,18 +135,6 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// 2^e as both halves of a pair of fp16, 0 below its last step (e <= 0).
-__device__ __forceinline__ uint32_t exp2_half2(int e) {
-  const uint32_t h = e >= -14 ? (15 + e) << 10 : e >= -24 ? 1u << (24 + e) : 0u;
-  return h * 0x00010001u;
-}
-
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, 2)
     attend_many_kernel(Cache c, AttendArgs a, Parts sp, Div by_bs) {

@@ -57,17 +57,37 @@ __device__ __forceinline__ uint2 encode8(uint4 v, float inv) {
   return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
 
-// Codes times `ratio`, as codes again.
+// Codes times 2^e, as codes again (the products are at most the largest code).  In fp16
+// the products are exact wherever they do not round to code 0 (8 significant bits; what
+// fp16 cannot hold is far below the smallest code), so that there is one rounding.
+// Codes of a block whose scale shrinks by more than 2^15 are too small to be anything
+// but 0 and the next few: those go through fp32.
 template <int FROM, int TO>
-__device__ __forceinline__ uint32_t recode4(uint32_t four, float ratio) {
-  float x[4];
-  decode4<FROM>(four, x);
-  return encode2<TO>(x[0] * ratio, x[1] * ratio) | (encode2<TO>(x[2] * ratio, x[3] * ratio) << 16);
+__device__ __forceinline__ uint4 recode16(uint4 v, int e) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (e <= 15) {
+    const uint32_t factor = exp2_half2(e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t lo, hi;
+      halves<FROM>(w[i], lo, hi);
+      w[i] = codes_of<TO>(mul_half2(lo, factor), mul_half2(hi, factor));
+    }
+  } else {
+    const float ratio = exp2_int(min(e, 127));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x[4];
+      decode4<FROM>(w[i], x);
+      w[i] = encode2<TO>(x[0] * ratio, x[1] * ratio) | encode2<TO>(x[2] * ratio, x[3] * ratio) << 16;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <int FROM, int TO>
-__device__ __forceinline__ uint4 recode16(uint4 v, float ratio) {
-  return make_uint4(recode4<FROM, TO>(v.x, ratio), recode4<FROM, TO>(v.y, ratio),
-                    recode4<FROM, TO>(v.z, ratio), recode4<FROM, TO>(v.w, ratio));
+
+// Exponent of a scale (a power of two).
+__device__ __forceinline__ int exp_of(float scale) {
+  return static_cast<int>(__float_as_uint(scale) >> 23) - 127;
 }
 
 // One warp: one touched block of one head, keys (blockIdx.y 0) or values.
@@ -134,10 +154,10 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (old >= scale) {
       scale = old;
     } else {
-      const float ratio = old / scale;
+      const int down = exp_of(old) - exp_of(scale);
       uint4* p = reinterpret_cast<uint4*>(rows);
       for (int idx = lane; idx < (lo - first) * (D / 16); idx += 32)
-        p[idx] = recode16<FMT, FMT>(p[idx], ratio);
+        p[idx] = recode16<FMT, FMT>(p[idx], down);
     }
     __syncwarp();  // every lane has read the old scale
   }
@@ -224,7 +244,10 @@ __global__ void __launch_bounds__(kGatherThreads)
 
 // ---- compact ----
 
-constexpr int kKeepRows = 16;  // rows whose codes a warp keeps in registers
+constexpr int kCompactThreads = 256;
+constexpr int kKeepRows = 16;     // rows whose codes a warp keeps in registers
+constexpr int kLookRows = 1024;   // rows of a CTA at most (the largest block)
+constexpr int kMaxBlocks = 16;    // blocks of a CTA at most: two a warp
 
 // Bytes 2 k and 2 k + 1 as two signed 16-bit integers.
 template <int K>
@@ -259,137 +282,111 @@ __device__ __forceinline__ float max_code16(uint4 v) {
   }
 }
 
-// One warp: one new block of one head, keys and values.  A lane looks up a row (its
-// kept index, its block, the scales), which the warp then shares: three loads that wait
-// for one another before 4 KB are on their way.
+// One CTA: some new blocks of one head, keys and values.  Its threads look the rows up
+// (kept index, block, scales: three loads that wait for one another, once for all
+// blocks), then each warp takes whole blocks.  (A warp that looked up its own 16 rows
+// spent two thirds of its time on that: 106 us instead of MEASURED on 28 layers.)
 template <int D, int FROM, int TO>
-__global__ void __launch_bounds__(32 * kWarps, 6)
-    compact_kernel(Cache c, Cache to, CompactArgs a, int per_unit) {
+__global__ void __launch_bounds__(kCompactThreads, 3)
+    compact_kernel(Cache c, Cache to, CompactArgs a, int per_unit, int blocks) {
   constexpr int CH = D / 16;                     // 16-byte chunks of a row
-  constexpr int RPI = 32 / CH;                   // rows of one load of the warp
+  constexpr int RPI = 32 / CH;                   // rows of one load of a warp
   constexpr int KEEP = kKeepRows / RPI;
-  const int lane = threadIdx.x % 32;
+  __shared__ int s_row[kLookRows];               // place in the pools (rows of d codes from the
+  __shared__ float s_scale[2][kLookRows];        // layer's first, of this head); -1: none
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int ch = lane % CH;
-  const uint32_t task = blockIdx.x * kWarps + threadIdx.x / 32;
-  const uint32_t u = task / per_unit;
-  const int jb = task % per_unit;
+  const int u = blockIdx.x / per_unit;
+  const int jb0 = blockIdx.x % per_unit * blocks;
   const int h = u % c.H, b = (u / c.H) % c.B, l = u / (c.H * c.B);
-  if (l >= c.L) return;
-  const int j0 = jb * to.bs;
-  const int32_t* kept = a.kept + static_cast<size_t>(u) * a.budget;
-  // (read before the checks below: the index arrays do not depend on them)
-  int slot = j0 + lane < a.budget && lane < to.bs ? kept[j0 + lane] : -1;
-  const int new_blk = block_at(to, b, jb);
   bool bad = false;
   const int len = length_of(c, b, &bad);
   const int nk = a.n_kept[u];
   const int new_len = length_of(to, b, &bad);
-  if (bad || nk < 0 || nk > a.budget || nk != new_len) {
-    if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
-    return;
-  }
   const int pad = a.pad[b];
-  const int rows = min(nk - j0, to.bs);
-  // the row of 32 that this lane looks after: its place in the pools (rows of d codes
-  // from the layer's first, of this head) and its scales; -1 outside the sequence
-  const size_t base = block_row(c, l, 0, h);
-  const size_t scale_base = scale_at(c, l, 0, h);
-  int row;
-  float ks, vs;
-  auto look_up = [&](int r0) {
-    const int r = r0 + lane;
-    row = -1;
-    ks = vs = 0.f;
-    if (r >= rows) return;
-    const long long pos = static_cast<long long>(slot) - pad;
-    const bool in = pos >= 0 && pos < len && slot >= 0 && slot < a.T;
-    const int blk = in ? block_at(c, b, static_cast<int>(pos) / c.bs) : -1;
-    if (blk < 0) {
-      bad = true;
-      return;
-    }
-    row = blk * c.H * c.bs + static_cast<int>(pos) % c.bs;  // below 2^31: checked on the host
-    const size_t sc = scale_base + static_cast<size_t>(blk) * c.H;
-    ks = __ldg(c.scale[0] + sc);
-    vs = __ldg(c.scale[1] + sc);
-  };
-  look_up(0);
-  if (a.credit_out) {
-    for (int j = j0 + lane; j < min(j0 + to.bs, a.budget); j += 32) {
-      const int s = j < nk ? (j < j0 + 32 ? slot : kept[j]) : -1;
-      a.credit_out[static_cast<size_t>(u) * a.budget + j] =
-          s >= 0 && s < a.T ? a.credit_post[static_cast<size_t>(u) * a.T + s] : 0.f;
-    }
-  }
-  if (rows <= 0) return;
-  if (new_blk < 0) {
-    if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
+  if (bad || nk < 0 || nk > a.budget || nk != new_len) {
+    if (threadIdx.x == 0) report(c, KVC_STATUS_BAD_INDEX);
     return;
   }
-  // chunk ch of row r (r0 + 0..31 are looked up) of pool w
-  auto load = [&](int w, int r) {
-    const int from = __shfl_sync(0xffffffffu, row, r % 32);
-    return from >= 0 ? __ldg(reinterpret_cast<const uint4*>(c.pool[w]) + (base + from) * CH + ch)
-                     : make_uint4(0, 0, 0, 0);
-  };
-  uint4 kk[KEEP], kv[KEEP];
-#pragma unroll
-  for (int i = 0; i < KEEP; ++i) kk[i] = load(0, i * RPI + lane / CH);
-#pragma unroll
-  for (int i = 0; i < KEEP; ++i) kv[i] = load(1, i * RPI + lane / CH);
-  float km = 0.f, vm = 0.f;
-#pragma unroll
-  for (int i = 0; i < KEEP; ++i) {
-    const int r = i * RPI + lane / CH;
-    km = fmaxf(km, max_code16<FROM>(kk[i]) * __shfl_sync(0xffffffffu, ks, r));
-    vm = fmaxf(vm, max_code16<FROM>(kv[i]) * __shfl_sync(0xffffffffu, vs, r));
-  }
-  // the other rows of larger blocks (read again below, from L2)
-  auto more = [&](auto f) {
-    for (int r0 = 0; r0 < rows; r0 += 32) {
-      if (r0 > 0) {
-        slot = r0 + lane < rows ? kept[j0 + r0 + lane] : -1;
-        look_up(r0);
-      }
-      for (int r = r0 == 0 ? kKeepRows : r0; r < min(rows, r0 + 32); r += RPI) {
-        const int mine = r + lane / CH;
-        const uint4 k = load(0, mine), v = load(1, mine);
-        f(mine, k, v, __shfl_sync(0xffffffffu, ks, mine % 32), __shfl_sync(0xffffffffu, vs, mine % 32));
+  const int j0 = jb0 * to.bs;
+  const size_t scale_base = scale_at(c, l, 0, h);
+  for (int r = threadIdx.x; r < blocks * to.bs && j0 + r < a.budget; r += kCompactThreads) {
+    const size_t at = static_cast<size_t>(u) * a.budget + j0 + r;
+    int row = -1;
+    float ks = 0.f, vs = 0.f, credit = 0.f;
+    if (j0 + r < nk) {
+      const int slot = a.kept[at];
+      const long long pos = static_cast<long long>(slot) - pad;
+      if (slot >= 0 && slot < a.T && a.credit_out)
+        credit = a.credit_post[static_cast<size_t>(u) * a.T + slot];
+      const bool in = pos >= 0 && pos < len && slot >= 0 && slot < a.T;
+      const int blk = in ? block_at(c, b, static_cast<int>(pos) / c.bs) : -1;
+      if (blk < 0) {
+        bad = true;
+      } else {
+        row = blk * c.H * c.bs + static_cast<int>(pos) % c.bs;  // below 2^31: checked on the host
+        const size_t sc = scale_base + static_cast<size_t>(blk) * c.H;
+        ks = __ldg(c.scale[0] + sc);
+        vs = __ldg(c.scale[1] + sc);
       }
     }
-  };
-  if (rows > kKeepRows)
-    more([&](int, uint4 k, uint4 v, float s, float t) {
-      km = fmaxf(km, max_code16<FROM>(k) * s);
-      vm = fmaxf(vm, max_code16<FROM>(v) * t);
-    });
-  if (rows > 32) {  // back to the first rows' scales
-    slot = kept[j0 + lane];
-    look_up(0);
+    s_row[r] = row;
+    s_scale[0][r] = ks;
+    s_scale[1][r] = vs;
+    if (a.credit_out) a.credit_out[at] = credit;
   }
-  const float k_scale = exp2_int(scale_exp<TO>(warp_max(km)));
-  const float v_scale = exp2_int(scale_exp<TO>(warp_max(vm)));
-  const float k_inv = 1.f / k_scale, v_inv = 1.f / v_scale;  // exact
-  const size_t out = block_row(to, l, new_blk, h) * CH + ch;
-  uint4* ko = reinterpret_cast<uint4*>(to.pool[0]) + out;
-  uint4* vo = reinterpret_cast<uint4*>(to.pool[1]) + out;
-  auto store = [&](int r, uint4 k, uint4 v, float s, float t) {
-    if (r >= rows) return;
-    // (a row whose scale stays keeps its codes)
-    ko[r * CH] = FROM == TO && s == k_scale ? k : recode16<FROM, TO>(k, s * k_inv);
-    vo[r * CH] = FROM == TO && t == v_scale ? v : recode16<FROM, TO>(v, t * v_inv);
-  };
+  __syncthreads();
+  const size_t base = block_row(c, l, 0, h);
+  for (int jb = warp; jb < blocks; jb += kCompactThreads / 32) {
+    const int rows = min(nk - j0 - jb * to.bs, to.bs);
+    if (rows <= 0) break;
+    const int new_blk = block_at(to, b, jb0 + jb);
+    if (new_blk < 0) {
+      bad = true;
+      continue;
+    }
+    const int* my_row = s_row + jb * to.bs;
+    const float* my_ks = s_scale[0] + jb * to.bs;
+    const float* my_vs = s_scale[1] + jb * to.bs;
+    auto load = [&](const uint8_t* pool, int r) {  // chunk ch of row r
+      const int from = r < rows ? my_row[r] : -1;
+      return from >= 0 ? __ldg(reinterpret_cast<const uint4*>(pool) + (base + from) * CH + ch)
+                       : make_uint4(0, 0, 0, 0);
+    };
+    uint4 kk[KEEP], kv[KEEP];
 #pragma unroll
-  for (int i = 0; i < KEEP; ++i) {
-    const int r = i * RPI + lane / CH;
-    const float s = __shfl_sync(0xffffffffu, ks, r), t = __shfl_sync(0xffffffffu, vs, r);
-    store(r, kk[i], kv[i], s, t);
-  }
-  if (rows > kKeepRows) more(store);
-  if (lane == 0) {
-    const size_t sc = scale_at(to, l, new_blk, h);
-    to.scale[0][sc] = k_scale;
-    to.scale[1][sc] = v_scale;
+    for (int i = 0; i < KEEP; ++i) kk[i] = load(c.pool[0], i * RPI + lane / CH);
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) kv[i] = load(c.pool[1], i * RPI + lane / CH);
+    float km = 0.f, vm = 0.f;
+    auto most = [&](int r, uint4 k, uint4 v) {
+      if (r >= rows) return;
+      km = fmaxf(km, max_code16<FROM>(k) * my_ks[r]);
+      vm = fmaxf(vm, max_code16<FROM>(v) * my_vs[r]);
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) most(i * RPI + lane / CH, kk[i], kv[i]);
+    // (the other rows of larger blocks are read twice, the second time from L2)
+    for (int r = kKeepRows + lane / CH; r < rows; r += RPI)
+      most(r, load(c.pool[0], r), load(c.pool[1], r));
+    const int k_exp = scale_exp<TO>(warp_max(km)), v_exp = scale_exp<TO>(warp_max(vm));
+    const size_t out = block_row(to, l, new_blk, h) * CH + ch;
+    uint4* ko = reinterpret_cast<uint4*>(to.pool[0]) + out;
+    uint4* vo = reinterpret_cast<uint4*>(to.pool[1]) + out;
+    auto store = [&](int r, uint4 k, uint4 v) {
+      if (r >= rows) return;
+      ko[r * CH] = recode16<FROM, TO>(k, exp_of(my_ks[r]) - k_exp);
+      vo[r * CH] = recode16<FROM, TO>(v, exp_of(my_vs[r]) - v_exp);
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) store(i * RPI + lane / CH, kk[i], kv[i]);
+    for (int r = kKeepRows + lane / CH; r < rows; r += RPI)
+      store(r, load(c.pool[0], r), load(c.pool[1], r));
+    if (lane == 0) {
+      const size_t sc = scale_at(to, l, new_blk, h);
+      to.scale[0][sc] = exp2_int(k_exp);
+      to.scale[1][sc] = exp2_int(v_exp);
+    }
   }
   if (bad) report(c, KVC_STATUS_BAD_INDEX);
 }
@@ -427,12 +424,14 @@ cudaError_t launch_gather(const Cache& c, int format, int T, uint16_t* k_out, ui
 template <int D>
 static cudaError_t launch_compact_d(const Cache& c, int from, const Cache& to, int to_format,
                                     const CompactArgs& a, cudaStream_t s) {
-  const int per_unit = (a.budget + to.bs - 1) / to.bs;
-  const int grid = ctas(static_cast<long long>(c.L) * c.B * c.H * per_unit);
+  const int all = (a.budget + to.bs - 1) / to.bs;
+  const int blocks = min(min(max(kLookRows / to.bs, 1), kMaxBlocks), all);
+  const int per_unit = (all + blocks - 1) / blocks;
+  const int grid = c.L * c.B * c.H * per_unit;
   constexpr int E = KVC_CACHE8_E4M3, I = KVC_CACHE8_INT8;
   auto* kernel = from == E ? (to_format == E ? compact_kernel<D, E, E> : compact_kernel<D, E, I>)
                            : (to_format == E ? compact_kernel<D, I, E> : compact_kernel<D, I, I>);
-  kernel<<<grid, 32 * kWarps, 0, s>>>(c, to, a, per_unit);
+  kernel<<<grid, kCompactThreads, 0, s>>>(c, to, a, per_unit, blocks);
   return cudaGetLastError();
 }
 
