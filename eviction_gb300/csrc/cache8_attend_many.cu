@@ -8,8 +8,9 @@
 //   converters (4 warps)  codes from global memory to fp16 tiles in shared memory, in
 //                         the swizzled layout of the MMA operands, one tile ahead.
 //                         Keys carry their block's scale relative to the tile's
-//                         largest, values relative to the largest so far (powers of
-//                         two: exact, down to fp16's last step);
+//                         largest, values relative to one at or above the
+//                         largest so far (powers of two: exact, down to fp16's last
+//                         step);
 //   MMA (1 thread)        S = Q K^T (128 x 128, in TMEM), then O += P V with P read
 //                         from TMEM, where it takes the place of S;
 //   softmax (4 warps)     one thread a row: p = 2^(z - m), their sum in fp32, P to TMEM
@@ -43,6 +44,7 @@ constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps);
 constexpr int kTmemCols = 256;    // S / P: 128, O: up to 128
 constexpr int kMaxParts = 320;    // CTAs of a call that cuts heads
 constexpr float kRoom = 15.f, kStart = 8.f;  // log2 of the weights' limit and of a new m's
+constexpr int kHeadroom = 1;  // log2 of the room that a new value reference leaves: moving it scales O
 constexpr int kSpread = 8;  // log2 of how far below the largest value scale stays plain
 
 struct Parts {
@@ -59,6 +61,11 @@ struct Smem {
   static constexpr int kE = kMeta, kBack = kE + 2 * kTokens * 4, kInfo = kBack + 2 * kTokens * 4,
                        kRed = kInfo + 2 * 16, kBars = kRed + 2 * 4 * 16, kMisc = kBars + 16 * 8;
   static constexpr int kBytes = kMisc + 32 + 1024;  // and 1024 for the alignment
+};
+
+template <bool V>
+struct Bool {
+  static constexpr bool value = V;
 };
 
 // What a tile's converters tell the softmax warps.
@@ -299,10 +306,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float* e_col = s_e + st * kTokens;
       const float* back_col = s_back + st * kTokens;
       const float f = qf * info.k_ref;
-      const bool fast = info.plain && t0 + kTokens <= len - nq + 1;  // seen by all rows
+      const bool whole = t0 + kTokens <= len - nq + 1;  // seen by all rows
+      const int seen = limit - t0 + 1;                  // columns that this row sees
       uint32_t va[32], vb[32];
       float top;
-      if (fast) {
+      if (info.plain && whole) {
         float m0, m1;
         tmem_ld32_max(my_tmem + 64, va, m0);
         tmem_ld32_max(my_tmem + 96, vb, m1);
@@ -312,6 +320,21 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_ld32_max(my_tmem + 32, vb, m1);
         tmem_ld_wait();
         top = fmaxf(top, fmaxf(m0, m1)) * f;
+      } else if (info.plain) {
+        auto most = [&](const uint32_t (&v)[32], int first, float so_far) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            so_far = first + x < seen ? fmaxf(so_far, __uint_as_float(v[x])) : so_far;
+          return so_far;
+        };
+        tmem_ld32(my_tmem + 64, va);
+        tmem_ld32(my_tmem + 96, vb);
+        tmem_ld_wait();
+        top = most(vb, 96, most(va, 64, -INFINITY));
+        tmem_ld32(my_tmem, va);
+        tmem_ld32(my_tmem + 32, vb);
+        tmem_ld_wait();
+        top = most(vb, 32, most(va, 0, top)) * f;
       } else {
         top = -INFINITY;
 #pragma unroll 1
@@ -321,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
             const float z = fmaf(__uint_as_float(va[x]), f, e_col[k * 32 + x]);
-            if (t0 + k * 32 + x <= limit) top = fmaxf(top, z);
+            if (k * 32 + x < seen) top = fmaxf(top, z);
           }
         }
       }
@@ -357,30 +380,39 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float ref = m == -INFINITY ? 0.f : m;
       const float2 ff = make_float2(f, f), off = make_float2(-ref, -ref);
       float2 part_sum = make_float2(0.f, 0.f);
-      if (fast) {
-        auto weights = [&](const uint32_t (&v)[32], uint32_t to) {
+      if (info.plain) {
+        auto weights = [&](const uint32_t (&v)[32], int first, auto masked) {
           uint32_t p[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             float2 z = fma2(make_float2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])),
                             ff, off);
+            if constexpr (decltype(masked)::value) {
+              z.x = first + 2 * x < seen ? z.x : -INFINITY;
+              z.y = first + 2 * x + 1 < seen ? z.y : -INFINITY;
+            }
             z.x = ex2(z.x);
             z.y = ex2(z.y);
             part_sum = add2(part_sum, z);
             p[x] = half2_of(z.x, z.y);
           }
-          tmem_st16(to, p);
+          tmem_st16(my_tmem + first / 2, p);
         };
         // columns 0-63 are in registers, and P takes no others before 64-127 are read
-        weights(va, my_tmem);
-        tmem_ld32(my_tmem + 64, va);
-        weights(vb, my_tmem + 16);
-        tmem_ld32(my_tmem + 96, vb);
-        tmem_ld_wait();
-        weights(va, my_tmem + 32);
-        weights(vb, my_tmem + 48);
+        auto all = [&](auto masked) {
+          weights(va, 0, masked);
+          tmem_ld32(my_tmem + 64, va);
+          weights(vb, 32, masked);
+          tmem_ld32(my_tmem + 96, vb);
+          tmem_ld_wait();
+          weights(va, 64, masked);
+          weights(vb, 96, masked);
+        };
+        if (whole)
+          all(Bool<false>{});
+        else
+          all(Bool<true>{});
       } else {
-        const int seen = limit - t0 + 1;  // columns that this row sees
 #pragma unroll 1
         for (int k = 0; k < kTokens / 32; ++k) {
           uint32_t p[16];
@@ -472,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int blk[4], row[4];
     uint32_t ks[4], vs[4];  // scales as they are in memory
     uint4 kc[4][DB], vc[4][DB];
-    int v_ref = -1000;      // largest value exponent so far
+    int v_ref = -1000;      // what the values are relative to
     auto lookup = [&](int i) {  // the tile's blocks
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -499,28 +531,50 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     };
     auto load_codes = [&](const uint8_t* pool, uint4 (&to)[4][DB]) {
+      bool all = true;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 4; ++k) all = all && row[k] >= 0;
+      if (__all_sync(0xffffffffu, all)) {
 #pragma unroll
-        for (int x = 0; x < DB; ++x)
-          to[k][x] = row[k] >= 0 ? __ldg(reinterpret_cast<const uint4*>(
-                                       pool + static_cast<size_t>(row[k]) * D + (q4 + 4 * x) * 16))
-                                 : make_uint4(0, 0, 0, 0);
-    };
-    // 16 codes of a row, times 2^down, to their place in a tile
-    auto store = [&](uint8_t* tile, int r, int x, uint4 codes, bool scaled, uint32_t factor) {
-      const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-      uint32_t o[8];
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) halves<FMT>(w[k], o[2 * k], o[2 * k + 1]);
-      if (scaled) {
+          for (int x = 0; x < DB; ++x)
+            to[k][x] = __ldg(reinterpret_cast<const uint4*>(
+                pool + static_cast<size_t>(row[k]) * D + (q4 + 4 * x) * 16));
+      } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = mul_half2(o[k], factor);
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int x = 0; x < DB; ++x)
+            to[k][x] = row[k] >= 0 ? __ldg(reinterpret_cast<const uint4*>(
+                                         pool + static_cast<size_t>(row[k]) * D + (q4 + 4 * x) * 16))
+                                   : make_uint4(0, 0, 0, 0);
       }
-      uint8_t* at = tile + x * kBlock + r * 128;
-      *reinterpret_cast<uint4*>(at + (((2 * q4) ^ (r % 8)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(at + (((2 * q4 + 1) ^ (r % 8)) << 4)) =
-          make_uint4(o[4], o[5], o[6], o[7]);
+    };
+    // 16 codes each of this lane's rows, times their factors, to their places in a tile
+    // (the two 16-byte places of a chunk are the same in all rows: row_in + 32 k)
+    uint8_t* const place0 = smem + row_in * 128 + (((2 * q4) ^ (row_in % 8)) << 4);
+    uint8_t* const place1 = smem + row_in * 128 + (((2 * q4 + 1) ^ (row_in % 8)) << 4);
+    constexpr uint32_t kOne = 0x3C003C00u;
+    auto store = [&](int tile, const uint4 (&codes)[4][DB], const uint32_t (&factor)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool scaled = __any_sync(0xffffffffu, factor[k] != kOne);
+#pragma unroll
+        for (int x = 0; x < DB; ++x) {
+          const uint32_t w[4] = {codes[k][x].x, codes[k][x].y, codes[k][x].z, codes[k][x].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) halves<FMT>(w[y], o[2 * y], o[2 * y + 1]);
+          if (scaled) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y) o[y] = mul_half2(o[y], factor[k]);
+          }
+          const int at = tile + x * kBlock + k * 32 * 128;
+          *reinterpret_cast<uint4*>(place0 + at) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(place1 + at) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      }
     };
     // a tile's codes are loaded while the last one's are stored, its blocks and scales
     // one step before
@@ -563,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         absent |= o.w;
       }
       k_max = max(k_max, -126);
-      v_ref = max(max(v_ref, v_max), -126);
+      if (v_max > v_ref) v_ref = max(v_max + kHeadroom, -126);
       const bool plain = !absent && v_ref - v_min <= kSpread;
       if (q4 == 0) {
 #pragma unroll
@@ -586,33 +640,20 @@ __global__ void __launch_bounds__(kThreads, 2)
       warp_arrive(&m_full[st]);
       // ---- keys and values, relative to those scales ----
       uint32_t k_factor[4], v_factor[4];
-      bool k_scaled = false, v_scaled = false;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        k_factor[k] = exp2_half2(min(ke[k] - k_max, 0));
-        v_factor[k] = exp2_half2(min(ve[k] - v_ref, 0));
-        k_scaled = k_scaled || ke[k] != k_max;
-        v_scaled = v_scaled || (plain && ve[k] != v_ref);
+        k_factor[k] = row[k] < 0 ? kOne : exp2_half2(min(ke[k] - k_max, 0));
+        v_factor[k] = row[k] < 0 || !plain ? kOne : exp2_half2(min(ve[k] - v_ref, 0));
       }
-      k_scaled = __any_sync(0xffffffffu, k_scaled);
-      v_scaled = __any_sync(0xffffffffu, v_scaled);
       if (!warp_wait(k_empty, (i & 1) ^ 1, abort, c.status)) break;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int x = 0; x < DB; ++x)
-          store(smem + Sm::kK, row_in + 32 * k, x, kc[k][x], k_scaled, k_factor[k]);
+      store(Sm::kK, kc, k_factor);
       fence_async_shared();
       warp_arrive(k_full);
       resolve(i + 1);
       load_codes(kp, kc);
       lookup(i + 2);
       if (!warp_wait(v_empty, (i & 1) ^ 1, abort, c.status)) break;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int x = 0; x < DB; ++x)
-          store(smem + Sm::kV, row_in + 32 * k, x, vc[k][x], v_scaled, v_factor[k]);
+      store(Sm::kV, vc, v_factor);
       fence_async_shared();
       warp_arrive(v_full);
       load_codes(vp, vc);
