@@ -41,6 +41,7 @@ namespace {
 constexpr int kRows = 128, kTokens = 128;
 constexpr int kSoftmaxWarps = 4, kConvertWarps = 4;
 constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps);
+constexpr int kInfos = 4;         // tiles whose scales are told ahead
 constexpr int kTmemCols = 256;    // S / P: 128, O: up to 128
 constexpr int kMaxParts = 320;    // CTAs of a call that cuts heads
 constexpr float kRoom = 15.f, kStart = 8.f;  // log2 of the weights' limit and of a new m's
@@ -58,8 +59,10 @@ template <int D>
 struct Smem {
   static constexpr int kTile = kTokens * D * 2;
   static constexpr int kV = 0, kK = kTile, kQ = 2 * kTile, kMeta = 3 * kTile;
-  static constexpr int kE = kMeta, kBack = kE + 2 * kTokens * 4, kInfo = kBack + 2 * kTokens * 4,
-                       kRed = kInfo + 2 * 16, kBars = kRed + 2 * 4 * 16, kMisc = kBars + 16 * 8;
+  static constexpr int kE = kMeta, kBack = kE + kInfos * kTokens * 4,
+                       kInfo = kBack + kInfos * kTokens * 4,
+                       kTok = kInfo + kInfos * 16, kRed = kTok + 2 * kTokens * 8,
+                       kBars = kRed + 2 * kConvertWarps * 16, kMisc = kBars + 24 * 8;
   static constexpr int kBytes = kMisc + 32 + 1024;  // and 1024 for the alignment
 };
 
@@ -152,14 +155,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr uint32_t kOutCol = 128;      // O's first TMEM column
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float* s_e = reinterpret_cast<float*>(smem + Sm::kE);        // [2][kTokens]
-  float* s_back = reinterpret_cast<float*>(smem + Sm::kBack);  // [2][kTokens] 2^-e
+  float* s_e = reinterpret_cast<float*>(smem + Sm::kE);        // [kInfos][kTokens]
+  float* s_back = reinterpret_cast<float*>(smem + Sm::kBack);  // [kInfos][kTokens] 2^-e
   TileInfo* s_info = reinterpret_cast<TileInfo*>(smem + Sm::kInfo);
-  int4* s_red = reinterpret_cast<int4*>(smem + Sm::kRed);
+  int2* s_tok = reinterpret_cast<int2*>(smem + Sm::kTok);  // [2][kTokens] row, exponents
+  int4* s_red = reinterpret_cast<int4*>(smem + Sm::kRed);  // [2][kConvertWarps]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kBars);
   uint64_t *q_full = bars, *k_full = bars + 1, *k_empty = bars + 2, *v_full = bars + 3,
            *v_empty = bars + 4, *s_full = bars + 5, *p_full = bars + 6, *o_full = bars + 7,
-           *m_full = bars + 8, *m_empty = bars + 10, *r_full = bars + 12, *done = bars + 13;
+           *r_full = bars + 8, *done = bars + 9, *m_full = bars + 10,
+           *m_empty = bars + 10 + kInfos;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sm::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + Sm::kMisc + 4);
   int* s_last = reinterpret_cast<int*>(smem + Sm::kMisc + 8);
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_init(p_full, kSoftmaxWarps);
     mbar_init(o_full, 1);
     mbar_init(r_full, kConvertWarps);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kInfos; ++i) {
       mbar_init(&m_full[i], kConvertWarps);
       mbar_init(&m_empty[i], kSoftmaxWarps);
     }
@@ -295,8 +300,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == 0 && n_tiles > 0)
       ok = warp_wait(q_full, 0, abort, c.status) && issue_scores(0);
     for (int i = 0; ok && i < n_tiles; ++i) {
-      const int t0 = (tile0 + i) * kTokens, st = i & 1;
-      if (!warp_wait(&m_full[st], (i >> 1) & 1, abort, c.status) ||
+      const int t0 = (tile0 + i) * kTokens, st = i % kInfos;
+      if (!warp_wait(&m_full[st], (i / kInfos) & 1, abort, c.status) ||
           !warp_wait(s_full, i & 1, abort, c.status)) {
         ok = false;
         break;
@@ -501,34 +506,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float* ksp = c.scale[0] + scale_at(c, l, 0, h);
     const float* vsp = c.scale[1] + scale_at(c, l, 0, h);
     const int32_t* table = c.table + static_cast<size_t>(b) * c.max_blocks;
-    int blk[4], row[4];
-    uint32_t ks[4], vs[4];  // scales as they are in memory
+    // This lane looks up token 32 cw + lane of a tile; the warps exchange what they find.
+    const int own = cw * 32 + lane;
+    int own_blk, own_row;
+    uint32_t own_ks, own_vs;  // scales as they are in memory
+    int row[4];               // of the tokens row_in + 32 k
     uint4 kc[4][DB], vc[4][DB];
-    int v_ref = -1000;      // what the values are relative to
+    int v_ref = -1000;        // what the values are relative to
     auto lookup = [&](int i) {  // the tile's blocks
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int t = (tile0 + i) * kTokens + row_in + 32 * k;
-        blk[k] = i < n_tiles && t < len ? __ldg(table + by_bs.div(t)) : -1;
-      }
+      const int t = (tile0 + i) * kTokens + own;
+      const bool in = i < n_tiles && t < len;
+      own_blk = __ldg(table + (in ? by_bs.div(t) : 0));
+      if (!in) own_blk = -1;
     };
     auto resolve = [&](int i) {  // rows and scales of the tile whose blocks are known
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int t = (tile0 + i) * kTokens + row_in + 32 * k;
-        row[k] = -1;
-        ks[k] = vs[k] = 0;
-        if (i < n_tiles && t < len) {
-          if (blk[k] < 0 || blk[k] >= c.n_blocks) {
-            bad = true;
-          } else {
-            row[k] = blk[k] * c.H * by_bs.bs + (t - by_bs.div(t) * by_bs.bs);
-            const size_t sc = static_cast<size_t>(blk[k]) * c.H;
-            ks[k] = __float_as_uint(__ldg(ksp + sc));
-            vs[k] = __float_as_uint(__ldg(vsp + sc));
-          }
-        }
-      }
+      const int t = (tile0 + i) * kTokens + own;
+      const bool in = i < n_tiles && t < len;
+      const bool found = in && static_cast<uint32_t>(own_blk) < static_cast<uint32_t>(c.n_blocks);
+      bad = bad || (in && !found);
+      const size_t sc = found ? static_cast<size_t>(own_blk) * c.H : 0;
+      own_ks = __float_as_uint(__ldg(ksp + sc));
+      own_vs = __float_as_uint(__ldg(vsp + sc));
+      own_row = found ? own_blk * c.H * by_bs.bs + (t - by_bs.div(t) * by_bs.bs) : -1;
     };
     auto load_codes = [&](const uint8_t* pool, uint4 (&to)[4][DB]) {
       bool all = true;
@@ -576,58 +575,37 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     };
-    // a tile's codes are loaded while the last one's are stored, its blocks and scales
-    // one step before
-    lookup(0);
-    resolve(0);
-    load_codes(kp, kc);
-    load_codes(vp, vc);
-    lookup(1);
-    for (int i = 0; i < n_tiles; ++i) {
-      const int st = i & 1;
-      // ---- the tile's scales ----
-      int ke[4], ve[4], k_max = -1000, v_max = -1000, v_min = 1000, absent = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        ke[k] = static_cast<int>(ks[k] >> 23) - 127;
-        ve[k] = static_cast<int>(vs[k] >> 23) - 127;
-        if (row[k] < 0) {
-          absent = 1;
-          continue;
-        }
-        k_max = max(k_max, ke[k]);
-        v_max = max(v_max, ve[k]);
-        v_min = min(v_min, ve[k]);
-      }
-      k_max = __reduce_max_sync(0xffffffffu, k_max);
-      v_max = __reduce_max_sync(0xffffffffu, v_max);
-      v_min = __reduce_min_sync(0xffffffffu, v_min);
-      absent = __any_sync(0xffffffffu, absent);
-      if (!warp_wait(&m_empty[st], ((i >> 1) & 1) ^ 1, abort, c.status)) break;
+    // A tile's rows and scales: this lane's rows and factors; the softmax warps are told.
+    uint32_t k_factor[4], v_factor[4], v_next[4];
+    auto announce = [&](int i) {
+      const int st = i % kInfos, ex = i & 1;
+      const bool there = own_row >= 0;
+      const int ke = static_cast<int>(own_ks >> 23) - 127, ve = static_cast<int>(own_vs >> 23) - 127;
+      int k_max = __reduce_max_sync(0xffffffffu, there ? ke : -1000);
+      int v_max = __reduce_max_sync(0xffffffffu, there ? ve : -1000);
+      int v_min = __reduce_min_sync(0xffffffffu, there ? ve : 1000);
+      int absent = __any_sync(0xffffffffu, !there);
       // (two buffers: a warp writes one again after all have read the other)
-      if (lane == 0) s_red[st * kConvertWarps + cw] = make_int4(k_max, v_max, v_min, absent);
+      s_tok[ex * kTokens + own] = make_int2(own_row, (ke & 0xffff) | ve << 16);
+      if (lane == 0) s_red[ex * kConvertWarps + cw] = make_int4(k_max, v_max, v_min, absent);
       warp_arrive(r_full);
-      if (!warp_wait(r_full, i & 1, abort, c.status)) break;
+      if (!warp_wait(&m_empty[st], ((i / kInfos) & 1) ^ 1, abort, c.status) ||
+          !warp_wait(r_full, i & 1, abort, c.status))
+        return false;
+      k_max = -126;
 #pragma unroll
       for (int k = 0; k < kConvertWarps; ++k) {
-        const int4 o = s_red[st * kConvertWarps + k];
+        const int4 o = s_red[ex * kConvertWarps + k];
         k_max = max(k_max, o.x);
         v_max = max(v_max, o.y);
         v_min = min(v_min, o.z);
         absent |= o.w;
       }
-      k_max = max(k_max, -126);
       if (v_max > v_ref) v_ref = max(v_max + kHeadroom, -126);
       const bool plain = !absent && v_ref - v_min <= kSpread;
-      if (q4 == 0) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool bare = !plain && row[k] >= 0;
-          s_e[st * kTokens + row_in + 32 * k] =
-              row[k] < 0 ? -INFINITY : bare ? static_cast<float>(ve[k] - v_ref) : 0.f;
-          s_back[st * kTokens + row_in + 32 * k] =
-              row[k] < 0 ? 0.f : bare ? exp2_int(min(v_ref - ve[k], 126)) : 1.f;
-        }
+      if (!plain) {
+        s_e[st * kTokens + own] = there ? static_cast<float>(ve - v_ref) : -INFINITY;
+        s_back[st * kTokens + own] = there ? exp2_int(min(v_ref - ve, 126)) : 0.f;
       }
       if (lane == 0 && cw == 0) {
         TileInfo info;
@@ -638,25 +616,59 @@ __global__ void __launch_bounds__(kThreads, 2)
         s_info[st] = info;
       }
       warp_arrive(&m_full[st]);
-      // ---- keys and values, relative to those scales ----
-      uint32_t k_factor[4], v_factor[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        k_factor[k] = row[k] < 0 ? kOne : exp2_half2(min(ke[k] - k_max, 0));
-        v_factor[k] = row[k] < 0 || !plain ? kOne : exp2_half2(min(ve[k] - v_ref, 0));
+        const int2 tok = s_tok[ex * kTokens + row_in + 32 * k];
+        row[k] = tok.x;
+        const int e = static_cast<int16_t>(tok.y & 0xffff), f = tok.y >> 16;
+        k_factor[k] = tok.x < 0 ? kOne : exp2_half2(min(e - k_max, 0));
+        v_next[k] = tok.x < 0 || !plain ? kOne : exp2_half2(min(f - v_ref, 0));
       }
-      if (!warp_wait(k_empty, (i & 1) ^ 1, abort, c.status)) break;
+      return true;
+    };
+    // A tile's keys can be stored once the last one's scores are done, its values once
+    // the last one's output is.  Between the two stores of one turn of the loop, which
+    // the products wait for, there are only the next values' loads.  Codes are on their
+    // way one tile ahead, scales two, blocks three.
+    lookup(0);
+    resolve(0);
+    lookup(1);
+    bool go = n_tiles > 0 && announce(0);
+    if (go) {
+      load_codes(kp, kc);
+      load_codes(vp, vc);
+      resolve(1);
+      lookup(2);
       store(Sm::kK, kc, k_factor);
       fence_async_shared();
       warp_arrive(k_full);
-      resolve(i + 1);
-      load_codes(kp, kc);
-      lookup(i + 2);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v_factor[k] = v_next[k];
+      if (n_tiles > 1) {
+        go = announce(1);
+        load_codes(kp, kc);
+        resolve(2);
+        lookup(3);
+      }
+    }
+    for (int i = 0; go && i < n_tiles; ++i) {
       if (!warp_wait(v_empty, (i & 1) ^ 1, abort, c.status)) break;
       store(Sm::kV, vc, v_factor);
       fence_async_shared();
       warp_arrive(v_full);
+      if (i + 1 == n_tiles) break;
       load_codes(vp, vc);
+      if (!warp_wait(k_empty, i & 1, abort, c.status)) break;
+      store(Sm::kK, kc, k_factor);
+      fence_async_shared();
+      warp_arrive(k_full);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v_factor[k] = v_next[k];
+      if (i + 2 == n_tiles) continue;
+      if (!announce(i + 2)) break;
+      load_codes(kp, kc);
+      resolve(i + 3);
+      lookup(i + 4);
     }
     if (bad) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
   }
