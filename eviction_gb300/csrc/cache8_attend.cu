@@ -672,11 +672,22 @@ cudaError_t launch_few(const Cache& c, const AttendArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Above this many query rows a head's work is bound by arithmetic: the other kernel.
+// Which kernel: this one reads a head's tokens once for each 16 query rows, the other
+// takes 128 rows at a time but starts and turns slower.  By the product of heads,
+// 16-row tiles and tokens (the table's capacity), this one / the other in us:
+//   4 heads x 2048 tokens, 112 rows (57 k)     19 / 24
+//   32 x 2048, 28 rows (131 k)                 24 / 25;   35 rows (197 k)  28 / 25
+//   128 x 1536, 28 rows (393 k)                36 / 38;   35 rows (590 k)  44 / 39
+//   16 x 16384, 28 rows (524 k)                42 / 48;   56 rows (1 M)    61 / 49
+//   512 x 860, 32 rows (881 k)                 70 / 66;   64 rows (1.8 M) 112 / 68
 constexpr int kFewRows = 32;
+constexpr long long kFewWork = 150'000;
 
 cudaError_t launch_attend(const Cache& c, int format, const AttendArgs& a, cudaStream_t s) {
-  if (a.G * a.n > kFewRows) return launch_attend_many(c, format, a, s);
+  const int R = a.G * a.n;
+  const long long work = static_cast<long long>(c.L) * c.B * c.H * ((R + 15) / 16) *
+                         (static_cast<long long>(c.max_blocks) * c.bs);
+  if (R > kFewRows && work >= kFewWork) return launch_attend_many(c, format, a, s);
   if (c.d == 64)
     return format == KVC_CACHE8_E4M3 ? launch_few<64, KVC_CACHE8_E4M3>(c, a, s)
                                      : launch_few<64, KVC_CACHE8_INT8>(c, a, s);

@@ -30,8 +30,8 @@
 // softmax and MMAs take turns; two CTAs on an SM (half of TMEM and shared memory
 // each) fill each other's gaps, and a CTA's beginning and end as well.
 //
-// Heads and row tiles that do not fill the GPU have their tokens cut into parts; the
-// last CTA of a row tile to finish joins them in order.  Every wait is bounded.
+// Heads and row tiles that do not fill the GPU have their tokens cut into parts, which
+// a second launch joins in order.  Every wait is bounded.
 #include "cache8_attend.cuh"
 
 namespace kvc {
@@ -52,7 +52,6 @@ struct Parts {
   int per_tile;   // CTAs of a row tile
   int row_tiles;  // of a head
   float* part;    // [kMaxParts][D + 2][kRows]: reference, sum, values
-  int* arrived;   // [kCounters] zero between calls
 };
 
 template <int D>
@@ -145,6 +144,35 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 
+// One row tile of one head, and how its tokens are cut.
+struct RowTile {
+  int l, b, h, r0, rows, nq, len, tiles, per, parts;
+  bool bad;
+};
+__device__ __forceinline__ RowTile row_tile(const Cache& c, const AttendArgs& a, const Parts& sp,
+                                            int ur) {
+  RowTile w;
+  const int u = ur / sp.row_tiles;
+  w.h = u % c.H;
+  w.b = (u / c.H) % c.B;
+  w.l = u / (c.H * c.B);
+  w.bad = false;
+  w.len = length_of(c, w.b, &w.bad);
+  w.nq = a.n_q ? a.n_q[w.b] : a.n;
+  if (w.nq < 0 || w.nq > a.n) w.bad = true;
+  w.r0 = (ur % sp.row_tiles) * kRows;
+  w.rows = w.bad ? 0 : min(a.G * w.nq - w.r0, kRows);
+  w.tiles = w.per = w.parts = 0;
+  if (w.rows <= 0) return w;
+  // the last token that one of the rows sees
+  const int r1 = w.r0 + w.rows - 1;
+  const int last_q = w.r0 / w.nq == r1 / w.nq ? r1 % w.nq : w.nq - 1;
+  w.tiles = div_up(max(w.len - w.nq + last_q + 1, 0), kTokens);
+  w.per = max(div_up(w.tiles, sp.per_tile), 2);
+  w.parts = max(div_up(w.tiles, w.per), 1);
+  return w;
+}
+
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, 2)
     attend_many_kernel(Cache c, AttendArgs a, Parts sp, Div by_bs) {
@@ -167,33 +195,17 @@ __global__ void __launch_bounds__(kThreads, 2)
            *m_empty = bars + 10 + kInfos;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sm::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + Sm::kMisc + 4);
-  int* s_last = reinterpret_cast<int*>(smem + Sm::kMisc + 8);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   // ---- this CTA's row tile and tokens ----
   const int part = blockIdx.x % sp.per_tile;
-  const int ur = blockIdx.x / sp.per_tile;
-  const int rt = ur % sp.row_tiles;
-  const int u = ur / sp.row_tiles;
-  const int h = u % c.H, b = (u / c.H) % c.B, l = u / (c.H * c.B);
+  const RowTile w = row_tile(c, a, sp, blockIdx.x / sp.per_tile);
+  if (w.bad && threadIdx.x == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
+  if (w.rows <= 0 || part >= w.parts) return;
+  const int l = w.l, b = w.b, h = w.h, r0 = w.r0, rows = w.rows, nq = w.nq, len = w.len,
+            parts = w.parts;
+  const int tile0 = part * w.per, n_tiles = min(w.per, w.tiles - tile0);
   bool bad = false;
-  const int len = length_of(c, b, &bad);
-  const int nq = a.n_q ? a.n_q[b] : a.n;
-  if (bad || nq < 0 || nq > a.n) {
-    if (threadIdx.x == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
-    return;
-  }
-  const int rows = min(a.G * nq - rt * kRows, kRows);
-  if (rows <= 0) return;
-  // the last token that one of the rows sees
-  const int r0 = rt * kRows, r1 = r0 + rows - 1;
-  const int last_q = r0 / nq == r1 / nq ? r1 % nq : nq - 1;
-  const int kv_end = max(len - nq + last_q + 1, 0);
-  const int all_tiles = div_up(kv_end, kTokens);
-  const int per = max(div_up(all_tiles, sp.per_tile), 2);
-  const int parts = max(div_up(all_tiles, per), 1);
-  if (part >= parts) return;
-  const int tile0 = part * per, n_tiles = min(per, all_tiles - tile0);
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, kSoftmaxWarps);
@@ -677,44 +689,36 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
-  if (parts == 1) return;
-
-  // ---- join the parts: the last CTA to arrive, in the order of the parts ----
-  // (also after an abort, so that the count is whole again)
-  if (threadIdx.x == 0) {
-    int seen;
-    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
-                 : "=r"(seen)
-                 : "l"(sp.arrived + ur)
-                 : "memory");
-    *s_last = seen == parts - 1;
-    if (seen == parts - 1) sp.arrived[ur] = 0;  // ready for the next call
-  }
-  __syncthreads();
-  if (!*s_last) return;
-  constexpr size_t kSlot = (D + 2) * kRows;
-  const float* first = sp.part + static_cast<size_t>(ur) * sp.per_tile * kSlot;
-  // a thread takes 8 values of a row
-  for (int x = threadIdx.x; x < kRows * (D / kPer); x += kThreads) {
-    const int row = x % kRows, d0 = x / kRows * kPer;
-    if (row >= rows) continue;
-    const float* from = first + row;
-    float mm = -INFINITY, y[kPer], s = 0.f;
-    for (int w = 0; w < parts; ++w) mm = fmaxf(mm, __ldcg(from + w * kSlot));
-    const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) y[k] = 0.f;
-#pragma unroll 2
-    for (int w = 0; w < parts; ++w) {
-      const float* pw = from + w * kSlot;
-      const float f = ex2(__ldcg(pw) - ref);
-      s += f * __ldcg(pw + kRows);
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) y[k] += f * __ldcg(pw + (2 + d0 + k) * kRows);
-    }
-    write_row(c, a, l, b, h, r0 + row, nq, d0, y, mm, s);
-  }
 #endif
+}
+
+// Joins the parts of a row tile, in their order: 128 rows x kJoin values of a CTA, so
+// that many SMs read the parts.  (One CTA alone took longer for it than the parts'
+// own work on 16 heads of 16384 tokens.)
+constexpr int kJoin = 8;
+template <int D>
+__global__ void __launch_bounds__(kRows) attend_many_join_kernel(Cache c, AttendArgs a, Parts sp) {
+  static_assert(kJoin == kPer, "write_row takes kPer values");
+  const RowTile w = row_tile(c, a, sp, blockIdx.x);
+  const int row = threadIdx.x, d0 = blockIdx.y * kJoin;
+  if (w.parts <= 1 || row >= w.rows) return;
+  constexpr size_t kSlot = (D + 2) * kRows;
+  const float* from = sp.part + static_cast<size_t>(blockIdx.x) * sp.per_tile * kSlot + row;
+  float m = -INFINITY, sum = 0.f, y[kJoin];
+#pragma unroll 8
+  for (int k = 0; k < w.parts; ++k) m = fmaxf(m, from[k * kSlot]);
+  const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+  for (int x = 0; x < kJoin; ++x) y[x] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < w.parts; ++k) {
+    const float* p = from + k * kSlot;
+    const float f = ex2(p[0] - ref);
+    sum += f * p[kRows];
+#pragma unroll
+    for (int x = 0; x < kJoin; ++x) y[x] += f * p[(2 + d0 + x) * kRows];
+  }
+  write_row(c, a, w.l, w.b, w.h, w.r0 + row, w.nq, d0, y, m, sum);
 }
 
 template <int D, int FMT>
@@ -725,13 +729,15 @@ cudaError_t launch_many(const Cache& c, const AttendArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   Parts sp;
   sp.row_tiles = (a.G * a.n + kRows - 1) / kRows;
-  sp.arrived = static_cast<int*>(a.workspace);
-  sp.part = reinterpret_cast<float*>(sp.arrived + kCounters);
+  sp.part = reinterpret_cast<float*>(static_cast<int*>(a.workspace) + kCounters);
   const long long tiles = static_cast<long long>(c.L) * c.B * c.H * sp.row_tiles;
   long long per = min(2 * a.num_sms, kMaxParts) / tiles;
   sp.per_tile = static_cast<int>(per < 1 ? 1 : per);
   kernel<<<static_cast<int>(tiles * sp.per_tile), kThreads, Smem<D>::kBytes, s>>>(c, a, sp,
                                                                                   make_div(c.bs));
+  const cudaError_t launched = cudaGetLastError();
+  if (launched != cudaSuccess || sp.per_tile == 1) return launched;
+  attend_many_join_kernel<D><<<dim3(static_cast<int>(tiles), D / kJoin), kRows, 0, s>>>(c, a, sp);
   return cudaGetLastError();
 }
 

@@ -20,6 +20,12 @@ def _need_cuda():
         pytest.skip("needs a CUDA GPU")
 
 
+# Room in the table beyond what a test's sequences need: which of the attention kernels a call goes
+# to depends on the table's capacity, and with this much room calls of more than 32 query rows go to
+# the one for many.
+ROOM = [1, 64]
+
+
 def _ints(x):
     return torch.as_tensor(np.asarray(x, np.int32)).cuda()
 
@@ -28,9 +34,10 @@ class Pair:
     """A model cache and the same one on the GPU."""
 
     def __init__(self, L, B, H, d, bs, max_blocks, fmt, n_blocks=None, seed=0, G=1, window=8,
-                 budget=32, max_T=512, **cfg):
+                 budget=32, max_T=512, room=1, **cfg):
         import eviction_gb300 as kvc
         n_blocks = n_blocks or B * max_blocks + 3
+        max_blocks *= room
         self.rng = np.random.default_rng(seed)
         self.ref = cr.RefCache(L, B, H, d, n_blocks, bs, max_blocks, fmt)
         self.ref.free_list[:] = self.rng.permutation(n_blocks)
@@ -188,24 +195,29 @@ def test_append_skips_what_it_cannot_write():
                                         (64, 2, 3, 64, 2), (128, 2, 8, 24, 3), (64, 1, 5, 8, 8),
                                         (128, 1, 13, 16, 1), (64, 1, 2, 1, 5), (128, 1, 7, 16, 37),
                                         (64, 2, 4, 16, 64), (128, 1, 3, 130, 128)])
-def test_attend_matches_model(fmt, d, H, G, bs, n):
+@pytest.mark.parametrize("room", ROOM)
+def test_attend_matches_model(fmt, d, H, G, bs, n, room):
+    if room > 1 and G * n <= 32:
+        pytest.skip("the kernel for few queries either way")
     lens = [0, 1, n, 130, 131 + n, 64, 16, 95]
-    p = Pair(2, len(lens), H, d, bs, -(-300 // bs), fmt, G=G, window=128, seed=n + bs)
+    p = Pair(2, len(lens), H, d, bs, -(-300 // bs), fmt, G=G, window=128, seed=n + bs, room=room)
     p.fill(lens)
     p.attend(n, token_major=bool(bs % 2))
 
 
 @pytest.mark.parametrize("n,n_q", [(5, [0, 1, 5, 3, 2]), (40, [40, 0, 17, 1, 33])])
-def test_attend_ragged_queries(n, n_q):
-    p = Pair(1, 5, 2, 128, 16, 8, "e4m3", G=3, window=64)
+@pytest.mark.parametrize("room", ROOM)
+def test_attend_ragged_queries(n, n_q, room):
+    p = Pair(1, 5, 2, 128, 16, 8, "e4m3", G=3, window=64, room=room)
     p.fill([100, 50, 17, 1, 16])
     p.attend(n, n_q=n_q)
     p.attend(n, n_q=n_q, token_major=True, lse=False)
 
 
-def test_attend_queries_before_the_first_token():
+@pytest.mark.parametrize("G,room", [(2, 1), (8, 1), (8, 1024)])
+def test_attend_queries_before_the_first_token(G, room):
     """More queries than tokens: the first ones see nothing and get zeros."""
-    p = Pair(1, 3, 1, 64, 16, 4, "int8", G=2, window=16)
+    p = Pair(1, 3, 1, 64, 16, 4, "int8", G=G, window=16, room=room)
     p.fill([3, 0, 9])
     q, out, lse = p.attend(9)
     assert (out[0, 0, :, :6] == 0).all() and (out[0, 1] == 0).all()
@@ -214,18 +226,23 @@ def test_attend_queries_before_the_first_token():
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("H,G,bs,lens,n", [(1, 1, 16, [3000], 1), (2, 7, 64, [2500, 7, 1777], 1),
-                                           (1, 4, 7, [1999, 1024, 1025], 2), (1, 8, 16, [2048], 20)])
-def test_attend_long(fmt, H, G, bs, lens, n):
-    p = Pair(1, len(lens), H, 128, bs, -(-max(lens) // bs), fmt, G=G, window=32)
+                                           (1, 4, 7, [1999, 1024, 1025], 2), (1, 8, 16, [2048], 20),
+                                           (2, 7, 16, [3000, 1, 2047], 20)])
+@pytest.mark.parametrize("room", ROOM)
+def test_attend_long(fmt, H, G, bs, lens, n, room):
+    if room > 1 and G * n <= 32:
+        pytest.skip("the kernel for few queries either way")
+    p = Pair(1, len(lens), H, 128, bs, -(-max(lens) // bs), fmt, G=G, window=32, room=room)
     p.fill(lens)
     p.attend(n)
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("B,H,longest,n", [(100, 2, 300, 1), (70, 1, 900, 2), (33, 1, 60, 20), (3, 1, 6000, 1)])
-def test_attend_many_and_uneven_sequences(fmt, B, H, longest, n):
+@pytest.mark.parametrize("G", [1, 2])
+def test_attend_many_and_uneven_sequences(fmt, B, H, longest, n, G):
     """Heads cut anywhere: lengths from nothing to the longest, some sequences without queries."""
-    p = Pair(1, B, H, 64, 16, -(-longest // 16), fmt, window=32, seed=B)
+    p = Pair(1, B, H, 64, 16, -(-longest // 16), fmt, window=32, seed=B, G=G, room=1 if G == 1 else 64)
     lens = p.rng.integers(0, longest + 1, B) * (p.rng.random(B) < 0.8)
     lens[0], lens[-1] = longest, 1
     p.fill(lens.tolist())
@@ -236,10 +253,10 @@ def test_attend_many_and_uneven_sequences(fmt, B, H, longest, n):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
-@pytest.mark.parametrize("n", [1, 40])
-def test_attend_scales_far_apart(fmt, n):
+@pytest.mark.parametrize("n,room", [(1, 1), (40, 1), (40, 64)])
+def test_attend_scales_far_apart(fmt, n, room):
     """Blocks whose value scales lie 2^60 apart, and sharp softmaxes."""
-    p = Pair(1, 2, 1, 64, 8, 30, fmt, G=2, window=64)
+    p = Pair(1, 2, 1, 64, 8, 30, fmt, G=2, window=64, room=room)
     p.fill([200, 123])
     for w, lo, hi in ((0, -3, 1), (1, -50, 10)):
         p.ref.scale[w] *= 2.0 ** p.rng.integers(lo, hi, p.ref.scale[w].shape)
@@ -249,10 +266,10 @@ def test_attend_scales_far_apart(fmt, n):
     p.attend(n, q_scale=1e-4)
 
 
-@pytest.mark.parametrize("n", [1, 5, 40])
-def test_attend_reads_nothing_behind_a_sequence(n):
+@pytest.mark.parametrize("n,room", [(1, 1), (5, 1), (40, 1), (40, 64)])
+def test_attend_reads_nothing_behind_a_sequence(n, room):
     """NaN codes past the end and in free blocks change nothing; -1 past the table's blocks is fine."""
-    p = Pair(1, 3, 2, 128, 16, 12, "e4m3", G=4, window=64, seed=3)
+    p = Pair(1, 3, 2, 128, 16, 12, "e4m3", G=4, window=64, seed=3, room=room)
     p.fill([n + 3, 100, 33])
     for w in (0, 1):
         used = np.zeros(p.ref.pool[w].shape[1:4:2], bool)  # [n_blocks, bs]
@@ -264,9 +281,10 @@ def test_attend_reads_nothing_behind_a_sequence(n):
     p.attend(n)
 
 
-def test_attend_infinite_and_nan_queries():
+@pytest.mark.parametrize("G,room", [(2, 1), (10, 1), (10, 1024)])
+def test_attend_infinite_and_nan_queries(G, room):
     """A query row that is not finite spoils its own output only."""
-    p = Pair(1, 1, 1, 64, 16, 8, "e4m3", G=2, window=8)
+    p = Pair(1, 1, 1, 64, 16, 8, "e4m3", G=G, window=8, room=room)
     p.fill([70])
     q, out, _ = p.attend(4)
     q2 = q.clone()
@@ -274,21 +292,21 @@ def test_attend_infinite_and_nan_queries():
     q2[0, 0, 0, 3, 5] = float("inf")
     out2 = torch.zeros_like(out)
     p.h.cache8_attend(p.c, q2, out2)
-    spoilt = torch.zeros(2, 4, dtype=torch.bool, device="cuda")
+    spoilt = torch.zeros(G, 4, dtype=torch.bool, device="cuda")
     spoilt[1, 2] = spoilt[0, 3] = True
     assert torch.isnan(out2[0, 0, 1, 2]).all()
     assert torch.equal(out2[0, 0][~spoilt], out[0, 0][~spoilt])
 
 
-@pytest.mark.parametrize("n", [1, 40])
-def test_attend_bad_pages_are_absent(n):
+@pytest.mark.parametrize("n,room", [(1, 1), (40, 1), (40, 256)])
+def test_attend_bad_pages_are_absent(n, room):
     """Tokens in a block out of range do not count; bad lengths and counts are skipped."""
-    p = Pair(1, 4, 1, 64, 16, 8, "int8", G=2, window=64)
+    p = Pair(1, 4, 1, 64, 16, 8, "int8", G=2, window=64, room=room)
     p.fill([60, 60, 60, 60])
     good = p.ref.table.copy()
     p.ref.table[0, 3] = 10 ** 7   # the last block: 12 tokens
     p.ref.table[1, 3] = -1
-    p.ref.len[2] = 1000           # above max_blocks * block_size
+    p.ref.len[2] = 16 * 8 * room + 1  # above max_blocks * block_size
     p.ref.len[3] = -7
     p.sync_up()
     q = torch.from_numpy(p.rng.standard_normal((1, 4, 2, n, 64))).to(torch.bfloat16).cuda()
@@ -311,8 +329,9 @@ def test_attend_bad_pages_are_absent(n):
     assert p.h.device_status() == cr.BAD_INDEX and (out == 7.0).all()
 
 
-def test_attend_is_repeatable():
-    p = Pair(1, 3, 2, 128, 16, 130, "e4m3", G=7, window=64)
+@pytest.mark.parametrize("room", ROOM)
+def test_attend_is_repeatable(room):
+    p = Pair(1, 3, 2, 128, 16, 130, "e4m3", G=7, window=64, room=room)
     p.fill([2000, 500, 1])
     for n in (1, 3, 50):
         q, out, lse = p.attend(n) if n == 1 else (torch.randn((1, 3, 14, n, 128), device="cuda").to(
