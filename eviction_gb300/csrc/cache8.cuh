@@ -69,6 +69,31 @@ cudaError_t launch_attend(const Cache& c, int format, const AttendArgs& a, cudaS
 
 #if defined(__CUDACC__)
 
+// Every kernel of the cache may be launched while the one before it on the stream still
+// runs (a decode step is a chain of kernels of a few microseconds: their launch
+// latencies overlap).  before_all() comes first in a kernel: nothing is read or written
+// until that one has completed and its writes are visible; the next kernel's launch
+// may begin then.
+__device__ __forceinline__ void before_all() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class... Params, class... Args>
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t s,
+                   Args... args) {
+  cudaLaunchAttribute overlap;
+  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  overlap.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 __device__ __forceinline__ float exp2_int(int e) {  // 2^e, -126 <= e <= 127
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }

@@ -146,6 +146,8 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
   const int g = lane / 4, q4 = lane % 4;
   bool bad = false, unused = false;
 
+  before_all();
+
   // ---- this CTA's work: steps [begin, ...) of a head, `left` steps in all ----
   // (every warp computes it for itself; all counts are below 2^31, checked on the host)
   const int heads = c.H * sp.row_tiles;  // of one sequence and layer
@@ -650,8 +652,7 @@ cudaError_t launch_few(const Cache& c, const AttendArgs& a, const Split& sp, cud
   const cudaError_t e = allow_smem(kernel, smem, told);
   if (e != cudaSuccess) return e;
   const int grid = min(a.num_sms * (kSmWarps / W), kMaxCtas);
-  kernel<<<grid, 32 * W, smem, s>>>(c, a, sp, make_div(c.bs));
-  return cudaGetLastError();
+  return launch(kernel, grid, 32 * W, smem, s, c, a, sp, make_div(c.bs));
 }
 
 template <int D, int FMT>

@@ -197,6 +197,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int* abort = reinterpret_cast<volatile int*>(smem + Sm::kMisc + 4);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
+  before_all();
+
   // ---- this CTA's row tile and tokens ----
   const int part = blockIdx.x % sp.per_tile;
   const RowTile w = row_tile(c, a, sp, blockIdx.x / sp.per_tile);
@@ -699,6 +701,7 @@ constexpr int kJoin = 8;
 template <int D>
 __global__ void __launch_bounds__(kRows) attend_many_join_kernel(Cache c, AttendArgs a, Parts sp) {
   static_assert(kJoin == kPer, "write_row takes kPer values");
+  before_all();
   const RowTile w = row_tile(c, a, sp, blockIdx.x);
   const int row = threadIdx.x, d0 = blockIdx.y * kJoin;
   if (w.parts <= 1 || row >= w.rows) return;
@@ -725,7 +728,7 @@ template <int D, int FMT>
 cudaError_t launch_many(const Cache& c, const AttendArgs& a, cudaStream_t s) {
   auto* kernel = attend_many_kernel<D, FMT>;
   static std::atomic<uint64_t> told{0};
-  const cudaError_t e = allow_smem(kernel, Smem<D>::kBytes, told);
+  cudaError_t e = allow_smem(kernel, Smem<D>::kBytes, told);
   if (e != cudaSuccess) return e;
   Parts sp;
   sp.row_tiles = (a.G * a.n + kRows - 1) / kRows;
@@ -733,12 +736,11 @@ cudaError_t launch_many(const Cache& c, const AttendArgs& a, cudaStream_t s) {
   const long long tiles = static_cast<long long>(c.L) * c.B * c.H * sp.row_tiles;
   long long per = min(2 * a.num_sms, kMaxParts) / tiles;
   sp.per_tile = static_cast<int>(per < 1 ? 1 : per);
-  kernel<<<static_cast<int>(tiles * sp.per_tile), kThreads, Smem<D>::kBytes, s>>>(c, a, sp,
-                                                                                  make_div(c.bs));
-  const cudaError_t launched = cudaGetLastError();
-  if (launched != cudaSuccess || sp.per_tile == 1) return launched;
-  attend_many_join_kernel<D><<<dim3(static_cast<int>(tiles), D / kJoin), kRows, 0, s>>>(c, a, sp);
-  return cudaGetLastError();
+  e = launch(kernel, static_cast<int>(tiles * sp.per_tile), kThreads, Smem<D>::kBytes, s, c, a, sp,
+             make_div(c.bs));
+  if (e != cudaSuccess || sp.per_tile == 1) return e;
+  return launch(attend_many_join_kernel<D>, dim3(static_cast<int>(tiles), D / kJoin), kRows, 0, s, c,
+                a, sp);
 }
 
 }  // namespace

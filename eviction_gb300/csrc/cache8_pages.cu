@@ -77,6 +77,7 @@ __device__ __forceinline__ Place place_of(const int* ends, int e) {
 __global__ void __launch_bounds__(kThreads, 1) grow_kernel(Cache c, const int32_t* n_new) {
   __shared__ int ends[kSeqs], have[kSeqs];
   const int t = threadIdx.x;
+  before_all();
   const int top = *c.free_top;
   bool bad = top < 0 || top > c.n_blocks;
   long long need_all = 0;  // of this thread's sequences
@@ -285,6 +286,7 @@ __device__ __noinline__ void free_many(const Cache& c, int n, const int32_t* seq
 __global__ void __launch_bounds__(kThreads, 1) free_kernel(Cache c, int n, const int32_t* seqs) {
   __shared__ int ends[kSeqs], numbers[kSeqs];
   __shared__ uint32_t marks[kMarkBits / 32];
+  before_all();
   if (n > kSeqs || c.B > kMarkBits) {
     free_many(c, n, seqs, ends, marks);
     return;
@@ -397,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int ends[kSeqs], part[kSeqs];
   __shared__ uint32_t marks[kMarkBits / 32];
   const int t = threadIdx.x;
+  before_all();
   if (t == 0) *c.err = 0;
   const int top = *c.free_top;
   bool bad = top < 0 || top > c.n_blocks;
@@ -504,6 +507,7 @@ constexpr int kCopyUnroll = 8;
 // layers a CTA that all are resident at once.)
 __global__ void __launch_bounds__(kCopyThreads, 3)
     fork_copy_kernel(Cache c, int layers, const int32_t* src, const int32_t* dst) {
+  before_all();
   const int s = src[blockIdx.x], d = dst[blockIdx.x];
   if (*c.err) return;  // refused: the numbers may be out of range
   const int len = c.seq_len[d];
@@ -543,25 +547,22 @@ __global__ void __launch_bounds__(kCopyThreads, 3)
 }  // namespace
 
 cudaError_t launch_grow(const Cache& c, const int32_t* n_new, cudaStream_t s) {
-  grow_kernel<<<1, kThreads, 0, s>>>(c, n_new);
-  return cudaGetLastError();
+  return launch(grow_kernel, 1, kThreads, 0, s, c, n_new);
 }
 
 cudaError_t launch_free(const Cache& c, int n, const int32_t* seqs, cudaStream_t s) {
-  free_kernel<<<1, kThreads, 0, s>>>(c, n, seqs);
-  return cudaGetLastError();
+  return launch(free_kernel, 1, kThreads, 0, s, c, n, seqs);
 }
 
 cudaError_t launch_fork(const Cache& c, int n, const int32_t* src, const int32_t* dst,
                         int num_sms, cudaStream_t s) {
-  fork_kernel<<<1, kThreads, 0, s>>>(c, n, src, dst);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch(fork_kernel, 1, kThreads, 0, s, c, n, src, dst);
   if (e != cudaSuccess) return e;
   // three CTAs an SM, and gridDim.y is at most 65535
   const long long share = static_cast<long long>(n) * c.L / (3 * num_sms);
   const int layers = static_cast<int>(max(max(share, static_cast<long long>(c.L) / 65535 + 1), 1ll));
-  fork_copy_kernel<<<dim3(n, (c.L + layers - 1) / layers), kCopyThreads, 0, s>>>(c, layers, src, dst);
-  return cudaGetLastError();
+  return launch(fork_copy_kernel, dim3(n, (c.L + layers - 1) / layers), kCopyThreads, 0, s, c, layers,
+                src, dst);
 }
 
 }  // namespace cache8

@@ -95,6 +95,7 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(32 * kWarps)
     append_kernel(Cache c, Rows k_new, Rows v_new, int n, int per_seq, const int32_t* n_new) {
   constexpr int CH = D / 8;  // 16-byte chunks of a bf16 row
+  before_all();
   const int lane = threadIdx.x % 32;
   const uint32_t task = blockIdx.x * kWarps + threadIdx.x / 32;
   // heads fastest: the rows of a token-major source then lie side by side
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(kGatherThreads)
     gather_kernel(Cache c, int T, int ctas_per_unit, uint16_t* k_out, uint16_t* v_out,
                   int32_t* pad_out) {
   constexpr int CH = D / 8;
+  before_all();
   const int u = blockIdx.x / ctas_per_unit;
   const int part = blockIdx.x % ctas_per_unit;
   const int h = u % c.H, b = (u / c.H) % c.B, l = u / (c.H * c.B);
@@ -295,6 +297,7 @@ __global__ void __launch_bounds__(kCompactThreads, 4)
   constexpr int KEEP = kKeepRows / RPI;
   __shared__ int s_row[kLookRows];               // place in the pools (rows of d codes from the
   __shared__ float s_scale[2][kLookRows];        // layer's first, of this head); -1: none
+  before_all();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int ch = lane % CH;
   const int u = blockIdx.x / per_unit;
@@ -405,8 +408,7 @@ cudaError_t launch_append(const Cache& c, int format, const Rows& k, const Rows&
                                                         : append_kernel<64, KVC_CACHE8_INT8>)
                            : (format == KVC_CACHE8_E4M3 ? append_kernel<128, KVC_CACHE8_E4M3>
                                                         : append_kernel<128, KVC_CACHE8_INT8>);
-  kernel<<<grid, 32 * kWarps, 0, s>>>(c, k, v, n, per_seq, n_new);
-  return cudaGetLastError();
+  return launch(kernel, grid, 32 * kWarps, 0, s, c, k, v, n, per_seq, n_new);
 }
 
 cudaError_t launch_gather(const Cache& c, int format, int T, uint16_t* k_out, uint16_t* v_out,
@@ -418,8 +420,7 @@ cudaError_t launch_gather(const Cache& c, int format, int T, uint16_t* k_out, ui
                                                         : gather_kernel<64, KVC_CACHE8_INT8>)
                            : (format == KVC_CACHE8_E4M3 ? gather_kernel<128, KVC_CACHE8_E4M3>
                                                         : gather_kernel<128, KVC_CACHE8_INT8>);
-  kernel<<<grid, kGatherThreads, 0, s>>>(c, T, per_unit, k_out, v_out, pad);
-  return cudaGetLastError();
+  return launch(kernel, grid, kGatherThreads, 0, s, c, T, per_unit, k_out, v_out, pad);
 }
 
 template <int D>
@@ -432,8 +433,7 @@ static cudaError_t launch_compact_d(const Cache& c, int from, const Cache& to, i
   constexpr int E = KVC_CACHE8_E4M3, I = KVC_CACHE8_INT8;
   auto* kernel = from == E ? (to_format == E ? compact_kernel<D, E, E> : compact_kernel<D, E, I>)
                            : (to_format == E ? compact_kernel<D, I, E> : compact_kernel<D, I, I>);
-  kernel<<<grid, kCompactThreads, 0, s>>>(c, to, a, per_unit, blocks);
-  return cudaGetLastError();
+  return launch(kernel, grid, kCompactThreads, 0, s, c, to, a, per_unit, blocks);
 }
 
 cudaError_t launch_compact(const Cache& src, int src_format, const Cache& dst, int dst_format,
