@@ -137,12 +137,17 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
     return;
   }
+  const int holders = c.ref_count[blk];
   float* scale_ptr = (values ? c.scale[1] : c.scale[0]) + scale_at(c, l, blk, h);
   const float old = lo > first ? *scale_ptr : 0.f;
 #pragma unroll
   for (int s = 0; s < kKeep; ++s) m = max_abs8(keep[s], m);
   for (int idx = lane + 32 * kKeep; idx < total; idx += 32) m = max_abs8(load(idx), m);
   m = warp_max_half(m);
+  if (holders != 1) {  // a shared block is never written
+    if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
+    return;
+  }
   if (m >= 0x7f80u) {  // an infinity or a NaN: the finite values alone give the scale
     if (lane == 0) report(c, KVC_STATUS_NONFINITE);
     m = 0;
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(kCompactThreads, 4)
     const int rows = min(nk - j0 - jb * to.bs, to.bs);
     if (rows <= 0) break;
     const int new_blk = block_at(to, b, jb0 + jb);
-    if (new_blk < 0) {
+    if (new_blk < 0 || to.ref_count[new_blk] != 1) {  // (a shared block is never written)
       bad = true;
       continue;
     }

@@ -467,9 +467,10 @@ class Handle:
 
     def _ints(self, t, name, shape, device):
         import torch
-        if tuple(t.shape) != shape:
+        ptr = self._on(t, torch.int32, name, device)
+        if t.shape != shape:
             raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-        return self._on(t, torch.int32, name, device)
+        return ptr
 
     @staticmethod
     def _on(t, dtype, name, device):

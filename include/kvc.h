@@ -404,7 +404,7 @@ int kvc_refresh_decision(kvc_handle* h, const uint16_t* q, float* q_ref, float t
  *   free_list [n_blocks] int32, free_top [1] int32: entries [0, *free_top) are the
  *             free blocks, a stack
  *   ref_count [n_blocks] int32: sequences that hold the block.  A block that is
- *             not full is never shared.
+ *             not full is never shared, and a shared one is never written.
  * B, H, G and d come from the handle; sequences may be longer than max_T.
  * block_size 1..1024; n_blocks * H * block_size and B * max_blocks < 2^31,
  * max_blocks * block_size <= 2^30.
@@ -466,7 +466,8 @@ int kvc_cache8_grow(kvc_handle* h, const kvc_cache8* c, const int32_t* n_new, vo
  * then rounded to the new scale.  Writing the same rows again changes nothing.
  *   k, v   [n_layers][B][H][n][d] bf16 rows
  *   n_new  [B] int32, 0..n (rows past it are not read); a sequence whose count
- *          is out of range, or above its seq_len, is skipped (BAD_INDEX) */
+ *          is out of range, or above its seq_len, is skipped, and so is a block
+ *          that is out of range or whose ref_count is not 1 (BAD_INDEX) */
 int kvc_cache8_append(kvc_handle* h, const kvc_cache8* c, const kvc_rows* k, const kvc_rows* v,
                       int n, const int32_t* n_new, void* stream);
 
@@ -507,15 +508,16 @@ int kvc_cache8_gather(kvc_handle* h, const kvc_cache8* c, int T, uint16_t* k_out
  *                  n_kept must equal dst's seq_len[b], else the unit is skipped
  *   credit_post [n_layers][B][H][T] -> credit_out [n_layers][B][H][budget], as in
  *                  kvc_compact (zero past n_kept); both may be NULL
- * An index outside the sequence writes a zero row (BAD_INDEX). */
+ * An index outside the sequence writes a zero row, a block of dst that is out of
+ * range or whose ref_count is not 1 is skipped (BAD_INDEX). */
 int kvc_cache8_compact(kvc_handle* h, const kvc_cache8* src, const kvc_cache8* dst, int T,
                        const int32_t* pad, const int32_t* kept_idx, const int32_t* n_kept,
                        const float* credit_post, float* credit_out, void* stream);
 
 /* Start sequences dst[i] (empty, all different) from the caches of src[i] (which
  * may repeat): full blocks are shared (ref_count + 1), the rows of a started block
- * are copied, in all n_layers layers, into a block from the free stack (in list
- * order, as in grow).
+ * are copied, in the n_layers layers of c (the whole cache's), into a block from the
+ * free stack (in list order, as in grow).
  *   src, dst  [n] int32 sequence numbers; n = 0 does nothing
  * Changes nothing, with a status bit, where a number or block is out of range, a
  * dst repeats, is not empty or is also a src, or the stack is too short. */

@@ -172,7 +172,7 @@ class RefCache:
             for i in range(start // self.bs, self.blocks(end) if n else 0):
                 lo, hi = max(i * self.bs, start), min(end, (i + 1) * self.bs)
                 blk = self.table[b, i]
-                if not 0 <= blk < self.N:
+                if not 0 <= blk < self.N or self.ref[blk] != 1:
                     status |= BAD_INDEX
                     continue
                 for l in range(self.L):
@@ -241,6 +241,9 @@ class RefCache:
                             r = x[i * dst.bs:(i + 1) * dst.bs]
                             s = scale_of(r, dst.fmt)
                             blk = dst.table[b, i]
+                            if not 0 <= blk < dst.N or dst.ref[blk] != 1:
+                                status |= BAD_INDEX
+                                continue
                             dst.pool[w][l, blk, h, :len(r)] = encode(r / s, dst.fmt)
                             dst.scale[w][l, blk, h] = s
         return status
