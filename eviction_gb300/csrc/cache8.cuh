@@ -110,11 +110,13 @@ __device__ __forceinline__ int scale_exp(float amax) {
 }
 
 // The nearest codes of a (low byte) and b, which are in units of the scale.
-// NaN becomes 0, what is too large the largest code.
-template <int FMT>
+// NaN becomes 0 (if NAN_TOO), what is too large the largest code.
+template <int FMT, bool NAN_TOO = true>
 __device__ __forceinline__ uint32_t encode2(float a, float b) {
-  a = a == a ? a : 0.f;
-  b = b == b ? b : 0.f;
+  if constexpr (NAN_TOO) {
+    a = a == a ? a : 0.f;
+    b = b == b ? b : 0.f;
+  }
   if constexpr (FMT == KVC_CACHE8_E4M3) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));

@@ -500,12 +500,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyUnroll = 8;
+constexpr int kCopyUnroll = 4;
+constexpr int kCopyCtas = 6;  // of an SM
 
 // One CTA: the started block of one new sequence in some layers, all heads, keys and
-// values.  (Finding the blocks takes four loads that wait for one another: so many
-// layers a CTA that all are resident at once.)
-__global__ void __launch_bounds__(kCopyThreads, 3)
+// values.  Finding the blocks takes four loads that wait for one another: each CTA has
+// so many layers that all CTAs are resident at once.  (64 sequences, 28 layers, started
+// blocks of 32 rows on average, with the two launches before it: 32 us; 38 at 3 CTAs of
+// 8 loads a thread, 46 with a CTA for each layer.)
+__global__ void __launch_bounds__(kCopyThreads, kCopyCtas)
     fork_copy_kernel(Cache c, int layers, const int32_t* src, const int32_t* dst) {
   before_all();
   const int s = src[blockIdx.x], d = dst[blockIdx.x];
@@ -558,8 +561,8 @@ cudaError_t launch_fork(const Cache& c, int n, const int32_t* src, const int32_t
                         int num_sms, cudaStream_t s) {
   const cudaError_t e = launch(fork_kernel, 1, kThreads, 0, s, c, n, src, dst);
   if (e != cudaSuccess) return e;
-  // three CTAs an SM, and gridDim.y is at most 65535
-  const long long share = static_cast<long long>(n) * c.L / (3 * num_sms);
+  // as many CTAs as are resident at once, and gridDim.y is at most 65535
+  const long long share = static_cast<long long>(n) * c.L / (kCopyCtas * num_sms);
   const int layers = static_cast<int>(max(max(share, static_cast<long long>(c.L) / 65535 + 1), 1ll));
   return launch(fork_copy_kernel, dim3(n, (c.L + layers - 1) / layers), kCopyThreads, 0, s, c, layers,
                 src, dst);

@@ -48,12 +48,12 @@ __device__ __forceinline__ uint32_t warp_max_half(uint32_t m) {
 }
 
 // 8 bf16 values to 8 codes.
-template <int FMT>
+template <int FMT, bool NAN_TOO>
 __device__ __forceinline__ uint2 encode8(uint4 v, float inv) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t r[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = encode2<FMT>(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+  for (int i = 0; i < 4; ++i) r[i] = encode2<FMT, NAN_TOO>(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
   return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
 
@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
     return;
   }
-  if (m >= 0x7f80u) {  // an infinity or a NaN: the finite values alone give the scale
+  const bool finite_rows = m < 0x7f80u;
+  if (!finite_rows) {  // an infinity or a NaN: the finite values alone give the scale
     if (lane == 0) report(c, KVC_STATUS_NONFINITE);
     m = 0;
     for (int idx = lane; idx < total; idx += 32) m = max_abs8_finite(load(idx), m);
@@ -169,12 +170,17 @@ __global__ void __launch_bounds__(32 * kWarps)
   }
   const float inv = 1.f / scale;  // exact
   uint2* to = reinterpret_cast<uint2*>(rows + static_cast<size_t>(lo - first) * D);
+  if (finite_rows) {
 #pragma unroll
-  for (int s = 0; s < kKeep; ++s) {
-    const int idx = lane + 32 * s;
-    if (idx < total) to[idx] = encode8<FMT>(keep[s], inv);
+    for (int s = 0; s < kKeep; ++s) {
+      const int idx = lane + 32 * s;
+      if (idx < total) to[idx] = encode8<FMT, false>(keep[s], inv);
+    }
+    for (int idx = lane + 32 * kKeep; idx < total; idx += 32)
+      to[idx] = encode8<FMT, false>(load(idx), inv);
+  } else {
+    for (int idx = lane; idx < total; idx += 32) to[idx] = encode8<FMT, true>(load(idx), inv);
   }
-  for (int idx = lane + 32 * kKeep; idx < total; idx += 32) to[idx] = encode8<FMT>(load(idx), inv);
   if (lane == 0) *scale_ptr = scale;
 }
 
