@@ -187,13 +187,13 @@ int kvc_cache8_attend(kvc_handle* h, const kvc_cache8* c, const kvc_rows* q, int
     const long long rows_all = static_cast<long long>(c->n_layers) * h->dims.B * Hq * n;
     if (rows_all > INT_MAX)
       return fail(h, KVC_ERR_UNSUPPORTED, "n_layers * batch * query heads * n must be < 2^31");
-    // (the kernels count rows of 8 query rows by steps of 32 tokens)
+    // (the kernels count 8 query rows by steps of 32 tokens, and a few more a head)
     if (static_cast<long long>(c->n_layers) * h->dims.B * h->dims.H *
             ((static_cast<long long>(h->dims.G) * n + 7) / 8) *
-            ((static_cast<long long>(c->max_blocks) * c->block_size + 31) / 32) >
+            ((static_cast<long long>(c->max_blocks) * c->block_size + 31) / 32 + 8) >
         INT_MAX / 2)
       return fail(h, KVC_ERR_UNSUPPORTED, "n_layers * batch * n_kv_heads * ceil(G n / 8) * "
-                                          "ceil(max_blocks * block_size / 32) must be < 2^30");
+                                          "(max_blocks * block_size / 32 + 8) must be < 2^30");
     kvc::cache8::AttendArgs a{rows(*q), rows(*out), lse, n_q, n, h->dims.G,
                               kvc::scale_log2_of(h->cfg), h->num_sms, h->ws.attend};
     return run(h, kvc::kKernelCache8Attend, "cache8 attend", stream, [&](cudaStream_t s) {

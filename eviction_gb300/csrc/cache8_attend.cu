@@ -31,7 +31,8 @@
 //
 // Work is the list of all heads' steps of 32 tokens, one after another.  Many heads:
 // small CTAs, three on an SM, take equal stretches of the list, whatever the lengths
-// are, and walk the heads that they meet.  Few heads: one large CTA per SM takes a
+// are, and walk the heads that they meet (a head counts as a few steps more than it has,
+// what it takes to begin and end it).  Few heads: one large CTA per SM takes a
 // part of one head.  A head within one CTA is finished there; the parts of one that
 // is not go to the workspace, and the last CTA of it to finish joins them in order
 // (the result does not depend on which one that is).
@@ -47,6 +48,9 @@ constexpr int kStages = 2;
 constexpr int kSmWarps = 12;     // warps of an SM, by registers and shared memory
 constexpr int kMaxCtas = kCounters;  // CTAs of a call
 constexpr float kSlack = 8.f;    // log2 of how far a weight may pass 1
+// Steps that beginning and ending a head costs a small CTA (512 heads of 612 to 1112
+// tokens: 28.5 us at 0, 27.6 at 4, 26.7 at 8, 27.0 at 12).
+constexpr int kHeadCost = 8;
 constexpr int kMinRounds = 3;    // steps of a CTA's warps at least, before a head is cut
 
 struct Split {
@@ -195,6 +199,10 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
       before += chunk;
     }
   };
+  // (in the list, each head of a small CTA's kernel has kHeadCost places before its steps)
+  constexpr int kCost = W == kSmWarps ? 0 : kHeadCost;
+  auto places = [](int n) { return n > 0 ? n + kCost : 0; };
+  if (kCost > 0) all += kCost * sum_over([](int n) { return n > 0; });
   const int n_cta = gridDim.x, total = all * heads * c.L;
   if (total == 0) return;
   int chunk = max(div_up(total, n_cta), kMinRounds * W);
@@ -224,18 +232,25 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
   } else {
     const int lo = blockIdx.x * chunk;
     if (static_cast<long long>(blockIdx.x) * chunk >= total) return;
-    left = min(chunk, total - lo);
     l = lo / (all * heads);
     int in;
-    b = find(lo % (all * heads), [](int n) { return n; }, &in, &steps);
-    head = in / steps;
-    begin = in % steps;
+    b = find(lo % (all * heads), places, &in, &steps);
+    head = in / (steps + kCost);
+    begin = in % (steps + kCost) - kCost;  // below 0: before the head's first step
+    left = min(chunk, total - lo);
   }
+
   uint8_t* ring = smem + warp * (kStages * St::kBytes);
   const uint32_t ring_addr = smem_u32(ring);
 
-  int at = blockIdx.x * chunk;  // place in the list
+  int at = blockIdx.x * chunk;  // place in the list, of step `begin`
   for (;;) {
+    if (begin < 0) {  // on to the first step, if it is this CTA's
+      left += begin;
+      at -= begin;
+      begin = 0;
+      if (left <= 0) break;
+    }
     const int h = head / sp.row_tiles, rt = head % sp.row_tiles;
     const int end = min(steps, begin + left);
     const int len = c.seq_len[b];
@@ -628,7 +643,7 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
     left -= end - begin;
     if (W == kSmWarps || left == 0) break;
     at += end - begin;
-    begin = 0;
+    begin = -kCost;
     if (++head == heads) {
       head = 0;
       do {
