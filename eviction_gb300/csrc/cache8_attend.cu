@@ -693,11 +693,11 @@ cudaError_t launch_few(const Cache& c, const AttendArgs& a, cudaStream_t s) {
 // Which kernel: this one reads a head's tokens once for each 16 query rows, the other
 // takes 128 rows at a time but starts and turns slower.  By the product of heads,
 // 16-row tiles and tokens (the table's capacity), this one / the other in us:
-//   4 heads x 2048 tokens, 112 rows (57 k)     19 / 24
-//   32 x 2048, 28 rows (131 k)                 24 / 25;   35 rows (197 k)  28 / 25
-//   128 x 1536, 28 rows (393 k)                36 / 38;   35 rows (590 k)  44 / 39
-//   16 x 16384, 28 rows (524 k)                42 / 48;   56 rows (1 M)    61 / 49
-//   512 x 860, 32 rows (881 k)                 70 / 66;   64 rows (1.8 M) 112 / 68
+//   4 heads x 2048 tokens, 112 rows (57 k)     17 / 19
+//   32 x 2048, 28 rows (131 k)                 17 / 23;   56 rows (262 k)  27 / 24
+//   128 x 1536, 28 rows (393 k)                32 / 35;   35 rows (590 k)  41 / 36
+//   16 x 16384, 28 rows (524 k)                33 / 44;   56 rows (1 M)    55 / 47
+//   512 x 860, 32 rows (881 k)                 65 / 65;   64 rows (1.8 M) 109 / 66
 constexpr int kFewRows = 32;
 constexpr long long kFewWork = 150'000;
 
