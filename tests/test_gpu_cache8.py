@@ -26,6 +26,12 @@ def _need_cuda():
 ROOM = [1, 64]
 
 
+def _both_kernels(cases):
+    """Each case (the last two values: heads of a group, queries) without room and, if it has more
+    than 32 query rows, with room."""
+    return [(*c, room) for c in cases for room in ROOM if room == 1 or c[-2] * c[-1] > 32]
+
+
 def _ints(x):
     return torch.as_tensor(np.asarray(x, np.int32)).cuda()
 
@@ -201,14 +207,11 @@ def test_shared_blocks_are_not_written():
 # ---- attend ----
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
-@pytest.mark.parametrize("d,H,G,bs,n", [(64, 1, 1, 16, 1), (128, 2, 7, 16, 1), (128, 1, 4, 5, 1),
-                                        (64, 2, 3, 64, 2), (128, 2, 8, 24, 3), (64, 1, 5, 8, 8),
-                                        (128, 1, 13, 16, 1), (64, 1, 2, 1, 5), (128, 1, 7, 16, 37),
-                                        (64, 2, 4, 16, 64), (128, 1, 3, 130, 128)])
-@pytest.mark.parametrize("room", ROOM)
-def test_attend_matches_model(fmt, d, H, G, bs, n, room):
-    if room > 1 and G * n <= 32:
-        pytest.skip("the kernel for few queries either way")
+@pytest.mark.parametrize("d,H,bs,G,n,room", _both_kernels([
+    (64, 1, 16, 1, 1), (128, 2, 16, 7, 1), (128, 1, 5, 4, 1), (64, 2, 64, 3, 2), (128, 2, 24, 8, 3),
+    (64, 1, 8, 5, 8), (128, 1, 16, 13, 1), (64, 1, 1, 2, 5), (128, 1, 16, 7, 37), (64, 2, 16, 4, 64),
+    (128, 1, 130, 3, 128)]))
+def test_attend_matches_model(fmt, d, H, bs, G, n, room):
     lens = [0, 1, n, 130, 131 + n, 64, 16, 95]
     p = Pair(2, len(lens), H, d, bs, -(-300 // bs), fmt, G=G, window=128, seed=n + bs, room=room)
     p.fill(lens)
@@ -235,13 +238,10 @@ def test_attend_queries_before_the_first_token(G, room):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
-@pytest.mark.parametrize("H,G,bs,lens,n", [(1, 1, 16, [3000], 1), (2, 7, 64, [2500, 7, 1777], 1),
-                                           (1, 4, 7, [1999, 1024, 1025], 2), (1, 8, 16, [2048], 20),
-                                           (2, 7, 16, [3000, 1, 2047], 20)])
-@pytest.mark.parametrize("room", ROOM)
-def test_attend_long(fmt, H, G, bs, lens, n, room):
-    if room > 1 and G * n <= 32:
-        pytest.skip("the kernel for few queries either way")
+@pytest.mark.parametrize("H,bs,lens,G,n,room", _both_kernels([
+    (1, 16, [3000], 1, 1), (2, 64, [2500, 7, 1777], 7, 1), (1, 7, [1999, 1024, 1025], 4, 2),
+    (1, 16, [2048], 8, 20), (2, 16, [3000, 1, 2047], 7, 20)]))
+def test_attend_long(fmt, H, bs, lens, G, n, room):
     p = Pair(1, len(lens), H, 128, bs, -(-max(lens) // bs), fmt, G=G, window=32, room=room)
     p.fill(lens)
     p.attend(n)
