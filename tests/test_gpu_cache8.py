@@ -774,6 +774,75 @@ def test_other_stream_and_tracing():
     p.same()
 
 
+def test_two_handles_on_two_streams():
+    """Each handle has its own workspace: split sequences of both at once, many times."""
+    import eviction_gb300 as kvc
+    p = Pair(1, 2, 2, 128, 16, 130, "e4m3", G=4, window=64)
+    p.fill([2000, 1500])
+    h2 = kvc.Handle(p.cfg)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    want, got = [], []
+    for n in (1, 40):
+        q = torch.randn((1, 2, 8, n, 128), device="cuda").to(torch.bfloat16)
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:4], device="cuda")
+        p.h.cache8_attend(p.c, q, out, lse=lse)
+        want.append((q, out, lse))
+    torch.cuda.synchronize()
+    for i in range(40):
+        for h, s in zip((p.h, h2), streams):
+            q, out, lse = want[i % 2]
+            o, l = torch.empty_like(out), torch.empty_like(lse)
+            o.record_stream(s), l.record_stream(s)
+            s.wait_stream(torch.cuda.current_stream())
+            h.cache8_attend(p.c, q, o, lse=l, stream=s)
+            got.append((i % 2, o, l))
+    torch.cuda.synchronize()
+    for k, o, l in got:
+        assert torch.equal(o, want[k][1]) and torch.equal(l, want[k][2])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_largest_blocks(fmt):
+    """Blocks of 1024 tokens through every call."""
+    p = Pair(1, 2, 1, 128, 1024, 3, fmt, G=2, window=40, budget=1030, max_T=2100)
+    p.fill([2100, 1])
+    p.grow([30, 1023])
+    p.append([30, 1023], spread=3.0, token_major=True)
+    p.same()
+    p.attend(1)
+    p.attend(40)
+    T = 2130
+    k, v, pad, _ = cr.RefCache.gather(p.ref, T)
+    import eviction_gb300 as kvc
+    big = kvc.Handle(kvc.Config(1, 2, 1, 2, 128, T, 1030, window=40, n_recent=0))
+    ko, po = torch.zeros((1, 2, 1, T, 128), dtype=torch.bfloat16, device="cuda"), _ints([0, 0])
+    big.cache8_gather(p.c, T, po, ko)
+    assert np.array_equal(ko.double().cpu().numpy(), k) and np.array_equal(po.cpu().numpy(), pad)
+    kept, nk = _kept(p, 1030, T, [2130, 1024])
+    other = Pair(1, 2, 1, 128, 1024, 2, fmt, budget=1030, max_T=T, seed=4)
+    other.grow(nk[0, :, 0])
+    assert p.ref.compact(other.ref, pad, kept, nk) == 0
+    big.cache8_compact(p.c, other.c, T, po, _ints(kept), _ints(nk))
+    other.same()
+
+
+@pytest.mark.parametrize("G,n", [(100, 1), (33, 8), (512, 8)])
+def test_attend_large_groups(G, n):
+    p = Pair(1, 2, 1, 64, 16, 4, "int8", G=G, window=8)
+    p.fill([60, 7])
+    p.attend(n)
+
+
+def test_attend_many_short_sequences():
+    """More sequences than a CTA keeps the lengths of, most of them short or empty."""
+    p = Pair(1, 3000, 1, 64, 16, 2, "e4m3", G=1, window=2)
+    lens = p.rng.integers(0, 4, 3000)
+    lens[::97] = 30
+    p.fill(lens.tolist())
+    p.attend(1)
+    p.attend(2, n_q=p.rng.integers(0, 3, 3000))
+
+
 def test_pools_past_32_bits():
     """A pool of over 2^32 bytes in which the last blocks are used."""
     import eviction_gb300 as kvc
