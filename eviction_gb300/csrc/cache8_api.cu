@@ -48,7 +48,9 @@ int check_cache(const kvc_config& cfg, const kvc_cache8* c, const char** why) {
   return KVC_OK;
 }
 
-// A stride is a multiple of 8 values and not negative; one of an output's is not 0.
+// Strides are multiples of 8 values and not negative.  An output's rows may not share
+// memory: each axis has to step over all that the axes of smaller strides span (true of
+// any slice or permutation of a dense array).  Strides of axes of size 1 do not matter.
 int check_rows(kvc_handle* h, const kvc_rows* r, const char* name, bool written, int L, int B,
                int heads, int n) {
   if (!r || !r->data) return fail(h, KVC_ERR_ARG, std::string("null pointer: ") + name);
@@ -56,11 +58,14 @@ int check_rows(kvc_handle* h, const kvc_rows* r, const char* name, bool written,
   const int64_t stride[4] = {r->layer, r->seq, r->head, r->token};
   const int size[4] = {L, B, heads, n};
   for (int i = 0; i < 4; ++i) {
-    if (size[i] == 1) continue;
-    if (stride[i] < 0 || stride[i] % 8)
+    if (size[i] > 1 && (stride[i] < 0 || stride[i] % 8))
       return fail(h, KVC_ERR_ALIGN, std::string("strides must be multiples of 8 and >= 0: ") + name);
-    if (written && stride[i] < h->dims.d)
-      return fail(h, KVC_ERR_ARG, std::string("rows overlap: ") + name);
+    if (!written || size[i] == 1) continue;
+    __int128 span = h->dims.d;  // values from the first to past the last of the axes below
+    for (int k = 0; k < 4; ++k)
+      if (size[k] > 1 && (stride[k] < stride[i] || (stride[k] == stride[i] && k < i)))
+        span += static_cast<__int128>(stride[k]) * (size[k] - 1);
+    if (stride[i] < span) return fail(h, KVC_ERR_ARG, std::string("rows overlap: ") + name);
   }
   return KVC_OK;
 }
@@ -87,7 +92,6 @@ kvc::cache8::Cache view(const kvc_handle* h, const kvc_cache8& c) {
           c.block_size, c.max_blocks, h->ws.status, h->ws.status + 1};
 }
 
-// Strides of axes of size 1 do not matter: 0 keeps them out of the arithmetic.
 kvc::cache8::Rows rows(const kvc_rows& r) {
   return {r.data, r.layer, r.seq, r.head, r.token};
 }

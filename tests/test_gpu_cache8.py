@@ -638,6 +638,33 @@ def test_calls_refuse_bad_arguments():
     p.same()
 
 
+def _strided(shape, strides):
+    size = sum((n - 1) * s for n, s in zip(shape, strides)) + 1
+    return torch.zeros(size, dtype=torch.bfloat16, device="cuda").as_strided(shape, strides)
+
+
+@pytest.mark.parametrize("strides,fine", [
+    ((0, 256, 64, 64, 1), False),     # heads and tokens at the same place
+    ((0, 256, 64, 128, 1), False),    # token 1 of a head in head 2
+    ((0, 128, 64, 512, 1), False),    # sequence 1 begins in sequence 0's heads
+    ((0, 512, 128, 64, 1), True),     # dense
+    ((0, 576, 136, 64, 1), True),     # with gaps
+    ((0, 64, 256, 128, 1), True),     # sequences innermost
+    ((0, 1024, 64, 512, 1), True),    # token-major
+])
+def test_attend_refuses_output_rows_that_overlap(strides, fine):
+    import eviction_gb300 as kvc
+    p = Pair(1, 2, 2, 64, 16, 4, "e4m3", G=2, window=4)
+    q = torch.zeros((1, 2, 4, 2, 64), dtype=torch.bfloat16, device="cuda")
+    out = _strided((1, 2, 4, 2, 64), strides)
+    if fine:
+        p.h.cache8_attend(p.c, q, out)
+        return
+    with pytest.raises(kvc.KvcError) as e:
+        p.h.cache8_attend(p.c, q, out)
+    assert e.value.code == -1
+
+
 # ---- together ----
 
 def _steps(p, n_steps, check=True):
