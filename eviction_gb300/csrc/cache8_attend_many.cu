@@ -7,23 +7,27 @@
 // Row r of a KV head is query r % nq of its group's head r / nq.  Per 128 tokens:
 //   converters (4 warps)  codes from global memory to fp16 tiles in shared memory, in
 //                         the swizzled layout of the MMA operands, one tile ahead.
-//                         Keys carry their block's scale relative to the tile's
-//                         largest, values relative to one at or above the
-//                         largest so far (powers of two: exact, down to fp16's last
+//                         Keys and values carry their block's scale relative to the
+//                         tile's largest (powers of two: exact, down to fp16's last
 //                         step);
 //   MMA (1 thread)        S = Q K^T (128 x 128, in TMEM), then O += P V with P read
 //                         from TMEM, where it takes the place of S;
-//   softmax (4 warps)     one thread a row: p = 2^(z - m), their sum in fp32, P to TMEM
+//   softmax (4 warps)     one thread a row: the weights, their sum in fp32, P to TMEM
 //                         as fp16.  The first of these warps also issues the MMAs: it
 //                         would wait for them anyway.
-// The reference m of a row lies below its maximum: weights may reach 2^15 (fp16 has
-// the room) before m moves, and a new m leaves them at 2^8.  The maximum comes with the
-// TMEM load (tcgen05.ld.red).  Half of a row stays in registers between the maximum
-// and the exponentials, the other half is loaded again.
-// Where the value scales 2^e of a tile are more than 2^8 below the largest so far, 2^v,
-// fp16 would lose the values: such a tile's values are the bare codes, and its logits
-// x = z + e - v carry the scale, with 2^(v - e) p in the sum.  That path takes masks and
-// absent tokens as well (e = -inf).
+// A weight carries its token's value scale 2^e: w = 2^(x - m), x = z + e, and O is the
+// sum of w times the code, so that fp16 weights stay near 1 whatever the blocks' scales
+// are; the sum of the softmax takes 2^-e w.  Where the value scales of a tile are at
+// most 2^8 below its largest, 2^v, the values are codes times 2^(e - v) instead and the
+// weights 2^(z + v - m): no scale for each column, and the sum is scaled once a tile.
+// Else fp16 would lose the values: they are the bare codes, and the logits carry e column
+// by column.  That path takes absent tokens as well (e = -inf).
+// The reference m of a row lies below its largest x: weights may reach 2^15 (fp16 has
+// the room) before m moves, and a new m leaves them at 2^8.  Only what a row sees moves
+// it (but for v, at most 2^8): not a block of large values that has no weight or that a
+// mask hides.  The maximum comes with the TMEM load (tcgen05.ld.red).  Half of a row
+// stays in registers between the maximum and the exponentials, the other half is loaded
+// again.
 //
 // The arithmetic bounds this: 4 R d operations a token, 1024 cycles of the tensor
 // pipe per 128 x 128 tile of d = 128.  S and P share columns, so that one CTA's
@@ -50,8 +54,7 @@ constexpr int kInfos = 4;         // tiles whose scales are told ahead
 constexpr int kTmemCols = 256;    // S / P: 128, O: up to 128
 constexpr int kMaxParts = 320;    // CTAs of a call that cuts heads
 constexpr float kRoom = 15.f, kStart = 8.f;  // log2 of the weights' limit and of a new m's
-constexpr int kHeadroom = 1;  // log2 of the room that a new value reference leaves: moving it scales O
-constexpr int kSpread = 8;  // log2 of how far below the largest value scale stays plain
+constexpr int kSpread = 8;  // log2 of how far below the tile's largest value scale stays plain
 
 struct Parts {
   int per_tile;   // CTAs of a row tile
@@ -77,10 +80,10 @@ struct Bool {
 
 // What a tile's converters tell the softmax warps.
 struct TileInfo {
-  float k_ref;  // the scale that the tile's keys are relative to
-  int v_ref;    // log2 of the scale that its values are relative to (never falls)
-  int plain;    // no token is absent and no value scale is 2^kSpread below that
-  int unused;
+  float k_ref;   // the scale that the tile's keys are relative to
+  int plain;     // no token is absent and no value scale is 2^kSpread below the largest
+  float v_ref;   // log2 of the scale that the values are relative to, if plain; else 0
+  float v_back;  // 2^-v_ref
 };
 
 __device__ __forceinline__ void fence_async_shared() {
@@ -313,8 +316,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       return true;
     };
     const int limit = len - nq + j;     // last token that this row sees
-    float m = -INFINITY, sum = 0.f;     // reference and sum of the weights
-    int v_ref = 0;
+    float m = -INFINITY, sum = 0.f;     // reference of the weights, their sum
     bool ok = true;
     if (warp == 0 && n_tiles > 0)
       ok = warp_wait(q_full, 0, abort, c.status) && issue_scores(0);
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_ld32_max(my_tmem, va, m0);
         tmem_ld32_max(my_tmem + 32, vb, m1);
         tmem_ld_wait();
-        top = fmaxf(top, fmaxf(m0, m1)) * f;
+        top = fmaf(fmaxf(top, fmaxf(m0, m1)), f, info.v_ref);
       } else if (info.plain) {
         auto most = [&](const uint32_t (&v)[32], int first, float so_far) {
 #pragma unroll
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_ld32(my_tmem, va);
         tmem_ld32(my_tmem + 32, vb);
         tmem_ld_wait();
-        top = most(vb, 32, most(va, 0, top)) * f;
+        top = fmaf(most(vb, 32, most(va, 0, top)), f, info.v_ref);
       } else {
         top = -INFINITY;
 #pragma unroll 1
@@ -374,14 +376,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // ---- new references: what is there is scaled to them ----
       const bool raise = top > m + kRoom;
-      const bool shift = i > 0 && info.v_ref != v_ref;
-      if (__any_sync(0xffffffffu, raise || shift)) {
+      if (__any_sync(0xffffffffu, raise)) {
         const float next = raise ? top - kStart : m;
         const float keep = raise ? ex2(m - next) : 1.f;
         m = next;
         sum *= keep;
         if (i > 0) {
-          const float scale = keep * ex2(static_cast<float>(v_ref - info.v_ref));
           if (!warp_wait(o_full, (i - 1) & 1, abort, c.status)) {
             ok = false;
             break;
@@ -393,16 +393,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             tmem_ld16(my_tmem + kOutCol + k * 16, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * scale);
+            for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * keep);
             tmem_st16(my_tmem + kOutCol + k * 16, v);
           }
           tmem_st_wait();
         }
       }
-      v_ref = info.v_ref;
       // ---- weights: S's columns become P's ----
       const float ref = m == -INFINITY ? 0.f : m;
-      const float2 ff = make_float2(f, f), off = make_float2(-ref, -ref);
+      const float add = info.v_ref - ref;
+      const float2 ff = make_float2(f, f), off = make_float2(add, add);
       float2 part_sum = make_float2(0.f, 0.f);
       if (info.plain) {
         auto weights = [&](const uint32_t (&v)[32], int first, auto masked) {
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           tmem_st16(my_tmem + k * 16, p);
         }
       }
-      sum += part_sum.x + part_sum.y;
+      sum = fmaf(part_sum.x + part_sum.y, info.v_back, sum);
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(p_full);
@@ -479,8 +479,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (ok) {
       tc_fence_after();
       float* slot = sp.part + static_cast<size_t>(blockIdx.x) * ((D + 2) * kRows) + row;
-      const float unit = exp2_int(v_ref);
-      const float inv = sum == 0.f ? 0.f : unit / sum;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll 1
       for (int k = 0; k < D / 32; ++k) {
         uint32_t v[32];
@@ -503,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         } else if (there) {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) slot[(2 + k * 32 + x) * kRows] = __uint_as_float(v[x]) * unit;
+          for (int x = 0; x < 32; ++x) slot[(2 + k * 32 + x) * kRows] = __uint_as_float(v[x]);
         }
         __syncwarp();
       }
@@ -531,7 +530,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t own_ks, own_vs;  // scales as they are in memory
     int row[4];               // of the tokens row_in + 32 k
     uint4 kc[4][DB], vc[4][DB];
-    int v_ref = -1000;        // what the values are relative to
     auto lookup = [&](int i) {  // the tile's blocks
       const int t = (tile0 + i) * kTokens + own;
       const bool in = i < n_tiles && t < len;
@@ -611,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!warp_wait(&m_empty[st], ((i / kInfos) & 1) ^ 1, abort, c.status) ||
           !warp_wait(r_full, i & 1, abort, c.status))
         return false;
-      k_max = -126;
+      k_max = v_max = -126;
 #pragma unroll
       for (int k = 0; k < kConvertWarps; ++k) {
         const int4 o = s_red[ex * kConvertWarps + k];
@@ -620,18 +618,17 @@ __global__ void __launch_bounds__(kThreads, 2)
         v_min = min(v_min, o.z);
         absent |= o.w;
       }
-      if (v_max > v_ref) v_ref = max(v_max + kHeadroom, -126);
-      const bool plain = !absent && v_ref - v_min <= kSpread;
+      const bool plain = !absent && v_max - v_min <= kSpread;
       if (!plain) {
-        s_e[st * kTokens + own] = there ? static_cast<float>(ve - v_ref) : -INFINITY;
-        s_back[st * kTokens + own] = there ? exp2_int(min(v_ref - ve, 126)) : 0.f;
+        s_e[st * kTokens + own] = there ? static_cast<float>(ve) : -INFINITY;
+        s_back[st * kTokens + own] = there ? exp2_int(-ve) : 0.f;
       }
       if (lane == 0 && cw == 0) {
         TileInfo info;
         info.k_ref = exp2_int(k_max);
-        info.v_ref = v_ref;
         info.plain = plain;
-        info.unused = 0;
+        info.v_ref = plain ? static_cast<float>(v_max) : 0.f;
+        info.v_back = plain ? exp2_int(-v_max) : 1.f;
         s_info[st] = info;
       }
       warp_arrive(&m_full[st]);
@@ -641,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         row[k] = tok.x;
         const int e = static_cast<int16_t>(tok.y & 0xffff), f = tok.y >> 16;
         k_factor[k] = tok.x < 0 ? kOne : exp2_half2(min(e - k_max, 0));
-        v_next[k] = tok.x < 0 || !plain ? kOne : exp2_half2(min(f - v_ref, 0));
+        v_next[k] = tok.x < 0 || !plain ? kOne : exp2_half2(min(f - v_max, 0));
       }
       return true;
     };

@@ -1,0 +1,86 @@
+"""Attention over the 8-bit paged cache at the ends of what its scales and queries may hold, on both
+kernels, within the per-token bound of tests/cache8_bounds.py."""
+import numpy as np
+import pytest
+import torch
+
+from tests import cache8_bounds as cb
+from tests import cache8_ref as cr
+from tests.test_gpu_cache8 import Pair, _ints
+
+pytestmark = pytest.mark.gpu
+
+# (queries, room in the table): few rows; many rows on the kernel for few; on the one for many
+KERNELS = [(1, 1), (40, 1), (40, 512)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+
+
+def _check(p, q, n_q=None, absent=None, status=0):
+    """Attend with q (numpy, [1, B, Hq, n, d]) and compare."""
+    qt = torch.from_numpy(q).to(torch.bfloat16).cuda()
+    out = torch.full_like(qt, 7.0)
+    lse = torch.full(qt.shape[:4], 7.0, device="cuda")
+    p.h.cache8_attend(p.c, qt, out, lse=lse, n_q=None if n_q is None else _ints(n_q))
+    assert p.h.device_status() == status
+    want, wl, tol, ltol = cb.attend(p.ref, qt.double().cpu().numpy(), p.scale, n_q, absent)
+    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    off = np.abs(got - want) - tol
+    assert (off <= 0).all(), (off.max(), np.argwhere(off > 0)[:3])
+    seen = np.isfinite(wl)
+    assert np.array_equal(np.isneginf(gl), ~seen)
+    assert (np.abs(gl - wl)[seen] <= ltol[seen]).all()
+    return got, gl
+
+
+def _outlier_cache(n, room, fmt, bs, tokens, d=64):
+    """A cache of ordinary rows whose keys have no first component, and queries that have one: a
+    block whose keys are given a first component gets logits of that product alone on top."""
+    p = Pair(1, len(tokens), 1, d, bs, -(-max(tokens) // bs), fmt, G=2, window=64, room=room, seed=n + bs)
+    p.fill(tokens)
+    p.ref.pool[0][..., 0] = 0
+    q = p.rng.standard_normal((1, len(tokens), 2, n, d))
+    q[..., 0] = 4.0
+    return p, q
+
+
+def _first(value, fmt):
+    return cr.encode(np.array([float(value)]), fmt)[0]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("far", [12, 30, 60, 100])
+@pytest.mark.parametrize("n,room", KERNELS)
+def test_value_scale_outlier_without_weight(n, room, far, fmt):
+    """One block's value scale is 2^far above the others'; its tokens' logits are far below the others',
+    so it does not count, wherever it lies."""
+    p, q = _outlier_cache(n, room, fmt, 8, [600, 420, 131])
+    for b, i in ((0, 20), (1, 0), (2, 8)):   # tile 1, the very first block, tile 0
+        blk = p.ref.table[b, i]
+        p.ref.pool[0][0, blk, 0, :, 1:] = 0
+        p.ref.pool[0][0, blk, 0, :, 0] = _first(-100, fmt)
+        p.ref.scale[0][0, blk, 0] = 2.0 ** 5  # logit -100 2^5 4 / 8 = -1600
+        p.ref.scale[1][0, blk, 0] *= 2.0 ** far
+    p.ref.scale[1] *= np.float32(2.0 ** -min(far // 2, 50))
+    p.sync_up()
+    _check(p, q)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("far", [30, 100])
+@pytest.mark.parametrize("n,room", KERNELS[1:])
+def test_value_scale_outlier_among_masked_tokens(n, room, far, fmt):
+    """The outlier is the block of the newest tokens: later queries see it, with all the weight there
+    is, and earlier ones must not notice."""
+    p, q = _outlier_cache(n, room, fmt, 8, [600, 424])
+    for b in range(2):
+        blk = p.ref.table[b, p.ref.blocks(p.ref.len[b]) - 1]
+        p.ref.scale[1][0, blk, 0] *= 2.0 ** far
+    p.ref.scale[1] *= np.float32(2.0 ** -(far // 2))
+    p.sync_up()
+    _check(p, q)
