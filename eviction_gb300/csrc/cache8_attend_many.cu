@@ -8,8 +8,7 @@
 //   converters (4 warps)  codes from global memory to fp16 tiles in shared memory, in
 //                         the swizzled layout of the MMA operands, one tile ahead.
 //                         Keys and values carry their block's scale relative to the
-//                         tile's largest (powers of two: exact, down to fp16's last
-//                         step);
+//                         tile's largest (powers of two, and exact: see below);
 //   MMA (1 thread)        S = Q K^T (128 x 128, in TMEM), then O += P V with P read
 //                         from TMEM, where it takes the place of S;
 //   softmax (4 warps)     one thread a row: the weights, their sum in fp32, P to TMEM
@@ -20,8 +19,10 @@
 // are; the sum of the softmax takes 2^-e w.  Where the value scales of a tile are at
 // most 2^8 below its largest, 2^v, the values are codes times 2^(e - v) instead and the
 // weights 2^(z + v - m): no scale for each column, and the sum is scaled once a tile.
-// Else fp16 would lose the values: they are the bare codes, and the logits carry e column
-// by column.  That path takes absent tokens as well (e = -inf).
+// Keys are codes times 2^(their scale - the tile's largest), which fp16 holds exactly
+// where that is at most 2^15 down.  A tile whose scales are further apart than either
+// has bare codes for both, and its logits get their scales and e column by column.
+// That path takes absent tokens as well (e = -inf).
 // The reference m of a row lies below its largest x: weights may reach 2^15 (fp16 has
 // the room) before m moves, and a new m leaves them at 2^8.  Only what a row sees moves
 // it (but for v, at most 2^8): not a block of large values that has no weight or that a
@@ -54,7 +55,9 @@ constexpr int kInfos = 4;         // tiles whose scales are told ahead
 constexpr int kTmemCols = 256;    // S / P: 128, O: up to 128
 constexpr int kMaxParts = 320;    // CTAs of a call that cuts heads
 constexpr float kRoom = 15.f, kStart = 8.f;  // log2 of the weights' limit and of a new m's
-constexpr int kSpread = 8;  // log2 of how far below the tile's largest value scale stays plain
+// log2 of how far below the tile's largest scale a plain tile's scales lie at most.  Keys:
+// e4m3's last step is 2^-9, fp16's 2^-24.
+constexpr int kSpread = 8, kKeySpread = 15;
 
 struct Parts {
   int per_tile;   // CTAs of a row tile
@@ -80,8 +83,8 @@ struct Bool {
 
 // What a tile's converters tell the softmax warps.
 struct TileInfo {
-  float k_ref;   // the scale that the tile's keys are relative to
-  int plain;     // no token is absent and no value scale is 2^kSpread below the largest
+  float k_ref;   // the scale that the tile's keys are relative to, if plain; else 1
+  int plain;     // no token is absent and no scale is 2^kSpread / 2^kKeySpread below the largest
   float v_ref;   // log2 of the scale that the values are relative to, if plain; else 0
   float v_back;  // 2^-v_ref
 };
@@ -192,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* s_e = reinterpret_cast<float*>(smem + Sm::kE);        // [kInfos][kTokens]
-  float* s_back = reinterpret_cast<float*>(smem + Sm::kBack);  // [kInfos][kTokens] 2^-e
+  // [kInfos][kTokens] 2^-e and the key's scale, as two bf16
+  uint32_t* s_back = reinterpret_cast<uint32_t*>(smem + Sm::kBack);
   TileInfo* s_info = reinterpret_cast<TileInfo*>(smem + Sm::kInfo);
   int2* s_tok = reinterpret_cast<int2*>(smem + Sm::kTok);  // [2][kTokens] row, exponents
   int4* s_red = reinterpret_cast<int4*>(smem + Sm::kRed);  // [2][kConvertWarps]
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_after();
       const TileInfo info = s_info[st];
       const float* e_col = s_e + st * kTokens;
-      const float* back_col = s_back + st * kTokens;
+      const uint32_t* back_col = s_back + st * kTokens;
       const float f = qf * info.k_ref;
       const bool whole = t0 + kTokens <= len - nq + 1;  // seen by all rows
       const int seen = limit - t0 + 1;                  // columns that this row sees
@@ -369,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           tmem_ld_wait();
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
-            const float z = fmaf(__uint_as_float(va[x]), f, e_col[k * 32 + x]);
+            const float z =
+                fmaf(__uint_as_float(va[x]) * bf16_lo(back_col[k * 32 + x]), f, e_col[k * 32 + x]);
             if (k * 32 + x < seen) top = fmaxf(top, z);
           }
         }
@@ -445,16 +450,18 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int x = 0; x < 16; x += 2) {
             const float4 e4 = *reinterpret_cast<const float4*>(e_col + k * 32 + 2 * x);
-            const float4 b4 = *reinterpret_cast<const float4*>(back_col + k * 32 + 2 * x);
+            const uint4 b4 = *reinterpret_cast<const uint4*>(back_col + k * 32 + 2 * x);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const int at = 2 * (x + y);
-              float2 z = fma2(make_float2(__uint_as_float(va[at]), __uint_as_float(va[at + 1])), ff,
-                              y ? make_float2(e4.z, e4.w) : make_float2(e4.x, e4.y));
+              float2 z = make_float2(__uint_as_float(va[at]) * bf16_lo(y ? b4.z : b4.x),
+                                     __uint_as_float(va[at + 1]) * bf16_lo(y ? b4.w : b4.y));
+              z = fma2(z, ff, y ? make_float2(e4.z, e4.w) : make_float2(e4.x, e4.y));
               z = add2(z, off);
               z.x = k * 32 + at < seen ? ex2(z.x) : 0.f;
               z.y = k * 32 + at + 1 < seen ? ex2(z.y) : 0.f;
-              part_sum = fma2(z, y ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y), part_sum);
+              part_sum = fma2(z, make_float2(bf16_hi(y ? b4.z : b4.x), bf16_hi(y ? b4.w : b4.y)),
+                              part_sum);
               p[x + y] = half2_of(z.x, z.y);
             }
           }
@@ -598,13 +605,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int st = i % kInfos, ex = i & 1;
       const bool there = own_row >= 0;
       const int ke = static_cast<int>(own_ks >> 23) - 127, ve = static_cast<int>(own_vs >> 23) - 127;
+      // (an absent token's minima leave no tile plain)
       int k_max = __reduce_max_sync(0xffffffffu, there ? ke : -1000);
+      int k_min = __reduce_min_sync(0xffffffffu, there ? ke : -1000);
       int v_max = __reduce_max_sync(0xffffffffu, there ? ve : -1000);
-      int v_min = __reduce_min_sync(0xffffffffu, there ? ve : 1000);
-      int absent = __any_sync(0xffffffffu, !there);
+      int v_min = __reduce_min_sync(0xffffffffu, there ? ve : -1000);
       // (two buffers: a warp writes one again after all have read the other)
       s_tok[ex * kTokens + own] = make_int2(own_row, (ke & 0xffff) | ve << 16);
-      if (lane == 0) s_red[ex * kConvertWarps + cw] = make_int4(k_max, v_max, v_min, absent);
+      if (lane == 0) s_red[ex * kConvertWarps + cw] = make_int4(k_max, k_min, v_max, v_min);
       warp_arrive(r_full);
       if (!warp_wait(&m_empty[st], ((i / kInfos) & 1) ^ 1, abort, c.status) ||
           !warp_wait(r_full, i & 1, abort, c.status))
@@ -614,18 +622,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int k = 0; k < kConvertWarps; ++k) {
         const int4 o = s_red[ex * kConvertWarps + k];
         k_max = max(k_max, o.x);
-        v_max = max(v_max, o.y);
-        v_min = min(v_min, o.z);
-        absent |= o.w;
+        k_min = min(k_min, o.y);
+        v_max = max(v_max, o.z);
+        v_min = min(v_min, o.w);
       }
-      const bool plain = !absent && v_max - v_min <= kSpread;
+      const bool plain = v_max - v_min <= kSpread && k_max - k_min <= kKeySpread;
       if (!plain) {
         s_e[st * kTokens + own] = there ? static_cast<float>(ve) : -INFINITY;
-        s_back[st * kTokens + own] = there ? exp2_int(-ve) : 0.f;
+        s_back[st * kTokens + own] = there ? __float_as_uint(exp2_int(-ve)) | own_ks >> 16 : 0x3f80u;
       }
       if (lane == 0 && cw == 0) {
         TileInfo info;
-        info.k_ref = exp2_int(k_max);
+        info.k_ref = plain ? exp2_int(k_max) : 1.f;
         info.plain = plain;
         info.v_ref = plain ? static_cast<float>(v_max) : 0.f;
         info.v_back = plain ? exp2_int(-v_max) : 1.f;
@@ -637,8 +645,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int2 tok = s_tok[ex * kTokens + row_in + 32 * k];
         row[k] = tok.x;
         const int e = static_cast<int16_t>(tok.y & 0xffff), f = tok.y >> 16;
-        k_factor[k] = tok.x < 0 ? kOne : exp2_half2(min(e - k_max, 0));
-        v_next[k] = tok.x < 0 || !plain ? kOne : exp2_half2(min(f - v_max, 0));
+        k_factor[k] = plain ? exp2_half2(e - k_max) : kOne;
+        v_next[k] = plain ? exp2_half2(f - v_max) : kOne;
       }
       return true;
     };

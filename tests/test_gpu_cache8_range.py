@@ -84,3 +84,35 @@ def test_value_scale_outlier_among_masked_tokens(n, room, far, fmt):
     p.ref.scale[1] *= np.float32(2.0 ** -(far // 2))
     p.sync_up()
     _check(p, q)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("where", ["middle", "newest"])
+@pytest.mark.parametrize("n,room", KERNELS)
+def test_key_scale_outlier(n, room, where, fmt):
+    """Two blocks' key scales lie 2^9 to 2^67 above the others', whose logits are the usual ones;
+    theirs are far below (or, for the newest tokens, above, where a query sees them)."""
+    for far in (4, 11, 15, 16, 19, 20, 35, 62):
+        p, q = _outlier_cache(n, room, fmt, 8, [600, 420, 131])
+        for b in range(3):
+            last = p.ref.blocks(p.ref.len[b]) - 1
+            for i in ((1, last // 2) if where == "middle" else (last - 1, last)):
+                blk = p.ref.table[b, i]
+                p.ref.pool[0][0, blk, 0, :, 1:] = 0
+                sign = 1 if where == "newest" and b == 1 else -1
+                p.ref.pool[0][0, blk, 0, :, 0] = [_first(sign * x, fmt) for x in range(80, 112, 4)]
+                p.ref.scale[0][0, blk, 0] = 2.0 ** far
+        p.sync_up()
+        _check(p, q)
+
+
+@pytest.mark.parametrize("n,room", KERNELS)
+def test_small_key_blocks_beside_large_ones(n, room):
+    """Key blocks of every scale from 2^-40 to 2^8 at random, small values in all of them."""
+    p, q = _outlier_cache(n, room, "int8", 8, [600, 420, 131])
+    p.ref.scale[0][:] = 2.0 ** p.rng.integers(-40, -2, p.ref.scale[0].shape)
+    p.ref.scale[0][0, ::7] = 2.0 ** 8
+    p.ref.pool[0][:, ::7, :, :, 1:] = 0
+    p.ref.pool[0][:, ::7, :, :, 0] = _first(-90, "int8")
+    p.sync_up()
+    _check(p, q)
