@@ -338,8 +338,7 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
         }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // the row's largest magnitude to [1, 2)
-      const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      const int e = row_exp(mx);
       const float down = exp2_int(-e);
 #pragma unroll
       for (int k = 0; k < KV; ++k)
@@ -351,7 +350,7 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
             qf[nt][k * 4 + i * 2 + j / 2][j % 2] =
                 half2_of(bf16_lo(x[j]) * down, bf16_hi(x[j]) * down);
         }
-      const float up = a.scale_log2 * exp2_int(e);
+      const float up = finite_factor(a.scale_log2, exp2_int(e));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         qscale[nt][i] = __shfl_sync(0xffffffffu, up, (2 * q4 + i) * 4);
@@ -425,7 +424,7 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float& x = z[i / 2][nt][(i % 2) * 2 + j];
-            x = fmaf(x, ks * qscale[nt][j], ef);
+            x = fmaf(x, finite_factor(ks, qscale[nt][j]), ef);
           }
       }
       if (t0 + kTile > len - nq + 1) {  // not every query sees all of the step

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <atomic>
+#include <cfloat>
 
 #include "cache8.cuh"
 
@@ -50,6 +51,14 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
+
+// log2 of the power of two that a query row is divided by: its largest magnitude m goes
+// to [1, 4) (a zero or subnormal one below), with room in fp16 for all of bf16's range.
+__device__ __forceinline__ int row_exp(float m) {
+  return min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -126), 126);
+}
+// What a row's scores are multiplied by; finite, so that a score of 0 stays 0.
+__device__ __forceinline__ float finite_factor(float a, float b) { return fminf(a * b, FLT_MAX); }
 
 __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool there = row < rows;
     const int hq = h * a.G + (there ? r / nq : 0), j = there ? r % nq : 0;
     const uint32_t my_tmem = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    // the query row as fp16, its largest magnitude scaled to [1, 2)
+    // the query row as fp16, times a power of two
     float qf;
     {
       const uint4* q = reinterpret_cast<const uint4*>(a.q.at(l, b, hq, j));
@@ -266,9 +266,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int k = 0; k < 4; ++k)
           mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
       }
-      const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 100);
+      const int e = row_exp(mx);
       const float down = exp2_int(-e);
-      qf = a.scale_log2 * exp2_int(e);
+      qf = finite_factor(a.scale_log2, exp2_int(e));
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
         *reinterpret_cast<uint4*>(smem + Sm::kQ + (i / 8) * kBlock + row * 128 +
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const TileInfo info = s_info[st];
       const float* e_col = s_e + st * kTokens;
       const uint32_t* back_col = s_back + st * kTokens;
-      const float f = qf * info.k_ref;
+      const float f = finite_factor(qf, info.k_ref);
       const bool whole = t0 + kTokens <= len - nq + 1;  // seen by all rows
       const int seen = limit - t0 + 1;                  // columns that this row sees
       uint32_t va[32], vb[32];

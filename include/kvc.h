@@ -474,9 +474,14 @@ int kvc_cache8_append(kvc_handle* h, const kvc_cache8* c, const kvc_rows* k, con
 /* Attention of the newest tokens' queries over the cache:
  *   out_j = sum_t softmax_t(scale q_j . k_t) v_t over t <= seq_len[b] - n_q[b] + j,
  * for the H*G query heads (head h*G+g reads KV head h); scale is the
- * configuration's softmax_scale.  Arithmetic: the products take q, the codes and
- * the softmax weights in at least bf16's precision and accumulate in fp32; maxima
- * and sums are fp32.
+ * configuration's softmax_scale.  Arithmetic: products of fp16 operands, accumulated
+ * in fp32; maxima and sums in fp32.  Codes are exact.  A query row is held relative to
+ * its largest magnitude: exact for elements down to 2^-14 of it, below that to 2^-25
+ * of it.  Softmax weights have 11 bits, down to 2^-14 of the row's largest weight times
+ * value scale, below that to 2^-25 of it.  Any finite q will do: a query row's logits
+ * are exact to fp32's rounding as long as softmax_scale log2(e) max|q| times the key
+ * scale is finite in fp32 (beyond, that factor is taken as the largest fp32 number).
+ * A q that is not finite spoils its own row.
  *   q      [n_layers][B][H*G][n][d] bf16 rows, 1 <= n <= window
  *   n_q    [B] int32, 0..n, or NULL: n for every sequence.  Rows past n_q[b] are
  *          neither read nor written

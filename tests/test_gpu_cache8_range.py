@@ -116,3 +116,48 @@ def test_small_key_blocks_beside_large_ones(n, room):
     p.ref.pool[0][:, ::7, :, :, 0] = _first(-90, "int8")
     p.sync_up()
     _check(p, q)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("exp", [116, 126, 127, -100, -126, -133])
+@pytest.mark.parametrize("n,room", KERNELS)
+def test_largest_and_smallest_finite_queries(n, room, exp, fmt):
+    """Query rows of one magnitude 2^exp: keys with nothing but a first component, all different, so
+    that the softmax picks one token (or, of tiny queries, weighs all alike)."""
+    d, tokens = 64, 96
+    p = Pair(1, 1, 1, d, 16, 6, fmt, G=2, window=64, room=room * 2, seed=n)
+    p.fill([tokens])
+    p.ref.pool[0][:] = 0
+    order = p.rng.permutation(tokens)
+    # 96 different codes of one sign each, in e4m3 as in int8
+    codes = (np.arange(96) + 8).astype(np.uint8)
+    for t in range(tokens):
+        p.ref.pool[0][0, p.ref.table[0, t // 16], 0, t % 16, 0] = codes[order[t]]
+    p.ref.scale[0][:] = 2.0 ** -64
+    p.sync_up()
+    q = np.zeros((1, 1, 2, n, d))
+    q[..., 0] = 1.5 * 2.0 ** exp if exp > -133 else 2.0 ** exp
+    q[:, :, 1] *= -1
+    got, lse = _check(p, q)
+    if exp > 100:   # one token each: the bound above is wide there, this is not
+        keys = cr.decode(codes, fmt)[order]
+        v = p.ref.rows(1, 0, 0, 0)
+        for j in range(n):
+            see = tokens - n + j + 1
+            for g, t in ((0, keys[:see].argmax()), (1, keys[:see].argmin())):
+                assert (np.abs(got[0, 0, g, j] - v[t]) <= 2.0 ** -8 * np.abs(v[t])).all()
+                z = q[0, 0, g, j, 0] * keys[t] * 2.0 ** -64 * p.scale   # (a few fp32 roundings)
+                assert abs(lse[0, 0, g, j] - z) <= 2.0 ** -20 * abs(z)
+
+
+@pytest.mark.parametrize("n,room", KERNELS)
+def test_zero_keys_under_large_queries(n, room):
+    """Codes of zero give a logit of zero whatever the query's and the block's scales are."""
+    p = Pair(1, 1, 1, 64, 16, 16, "e4m3", G=2, window=64, room=room, seed=n)
+    p.fill([250])
+    p.ref.pool[0][:] = 0
+    p.ref.scale[0][:] = 2.0 ** p.rng.choice([-64, 0, 64], p.ref.scale[0].shape)
+    p.sync_up()
+    q = np.full((1, 1, 2, n, 64), 1.75 * 2.0 ** 127)
+    q[:, :, 1, :, ::2] *= -1
+    _check(p, q)
