@@ -181,13 +181,22 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t clamp_half2(uint32_t a, uint32_t lo, uint32_t hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 t;\n\tmax.f16x2 t, %1, %2;\n\tmin.f16x2 %0, t, %3;\n\t}"
+      : "=r"(r)
+      : "r"(a), "r"(lo), "r"(hi));
+  return r;
+}
+
 // 2^e as both halves of a pair of fp16, e <= 15; 0 below its last step.
 __device__ __forceinline__ uint32_t exp2_half2(int e) {
   const uint32_t h = e >= -14 ? (15 + e) << 10 : e >= -24 ? 1u << (24 + e) : 0u;
   return h * 0x00010001u;
 }
 
-// Pairs (0, 1) and (2, 3) of fp16 values, at most the largest code, to four codes.
+// Pairs (0, 1) and (2, 3) of fp16 values, at most the largest code (integers; e4m3
+// saturates by itself), to four codes.
 template <int FMT>
 __device__ __forceinline__ uint32_t codes_of(uint32_t lo, uint32_t hi) {
   if constexpr (FMT == KVC_CACHE8_E4M3) {

@@ -61,7 +61,8 @@ __device__ __forceinline__ uint2 encode8(uint4 v, float inv) {
   return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
 
-// Codes times 2^e, as codes again (the products are at most the largest code).  In fp16
+// Codes times 2^e, as codes again (the products are at most the largest code, but for
+// e4m3's 448 at the largest scale, which int8 does not reach: clamped).  In fp16
 // the products are exact wherever they do not round to code 0 (8 significant bits; what
 // fp16 cannot hold is far below the smallest code), so that there is one rounding.
 // Codes of a block whose scale shrinks by more than 2^15 are too small to be anything
@@ -75,7 +76,13 @@ __device__ __forceinline__ uint4 recode16(uint4 v, int e) {
     for (int i = 0; i < 4; ++i) {
       uint32_t lo, hi;
       halves<FROM>(w[i], lo, hi);
-      w[i] = codes_of<TO>(mul_half2(lo, factor), mul_half2(hi, factor));
+      lo = mul_half2(lo, factor);
+      hi = mul_half2(hi, factor);
+      if constexpr (FROM == KVC_CACHE8_E4M3 && TO == KVC_CACHE8_INT8) {  // to +-127
+        lo = clamp_half2(lo, 0xD7F0D7F0u, 0x57F057F0u);
+        hi = clamp_half2(hi, 0xD7F0D7F0u, 0x57F057F0u);
+      }
+      w[i] = codes_of<TO>(lo, hi);
     }
   } else {
     const float ratio = exp2_int(min(e, 127));

@@ -161,3 +161,34 @@ def test_zero_keys_under_large_queries(n, room):
     q = np.full((1, 1, 2, n, 64), 1.75 * 2.0 ** 127)
     q[:, :, 1, :, ::2] *= -1
     _check(p, q)
+
+
+# ---- compaction between formats ----
+
+@pytest.mark.parametrize("bs,to_bs", [(16, 16), (5, 64)])
+def test_compact_to_int8_at_the_largest_scale(bs, to_bs):
+    """e4m3 codes above 127 at the scale 2^64, beyond which int8's scale cannot grow: they become the
+    largest code, with their sign."""
+    lens, budget, T = [90, 30], 45, 90
+    p = Pair(1, 2, 2, 64, bs, -(-T // bs), "e4m3", budget=budget, max_T=T)
+    p.grow(lens)
+    k, v = p.new_rows(T), p.new_rows(T)
+    k[:, 0] *= 2.0 ** 72
+    v[:, 1, 1] *= 2.0 ** 75
+    v[:, 0, 0, ::3] *= 2.0 ** 71
+    p.append(lens, rows=(k, v))
+    p.same()
+    other = Pair(1, 2, 2, 64, to_bs, -(-budget // to_bs), "int8", budget=budget, max_T=T, seed=9)
+    kept, nk = np.full((1, 2, 2, budget), -1, np.int32), np.zeros((1, 2, 2), np.int32)
+    for b, n in enumerate(lens):
+        m = min(budget, n)
+        nk[:, b] = m
+        for h in range(2):
+            kept[0, b, h, :m] = np.sort(p.rng.permutation(n)[:m]) + T - n
+    assert other.grow(nk[0, :, 0]) == 0
+    pad = T - np.array(lens, np.int32)
+    assert p.ref.compact(other.ref, pad, kept, nk) == 0
+    assert any((np.abs(x.view(np.int8)) == 127).any() for x in other.ref.pool)
+    p.h.cache8_compact(p.c, other.c, T, _ints(pad), _ints(kept), _ints(nk))
+    assert p.h.device_status() == 0
+    other.same()
