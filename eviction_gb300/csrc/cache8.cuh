@@ -73,7 +73,8 @@ cudaError_t launch_attend(const Cache& c, int format, const AttendArgs& a, cudaS
 // runs (a decode step is a chain of kernels of a few microseconds: their launch
 // latencies overlap).  before_all() comes first in a kernel: nothing is read or written
 // until that one has completed and its writes are visible; the next kernel's launch
-// may begin then.
+// may begin then.  No kernel reads through the read-only path (__ldg, restrict): that is
+// for data that does not change while a kernel runs, and the one before still writes.
 __device__ __forceinline__ void before_all() {
   asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
     // Lane i looks after token i of a step.
     auto block_of = [&](int step) {
       const int t = step * kTile + lane;
-      return step < end && t < len ? __ldg(table + by_bs.div(t)) : -1;
+      return step < end && t < len ? table[by_bs.div(t)] : -1;
     };
     // start the copies of a step, whose tokens lie in the lanes' blocks `blk`
     auto fetch = [&](int step, int blk, int stage) {
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
       for (int k = 0; k < KV; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          raw[nt][k][i] = there ? __ldg(reinterpret_cast<const uint4*>(qp + (k * 4 + q4) * 16 + i * 8))
+          raw[nt][k][i] = there ? *reinterpret_cast<const uint4*>(qp + (k * 4 + q4) * 16 + i * 8)
                                 : make_uint4(0, 0, 0, 0);
     }
     fetch(step, blk, 0);

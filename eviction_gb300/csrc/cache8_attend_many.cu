@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       uint4 v[D / 8];
       float mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) v[i] = there ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < D / 8; ++i) v[i] = there ? q[i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto lookup = [&](int i) {  // the tile's blocks
       const int t = (tile0 + i) * kTokens + own;
       const bool in = i < n_tiles && t < len;
-      own_blk = __ldg(table + (in ? by_bs.div(t) : 0));
+      own_blk = table[in ? by_bs.div(t) : 0];
       if (!in) own_blk = -1;
     };
     auto resolve = [&](int i) {  // rows and scales of the tile whose blocks are known
@@ -549,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool found = in && static_cast<uint32_t>(own_blk) < static_cast<uint32_t>(c.n_blocks);
       bad = bad || (in && !found);
       const size_t sc = found ? static_cast<size_t>(own_blk) * c.H : 0;
-      own_ks = __float_as_uint(__ldg(ksp + sc));
-      own_vs = __float_as_uint(__ldg(vsp + sc));
+      own_ks = __float_as_uint(ksp[sc]);
+      own_vs = __float_as_uint(vsp[sc]);
       own_row = found ? own_blk * c.H * by_bs.bs + (t - by_bs.div(t) * by_bs.bs) : -1;
     };
     auto load_codes = [&](const uint8_t* pool, uint4 (&to)[4][DB]) {
@@ -562,15 +562,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int x = 0; x < DB; ++x)
-            to[k][x] = __ldg(reinterpret_cast<const uint4*>(
-                pool + static_cast<size_t>(row[k]) * D + (q4 + 4 * x) * 16));
+            to[k][x] = *reinterpret_cast<const uint4*>(pool + static_cast<size_t>(row[k]) * D +
+                                                       (q4 + 4 * x) * 16);
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int x = 0; x < DB; ++x)
-            to[k][x] = row[k] >= 0 ? __ldg(reinterpret_cast<const uint4*>(
-                                         pool + static_cast<size_t>(row[k]) * D + (q4 + 4 * x) * 16))
+            to[k][x] = row[k] >= 0 ? *reinterpret_cast<const uint4*>(
+                                         pool + static_cast<size_t>(row[k]) * D + (q4 + 4 * x) * 16)
                                    : make_uint4(0, 0, 0, 0);
       }
     };
