@@ -486,7 +486,7 @@ int kvc_cache8_append(kvc_handle* h, const kvc_cache8* c, const kvc_rows* k, con
  *   n_q    [B] int32, 0..n, or NULL: n for every sequence.  Rows past n_q[b] are
  *          neither read nor written
  *   out    as q, its rows apart in memory (KVC_ERR_ARG where strides let them
- *          overlap).  A query that sees no token (its position is before the first)
+ *          overlap); may be q itself.  A query that sees no token (its position is before the first)
  *          gets zeros
  *   lse    [n_layers][B][H*G][n] fp32 contiguous, or NULL: the natural logarithm
  *          of the sum of exp(scale q.k), -inf for a query that sees no token

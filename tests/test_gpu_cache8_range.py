@@ -1,5 +1,5 @@
-"""Attention over the 8-bit paged cache at the ends of what its scales and queries may hold, on both
-kernels, within the per-token bound of tests/cache8_bounds.py."""
+"""The 8-bit paged cache at the ends of what its scales and queries may hold, and calls that reach the
+attention kernel for many queries, within the per-token bound of tests/cache8_bounds.py."""
 import numpy as np
 import pytest
 import torch
@@ -34,7 +34,7 @@ def _check(p, q, n_q=None, absent=None, status=0):
     assert (off <= 0).all(), (off.max(), np.argwhere(off > 0)[:3])
     seen = np.isfinite(wl)
     assert np.array_equal(np.isneginf(gl), ~seen)
-    assert (np.abs(gl - wl)[seen] <= ltol[seen]).all()
+    assert (np.abs(gl[seen] - wl[seen]) <= ltol[seen]).all()
     return got, gl
 
 
@@ -161,6 +161,108 @@ def test_zero_keys_under_large_queries(n, room):
     q = np.full((1, 1, 2, n, 64), 1.75 * 2.0 ** 127)
     q[:, :, 1, :, ::2] *= -1
     _check(p, q)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("room", [1, 256])
+def test_bad_pages_are_absent_for_many_queries(room, fmt):
+    """Tokens of a block out of range do not count, wherever it lies; limits stay where they were."""
+    n, lens = 40, [60, 200, 333, 50]
+    p = Pair(1, 4, 1, 64, 16, 21, fmt, G=2, window=64, room=room)
+    p.fill(lens)
+    good = p.ref.table.copy()
+    absent = np.zeros((4, 400), bool)
+    for b, i, what in ((0, 3, 10 ** 7), (1, 0, -1), (2, 8, p.ref.N), (2, 20, -5), (3, 0, -1), (3, 1, -1),
+                       (3, 2, -1)):
+        p.ref.table[b, i] = what
+        absent[b, i * 16:(i + 1) * 16] = True
+    p.sync_up()
+    p.ref.table[:] = good
+    q = p.rng.standard_normal((1, 4, 2, n, 64))
+    _check(p, q, absent=absent, status=cr.BAD_INDEX)
+
+
+@pytest.mark.parametrize("scale", [0.03, 1.0, 3.5])
+@pytest.mark.parametrize("n,room", KERNELS)
+def test_softmax_scale_of_the_configuration(n, room, scale):
+    p = Pair(1, 3, 2, 128, 16, 30, "e4m3", G=3, window=64, room=room, softmax_scale=scale)
+    p.scale = float(np.float32(scale))
+    p.fill([450, 33, n])
+    _check(p, p.rng.standard_normal((1, 3, 6, n, 128)))
+
+
+def test_split_heads_of_many_queries_on_two_streams():
+    """Two handles at once, both with heads cut into parts and a second launch that joins them."""
+    import eviction_gb300 as kvc
+    p = Pair(1, 2, 2, 128, 16, 130, "e4m3", G=4, window=64, room=64)
+    p.fill([2000, 1500])
+    h2 = kvc.Handle(p.cfg)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    want, got = [], []
+    for n in (40, 64):
+        q, out, lse = p.attend(n)
+        want.append((q, out, lse))
+    torch.cuda.synchronize()
+    for i in range(40):
+        for h, s in zip((p.h, h2), streams):
+            q, out, lse = want[i % 2]
+            o, l = torch.empty_like(out), torch.empty_like(lse)
+            o.record_stream(s), l.record_stream(s)
+            s.wait_stream(torch.cuda.current_stream())
+            h.cache8_attend(p.c, q, o, lse=l, stream=s)
+            got.append((i % 2, o, l))
+    torch.cuda.synchronize()
+    for k, o, l in got:
+        assert torch.equal(o, want[k][1]) and torch.equal(l, want[k][2])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_largest_blocks_of_many_queries(fmt):
+    p = Pair(1, 2, 1, 128, 1024, 3, fmt, G=2, window=40, room=64)
+    p.fill([2100, 1025])
+    p.attend(40)
+
+
+def test_large_group_of_many_queries():
+    p = Pair(1, 2, 1, 64, 16, 4, "int8", G=512, window=8, room=64)
+    p.fill([60, 7])
+    p.attend(8)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,room", [(1, 1), (3, 1), (40, 1), (40, 512)])
+def test_output_in_the_queries_place(n, room, d):
+    """out may be q itself, also where a head's tokens are cut into parts."""
+    p = Pair(1, 2, 2, d, 16, 130, "e4m3", G=4, window=64, room=room)
+    p.fill([2000, 77])
+    q, out, lse = p.attend(n)
+    l2 = torch.zeros_like(lse)
+    p.h.cache8_attend(p.c, q, q, lse=l2)
+    assert torch.equal(q, out) and torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("n,room", KERNELS)
+def test_captured_attention_of_growing_sequences(n, room):
+    """One graph, replayed while the sequences grow past what they were at its capture."""
+    p = Pair(1, 3, 2, 64, 16, 60, "int8", G=2, window=64, room=room)
+    p.fill([n, 100, 0])
+    q = torch.randn((1, 3, 4, n, 64), device="cuda").to(torch.bfloat16)
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:4], device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            p.h.cache8_attend(p.c, q, out, lse=lse)
+    torch.cuda.synchronize()
+    for more in ([0, 0, 0], [1, 300, 17], [500, 5, 128], [3, 400, 600]):
+        assert p.grow(more) == 0
+        if max(more):
+            p.append(more)
+        q.normal_()
+        g.replay()
+        p.check_attend(q, out, lse)
+    assert p.h.device_status() == 0
 
 
 # ---- compaction between formats ----
