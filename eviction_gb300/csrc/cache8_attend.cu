@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(32 * W, kSmWarps / W)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float x = fmaxf(fmaxf(z[0][nt][j], z[0][nt][2 + j]), fmaxf(z[1][nt][j], z[1][nt][2 + j]));
-          up = up || x > m[nt][j] + kSlack;
+          up = up || x - m[nt][j] > kSlack;  // (not x > m + kSlack: that sum may round)
         }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll

@@ -55,6 +55,10 @@ constexpr int kInfos = 4;         // tiles whose scales are told ahead
 constexpr int kTmemCols = 256;    // S / P: 128, O: up to 128
 constexpr int kMaxParts = 320;    // CTAs of a call that cuts heads
 constexpr float kRoom = 15.f, kStart = 8.f;  // log2 of the weights' limit and of a new m's
+// From references of this size on the logits are rounded (as in the reference) before m is
+// taken off them, column by column: one rounding of the difference would leave weights
+// off by up to half a step of the logits, 2^-3 here.
+constexpr float kExactRef = 1048576.f;
 // log2 of how far below the tile's largest scale a plain tile's scales lie at most.  Keys:
 // e4m3's last step is 2^-9, fp16's 2^-24.
 constexpr int kSpread = 8, kKeySpread = 15;
@@ -380,9 +384,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       // ---- new references: what is there is scaled to them ----
-      const bool raise = top > m + kRoom;
+      const bool raise = top - m > kRoom;  // (not top > m + kRoom: that sum may round)
       if (__any_sync(0xffffffffu, raise)) {
-        const float next = raise ? top - kStart : m;
+        // (where top's own steps are 16, top - kStart may round to top - 16)
+        const float next = !raise ? m : top - (top - kStart) > kRoom ? top : top - kStart;
         const float keep = raise ? ex2(m - next) : 1.f;
         m = next;
         sum *= keep;
@@ -407,9 +412,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       // ---- weights: S's columns become P's ----
       const float ref = m == -INFINITY ? 0.f : m;
       const float add = info.v_ref - ref;
-      const float2 ff = make_float2(f, f), off = make_float2(add, add);
+      const float2 ff = make_float2(f, f), off = make_float2(add, add), back = make_float2(-ref, -ref);
       float2 part_sum = make_float2(0.f, 0.f);
-      if (info.plain) {
+      if (info.plain && __all_sync(0xffffffffu, fabsf(ref) < kExactRef)) {
         auto weights = [&](const uint32_t (&v)[32], int first, auto masked) {
           uint32_t p[16];
 #pragma unroll
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               float2 z = make_float2(__uint_as_float(va[at]) * bf16_lo(y ? b4.z : b4.x),
                                      __uint_as_float(va[at + 1]) * bf16_lo(y ? b4.w : b4.y));
               z = fma2(z, ff, y ? make_float2(e4.z, e4.w) : make_float2(e4.x, e4.y));
-              z = add2(z, off);
+              z = add2(z, back);
               z.x = k * 32 + at < seen ? ex2(z.x) : 0.f;
               z.y = k * 32 + at + 1 < seen ? ex2(z.y) : 0.f;
               part_sum = fma2(z, make_float2(bf16_hi(y ? b4.z : b4.x), bf16_hi(y ? b4.w : b4.y)),
@@ -627,10 +632,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         v_min = min(v_min, o.w);
       }
       const bool plain = v_max - v_min <= kSpread && k_max - k_min <= kKeySpread;
-      if (!plain) {
-        s_e[st * kTokens + own] = there ? static_cast<float>(ve) : -INFINITY;
-        s_back[st * kTokens + own] = there ? __float_as_uint(exp2_int(-ve)) | own_ks >> 16 : 0x3f80u;
-      }
+      // (a plain tile's scales are in its references)
+      s_e[st * kTokens + own] = plain ? static_cast<float>(v_max)
+                                      : there ? static_cast<float>(ve) : -INFINITY;
+      s_back[st * kTokens + own] =
+          plain ? 0x3f803f80u : there ? __float_as_uint(exp2_int(-ve)) | own_ks >> 16 : 0x3f80u;
       if (lane == 0 && cw == 0) {
         TileInfo info;
         info.k_ref = plain ? exp2_int(k_max) : 1.f;

@@ -479,9 +479,9 @@ int kvc_cache8_append(kvc_handle* h, const kvc_cache8* c, const kvc_rows* k, con
  * its largest magnitude: exact for elements down to 2^-14 of it, below that to 2^-25
  * of it.  Softmax weights have 11 bits, down to 2^-14 of the row's largest weight times
  * value scale, below that to 2^-25 of it.  Any finite q will do: a query row's logits
- * are exact to fp32's rounding as long as softmax_scale log2(e) max|q| times the key
- * scale is finite in fp32 (beyond, that factor is taken as the largest fp32 number).
- * A q that is not finite spoils its own row.
+ * are exact to fp32's rounding as long as they, and softmax_scale max|q| times the key
+ * scale, stay finite in fp32 when multiplied by log2(e) (a larger factor is taken as the
+ * largest fp32 number).  A q that is not finite spoils its own row.
  *   q      [n_layers][B][H*G][n][d] bf16 rows, 1 <= n <= window
  *   n_q    [B] int32, 0..n, or NULL: n for every sequence.  Rows past n_q[b] are
  *          neither read nor written

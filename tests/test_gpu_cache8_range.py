@@ -164,6 +164,39 @@ def test_zero_keys_under_large_queries(n, room):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("n,room", KERNELS)
+def test_logits_of_any_size(n, room, fmt):
+    """Logits from 2^13 to 2^62 that are all but equal (a few of fp32's steps apart, one step is 2^16
+    and more of a weight from 2^27 on): the output stays within the values, and lse with the logits."""
+    d, tokens = 64, 3000
+    p = Pair(1, 1, 1, d, 16, 188, fmt, G=2, window=64, room=room, seed=n)
+    p.fill([tokens])
+    p.ref.pool[0][:] = 0
+    p.ref.pool[0][..., 0] = _first(96, fmt)
+    codes = cr.encode(p.rng.integers(-100, 101, p.ref.pool[0].shape[:-1]).astype(float), fmt)
+    p.ref.pool[0][..., 1] = codes
+    v = p.ref.rows(1, 0, 0, 0)
+    for exp in range(7, 57):
+        p.ref.scale[0][:] = 2.0 ** (exp - 3)
+        p.sync_up()
+        for sign in (1, -1):
+            q = np.zeros((1, 1, 2, n, d))
+            q[..., 0], q[..., 1] = sign * 8 * 1.25, 8 * 2.0 ** -21
+            q[:, :, 1, :, 0] *= 1.5
+            qt = torch.from_numpy(q).to(torch.bfloat16).cuda()
+            out = torch.full_like(qt, 7.0)
+            lse = torch.full(qt.shape[:4], 7.0, device="cuda")
+            p.h.cache8_attend(p.c, qt, out, lse=lse)
+            got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+            assert np.isfinite(got).all() and np.isfinite(gl).all(), exp
+            # (a mean of values, each weight off by 2^-11, rounded to bf16)
+            room_for = 2.0 ** -7 * np.abs(v).max(0)
+            assert (got <= v.max(0) + room_for).all() and (got >= v.min(0) - room_for).all(), exp
+            z = q[..., 0] * 96 * 2.0 ** (exp - 3) * p.scale
+            assert (np.abs(gl - z) <= 2.0 ** -16 * np.abs(z) + np.log(tokens)).all(), exp
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("room", [1, 256])
 def test_bad_pages_are_absent_for_many_queries(room, fmt):
     """Tokens of a block out of range do not count, wherever it lies; limits stay where they were."""
