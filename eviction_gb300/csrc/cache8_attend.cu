@@ -37,7 +37,7 @@
 // is not go to the workspace, and the last CTA of it to finish joins them in order
 // (the result does not depend on which one that is).
 //
-// Measured: 64 sequences of 612 to 1112 tokens, 8 KV heads of 4 (114 MB) 26.7 us, 4.3
+// Measured: 64 sequences of 612 to 1112 tokens, 8 KV heads of 4 (114 MB) 26.9 us, 4.2
 // TB/s; 4 sequences of 32768, 4 heads of 7, int8 (134 MB) 30 us, 4.5 TB/s; one head of
 // 768 tokens 7.7 us.  Loads straight into registers, one step ahead, took 37 and 52 us.
 #include "cache8_attend.cuh"
@@ -52,8 +52,14 @@ constexpr int kStages = 2;
 constexpr int kSmWarps = 12;     // warps of an SM, by registers and shared memory
 constexpr int kMaxCtas = kCounters;  // CTAs of a call
 constexpr float kSlack = 8.f;    // log2 of how far a weight may pass 1
-// Steps that beginning and ending a head costs a small CTA (512 heads of 612 to 1112
-// tokens: 28.5 us at 0, 27.6 at 4, 26.7 at 8, 27.0 at 12).
+// Steps that beginning and ending a head costs a small CTA.  In us at 0 / 4 / 8 / 12 / 16:
+//   512 heads of 4 rows, 612-1112 tokens       28.6 / 27.7 / 26.8 / 27.2 / 27.5
+//   1024 heads of 4 rows, 40-300 tokens        28.7 / 23.5 / 22.9 / 23.1 / 23.2
+//   256 heads of 8 rows, 500-4000, d 64        23.2 / 22.2 / 21.7 / 21.5 / 21.8
+//   256 heads of 16 rows, 1000-3000            42.7 / 42.0 / 40.7 / 41.4 / 41.6
+//   192 heads of 5 rows, all 2048, int8        26.6 / 26.0 / 25.4 / 24.9 / 25.7
+//   256 heads of 7 rows, 64-8000               54.2 / 52.3 / 50.9 / 50.7 / 51.0
+//   128 heads of 28 rows, 1000-1536            33.9 / 32.7 / 32.6 / 32.7 / 31.8
 constexpr int kHeadCost = 8;
 constexpr int kMinRounds = 3;    // steps of a CTA's warps at least, before a head is cut
 

@@ -491,7 +491,11 @@ int kvc_cache8_append(kvc_handle* h, const kvc_cache8* c, const kvc_rows* k, con
  *   lse    [n_layers][B][H*G][n] fp32 contiguous, or NULL: the natural logarithm
  *          of the sum of exp(scale q.k), -inf for a query that sees no token
  * A sequence whose n_q is out of range is skipped; tokens in a block that is out
- * of range count as absent (both BAD_INDEX). */
+ * of range count as absent (both BAD_INDEX).
+ * Two kernels share the work, both within the arithmetic above: calls of few query
+ * rows (G*n <= 32, or little work in all), and calls of many.  The work is counted
+ * from max_blocks * block_size, since the lengths are on the device: a table with much
+ * more room than its sequences use may send a call to the slower one. */
 int kvc_cache8_attend(kvc_handle* h, const kvc_cache8* c, const kvc_rows* q, int n,
                       const int32_t* n_q, const kvc_rows* out, float* lse, void* stream);
 
