@@ -18,6 +18,8 @@ inline bool aligned16(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 inline int cuda_fail(kvc_handle* h, cudaError_t e, const char* where) {
   return fail(h, KVC_ERR_CUDA, std::string(where) + ": " + cudaGetErrorString(e));
 }
@@ -60,6 +62,69 @@ inline void mark_end(kvc_handle* h, int kernel, cudaEvent_t begin, cudaStream_t 
   do {                                                                        \
     if (!(p)) return fail(h, KVC_ERR_ARG, "null pointer: " #p);               \
     if (!aligned16(p)) return fail(h, KVC_ERR_ALIGN, "not 16-byte aligned: " #p); \
+  } while (0)
+
+// Strides are multiples of 8 values and not negative.  An output's rows may not share
+// memory: each axis has to step over all that the axes of smaller strides span (true of
+// any slice or permutation of a dense array).  Strides of axes of size 1 do not matter.
+inline int check_rows(kvc_handle* h, const kvc_rows* r, const char* name, bool written, int L, int B,
+                      int heads, int n) {
+  if (!r || !r->data) return fail(h, KVC_ERR_ARG, std::string("null pointer: ") + name);
+  if (!aligned16(r->data)) return fail(h, KVC_ERR_ALIGN, std::string("not 16-byte aligned: ") + name);
+  const int64_t stride[4] = {r->layer, r->seq, r->head, r->token};
+  const int size[4] = {L, B, heads, n};
+  for (int i = 0; i < 4; ++i) {
+    if (size[i] > 1 && (stride[i] < 0 || stride[i] % 8))
+      return fail(h, KVC_ERR_ALIGN, std::string("strides must be multiples of 8 and >= 0: ") + name);
+    if (!written || size[i] == 1) continue;
+    __int128 span = h->dims.d;  // values from the first to past the last of the axes below
+    for (int k = 0; k < 4; ++k)
+      if (size[k] > 1 && (stride[k] < stride[i] || (stride[k] == stride[i] && k < i)))
+        span += static_cast<__int128>(stride[k]) * (size[k] - 1);
+    if (stride[i] < span) return fail(h, KVC_ERR_ARG, std::string("rows overlap: ") + name);
+  }
+  return KVC_OK;
+}
+
+// The handle's device has to be the current one.
+inline int check_device(kvc_handle* h) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(h, e, "current device");
+  if (dev != h->device)
+    return fail(h, KVC_ERR_DEVICE, "the handle belongs to another device than the current one");
+  return KVC_OK;
+}
+
+// What an entry point does after its checks: the launch between two tracing marks.
+// Nothing thrown (an allocation of the error text or of a mark) leaves the C ABI.
+template <class F>
+int run(kvc_handle* h, int kernel, const char* name, void* stream, F launch) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaEvent_t b = mark_begin(h, s);
+  cudaError_t e = launch(s);
+  if (e != cudaSuccess) return cuda_fail(h, e, name);
+  mark_end(h, kernel, b, s);
+  return KVC_OK;
+}
+template <class F>
+int guarded(F f) {
+  try {
+    return f();
+  } catch (...) {
+    return KVC_ERR_NOMEM;
+  }
+}
+
+#define KVC_TRY(expr)               \
+  do {                              \
+    if (const int rc_ = (expr)) return rc_; \
+  } while (0)
+
+#define KVC_REQUIRE_INTS(p)                                                       \
+  do {                                                                            \
+    if (!(p)) return fail(h, KVC_ERR_ARG, "null pointer: " #p);                   \
+    if (!aligned4(p)) return fail(h, KVC_ERR_ALIGN, "not 4-byte aligned: " #p);   \
   } while (0)
 
 inline float scale_log2_of(const kvc_config& c) {

@@ -5,16 +5,17 @@
 
 #include "api_util.cuh"
 #include "cache8.cuh"
+#include "prompt.cuh"
 
 using kvc::aligned16;
-using kvc::cuda_fail;
+using kvc::aligned4;
+using kvc::check_device;
+using kvc::check_rows;
 using kvc::fail;
-using kvc::mark_begin;
-using kvc::mark_end;
+using kvc::guarded;
+using kvc::run;
 
 namespace {
-
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int check_cache(const kvc_config& cfg, const kvc_cache8* c, const char** why) {
   auto bad = [&](int code, const char* m) {
@@ -48,38 +49,6 @@ int check_cache(const kvc_config& cfg, const kvc_cache8* c, const char** why) {
   return KVC_OK;
 }
 
-// Strides are multiples of 8 values and not negative.  An output's rows may not share
-// memory: each axis has to step over all that the axes of smaller strides span (true of
-// any slice or permutation of a dense array).  Strides of axes of size 1 do not matter.
-int check_rows(kvc_handle* h, const kvc_rows* r, const char* name, bool written, int L, int B,
-               int heads, int n) {
-  if (!r || !r->data) return fail(h, KVC_ERR_ARG, std::string("null pointer: ") + name);
-  if (!aligned16(r->data)) return fail(h, KVC_ERR_ALIGN, std::string("not 16-byte aligned: ") + name);
-  const int64_t stride[4] = {r->layer, r->seq, r->head, r->token};
-  const int size[4] = {L, B, heads, n};
-  for (int i = 0; i < 4; ++i) {
-    if (size[i] > 1 && (stride[i] < 0 || stride[i] % 8))
-      return fail(h, KVC_ERR_ALIGN, std::string("strides must be multiples of 8 and >= 0: ") + name);
-    if (!written || size[i] == 1) continue;
-    __int128 span = h->dims.d;  // values from the first to past the last of the axes below
-    for (int k = 0; k < 4; ++k)
-      if (size[k] > 1 && (stride[k] < stride[i] || (stride[k] == stride[i] && k < i)))
-        span += static_cast<__int128>(stride[k]) * (size[k] - 1);
-    if (stride[i] < span) return fail(h, KVC_ERR_ARG, std::string("rows overlap: ") + name);
-  }
-  return KVC_OK;
-}
-
-// The handle's device has to be the current one.
-int check_device(kvc_handle* h) {
-  int dev = -1;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(h, e, "current device");
-  if (dev != h->device)
-    return fail(h, KVC_ERR_DEVICE, "the handle belongs to another device than the current one");
-  return KVC_OK;
-}
-
 int check(kvc_handle* h, const kvc_cache8* c) {
   const char* why = "";
   const int rc = check_cache(h->cfg, c, &why);
@@ -95,37 +64,6 @@ kvc::cache8::Cache view(const kvc_handle* h, const kvc_cache8& c) {
 kvc::cache8::Rows rows(const kvc_rows& r) {
   return {r.data, r.layer, r.seq, r.head, r.token};
 }
-
-// What an entry point does after its checks: the launch between two tracing marks.
-// Nothing thrown (an allocation of the error text or of a mark) leaves the C ABI.
-template <class F>
-int run(kvc_handle* h, int kernel, const char* name, void* stream, F launch) {
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaEvent_t b = mark_begin(h, s);
-  cudaError_t e = launch(s);
-  if (e != cudaSuccess) return cuda_fail(h, e, name);
-  mark_end(h, kernel, b, s);
-  return KVC_OK;
-}
-template <class F>
-int guarded(F f) {
-  try {
-    return f();
-  } catch (...) {
-    return KVC_ERR_NOMEM;
-  }
-}
-
-#define KVC_TRY(expr)               \
-  do {                              \
-    if (const int rc_ = (expr)) return rc_; \
-  } while (0)
-
-#define KVC_REQUIRE_INTS(p)                                                       \
-  do {                                                                            \
-    if (!(p)) return fail(h, KVC_ERR_ARG, "null pointer: " #p);                   \
-    if (!aligned4(p)) return fail(h, KVC_ERR_ALIGN, "not 4-byte aligned: " #p);   \
-  } while (0)
 
 }  // namespace
 
@@ -202,6 +140,33 @@ int kvc_cache8_attend(kvc_handle* h, const kvc_cache8* c, const kvc_rows* q, int
                               kvc::scale_log2_of(h->cfg), h->num_sms, h->ws.attend};
     return run(h, kvc::kKernelCache8Attend, "cache8 attend", stream, [&](cudaStream_t s) {
       return kvc::cache8::launch_attend(view(h, *c), c->format, a, s);
+    });
+  });
+}
+
+int kvc_cache8_weigh(kvc_handle* h, const kvc_cache8* c, const kvc_rows* q, int n,
+                     const int32_t* first, const int32_t* n_q, const float* lse, float decay,
+                     float* weights, int cap, void* stream) {
+  if (!h) return KVC_ERR_ARG;
+  return guarded([&] {
+    KVC_TRY(check(h, c));
+    if (n < 1 || n >= 1 << 30) return fail(h, KVC_ERR_SHAPE, "n must lie in [1, 2^30)");
+    if (cap < 1 || cap >= 1 << 30) return fail(h, KVC_ERR_SHAPE, "cap must lie in [1, 2^30)");
+    if (!(decay >= 0.f && decay <= 1.f)) return fail(h, KVC_ERR_ARG, "decay must lie in [0, 1]");
+    if (first && !n_q) return fail(h, KVC_ERR_ARG, "packed queries need n_q");
+    const int Hq = h->dims.H * h->dims.G;
+    KVC_TRY(check_rows(h, q, "q", false, c->n_layers, first ? 1 : h->dims.B, Hq, n));
+    if (first && !aligned4(first)) return fail(h, KVC_ERR_ALIGN, "not 4-byte aligned: first");
+    if (n_q && !aligned4(n_q)) return fail(h, KVC_ERR_ALIGN, "not 4-byte aligned: n_q");
+    KVC_REQUIRE_INTS(lse);
+    KVC_REQUIRE_INTS(weights);
+    const long long units = static_cast<long long>(c->n_layers) * h->dims.B * h->dims.H;
+    if (units > INT_MAX / (cap / 32 + 8ll))
+      return fail(h, KVC_ERR_UNSUPPORTED, "n_layers * batch * n_kv_heads * (cap / 32 + 8) must be < 2^31");
+    kvc::prompt::WeighArgs a{rows(*q), first, n_q, lse, weights, n, h->dims.G, cap,
+                             kvc::scale_log2_of(h->cfg), decay, h->num_sms};
+    return run(h, kvc::kKernelCache8Weigh, "cache8 weigh", stream, [&](cudaStream_t s) {
+      return kvc::prompt::launch_weigh(view(h, *c), c->format, a, s);
     });
   });
 }

@@ -40,7 +40,8 @@ const char* const kKernelNames[kvc::kNumKernels] = {
     "usage_pass1_rowstats_tcgen05", "usage_pass2_colsum_tcgen05", "mass_pool_ema",
     "segment_quota", "select_topk", "gather_compact", "refresh_trigger", "compact_paged",
     "redundancy_score", "mass_segment_select", "cache8_grow", "cache8_append", "cache8_attend",
-    "cache8_gather", "cache8_compact", "cache8_fork", "cache8_free"};
+    "cache8_gather", "cache8_compact", "cache8_fork", "cache8_free", "rotary", "prompt_attend",
+    "cache8_weigh", "keep_heaviest"};
 
 // Step 1: both passes of the window attention usage into the workspace.
 int run_usage(kvc_handle* h, const uint16_t* q, const uint16_t* k, int T, const int32_t* pad,

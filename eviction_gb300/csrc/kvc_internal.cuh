@@ -61,6 +61,10 @@ enum KernelId {
   kKernelCache8Compact,
   kKernelCache8Fork,
   kKernelCache8Free,
+  kKernelRotary,
+  kKernelPromptAttend,
+  kKernelCache8Weigh,
+  kKernelKeepHeaviest,
   kNumKernels
 };
 

@@ -23,7 +23,8 @@ ENTRY_POINTS = ("kvc_default_config", "kvc_create", "kvc_destroy", "kvc_stage_si
                 "kvc_compact_paged", "kvc_redundancy_score", "kvc_wait_self_test",
                 "kvc_event_host", "kvc_mass_select", "kvc_cache8_check", "kvc_cache8_grow",
                 "kvc_cache8_append", "kvc_cache8_attend", "kvc_cache8_gather",
-                "kvc_cache8_compact", "kvc_cache8_fork", "kvc_cache8_free")
+                "kvc_cache8_compact", "kvc_cache8_fork", "kvc_cache8_free", "kvc_rope_init",
+                "kvc_rotary", "kvc_prompt_attend", "kvc_cache8_weigh", "kvc_keep_heaviest")
 
 STATUS = {0: "KVC_OK", -1: "KVC_ERR_ARG", -2: "KVC_ERR_SHAPE", -3: "KVC_ERR_ALIGN",
           -4: "KVC_ERR_NOMEM", -5: "KVC_ERR_CUDA", -6: "KVC_ERR_DEVICE", -7: "KVC_ERR_TIMEOUT",
@@ -132,6 +133,17 @@ class _Rows(ctypes.Structure):
                                               for k in ("layer", "seq", "head", "token")]
 
 
+class _RopeConfig(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_int) for k in ("dim", "interleaved", "scaling")] +
+                [(k, ctypes.c_double) for k in ("base", "factor", "low", "high", "original",
+                                                "magnitude")])
+
+
+class _CRope(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("magnitude", ctypes.c_float), ("turn", ctypes.c_uint64 * 64)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -182,6 +194,11 @@ def load_library():
     L.kvc_cache8_compact.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P, _P, _P]
     L.kvc_cache8_fork.argtypes = [_P, _P, _I, _P, _P, _P]
     L.kvc_cache8_free.argtypes = [_P, _P, _I, _P, _P]
+    L.kvc_rope_init.argtypes = [ctypes.POINTER(_RopeConfig), ctypes.POINTER(_CRope)]
+    L.kvc_rotary.argtypes = [_P] * 6 + [_I] * 3 + [_P] * 3
+    L.kvc_prompt_attend.argtypes = [_P] * 4 + [_I, _I] + [_P] * 5
+    L.kvc_cache8_weigh.argtypes = [_P, _P, _P, _I, _P, _P, _P, ctypes.c_float, _P, _I, _P]
+    L.kvc_keep_heaviest.argtypes = [_P, _P, _I, _I] + [_P] * 5
     L.kvc_status_string.argtypes = [_I]
     L.kvc_status_string.restype = ctypes.c_char_p
     for name in ENTRY_POINTS:
@@ -293,6 +310,28 @@ class Cache8:
         """A cache of other sequences in the same pools and free stack (kvc_cache8_compact's dst)."""
         return Cache8(self.k_pool, self.v_pool, self.k_scale, self.v_scale, table, seq_len,
                       self.free_list, self.free_top, self.ref_count)
+
+
+class Rope:
+    """Rotary positions (kvc_rope of include/kvc.h): the first `dim` values of a row turn, pairs in
+    halves or interleaved; scaling "none", "linear", "ntk" (factor) or "bands" (factor, low, high,
+    original).  Computed on the host once; Handle.rotary takes it."""
+
+    SCALINGS = ("none", "linear", "ntk", "bands")
+
+    def __init__(self, dim, base=10000.0, interleaved=False, scaling="none", factor=1.0, low=1.0,
+                 high=4.0, original=0.0, magnitude=1.0):
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"scaling: one of {self.SCALINGS}, got {scaling!r}")
+        cfg = _RopeConfig(dim, int(bool(interleaved)), self.SCALINGS.index(scaling), base, factor,
+                          low, high, original, magnitude)
+        self._c = _CRope()
+        rc = load_library().kvc_rope_init(ctypes.byref(cfg), ctypes.byref(self._c))
+        if rc != 0:
+            raise KvcError(rc, "kvc_rope_init: dim a multiple of 16 up to 128, base >= 1, factor and "
+                               "magnitude > 0, for bands 0 <= low < high and original > 0")
+        self._ref = ctypes.byref(self._c)
+        self.dim = dim
 
 
 class Handle:
@@ -577,6 +616,114 @@ class Handle:
         self._check(load_library().kvc_cache8_free(
             self._h, ref, seqs.numel(), self._ints(seqs, "seqs", (seqs.numel(),), cache.device),
             self._stream(stream)), "kvc_cache8_free")
+
+    def cache8_weigh(self, cache, q, lse, weights, n_q=None, first=None, decay=1.0, stream=None):
+        """kvc_cache8_weigh: weights [L, B, H, cap] fp32 (in place) gather what the newest tokens'
+        queries give them.  q [L, B, H*G, n, d] bf16 (any strides), lse [L, B, H*G, n] fp32, n_q
+        [B] int32 or None; packed, with first [B] int32: q [L, H*G, n, d], lse [L, H*G, n]."""
+        import torch
+        ref = self._cache8(cache)
+        L, B = cache.n_layers, cache.batch
+        seqs = () if first is not None else (B,)
+        n = q.shape[-2] if q.dim() == 4 + len(seqs) else 0
+        shape = (L, *seqs, cache.n_kv_heads * self.cfg.group, n, cache.head_dim)
+        if lse.shape != shape[:-1]:
+            raise ValueError(f"lse: expected shape {shape[:-1]}, got {tuple(lse.shape)}")
+        if weights.dim() != 4 or weights.shape[:3] != (L, B, cache.n_kv_heads):
+            raise ValueError(f"weights: expected shape {(L, B, cache.n_kv_heads)} + (cap,), got "
+                             f"{tuple(weights.shape)}")
+        self._check(load_library().kvc_cache8_weigh(
+            self._h, ref, self._strided(q, "q", shape, cache.device, 1 if seqs else None), n,
+            None if first is None else self._ints(first, "first", (B,), cache.device),
+            None if n_q is None else self._ints(n_q, "n_q", (B,), cache.device),
+            self._on(lse, torch.float32, "lse", cache.device), decay,
+            self._on(weights, torch.float32, "weights", cache.device), weights.shape[3],
+            self._stream(stream)), "kvc_cache8_weigh")
+
+    # -- prompts ---------------------------------------------------------------
+    @staticmethod
+    def _strided(t, name, shape, device, seq_axis, layer_axis=0):
+        """kvc_rows of a bf16 tensor of `shape`, (..., heads, n, d), of any strides, d contiguous;
+        the axes of layers and sequences, None where there is none."""
+        import torch
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+            raise TypeError(f"{name}: expected a torch.bfloat16 tensor")
+        if t.device != device:
+            raise ValueError(f"{name}: on {t.device}, expected {device}")
+        if t.shape != shape or t.stride(-1) != 1:
+            raise ValueError(f"{name}: expected shape {shape}, the last axis contiguous")
+        s = t.stride()
+        return ctypes.byref(_Rows(t.data_ptr(), 0 if layer_axis is None else s[layer_axis],
+                                  0 if seq_axis is None else s[seq_axis], s[-3], s[-2]))
+
+    def rotary(self, rope, pos, q=None, k=None, q_out=None, k_out=None, n_tok=None, stream=None):
+        """kvc_rotary: rows of q [L, S, H*G, n, d] and k [L, S, H, n, d] bf16 (any strides; either
+        may be None) turned by pos [S, n] int32 into q_out and k_out (None: in place); n_tok [S]
+        int32 or None.  S sequences of the call's own: packed prompts are one."""
+        if not isinstance(rope, Rope):
+            raise TypeError("rope: expected a Rope")
+        c = self.cfg
+        one = q if q is not None else k
+        if one is None:
+            raise ValueError("q, k or both")
+        L, S, _, n = one.shape[:4] if one.dim() == 5 else (0,) * 4
+        rows = []
+        for name, t, out, heads in (("q", q, q_out, c.n_kv_heads * c.group),
+                                    ("k", k, k_out, c.n_kv_heads)):
+            if t is None and out is not None:
+                raise ValueError(f"{name}_out without {name}")
+            shape = (L, S, heads, n, c.head_dim)
+            rows.append([None if x is None else self._strided(x, nm, shape, self._device, 1)
+                         for nm, x in ((name, t), (name + "_out", t if out is None else out))])
+        self._check(load_library().kvc_rotary(
+            self._h, rope._ref, rows[0][0], rows[1][0], rows[0][1], rows[1][1], L, S, n,
+            self._ints(pos, "pos", (S, n), self._device),
+            None if n_tok is None else self._ints(n_tok, "n_tok", (S,), self._device),
+            self._stream(stream)), "kvc_rotary")
+
+    def prompt_attend(self, q, k, v, out, lse=None, first=None, n_tok=None, stream=None):
+        """kvc_prompt_attend: causal attention over whole prompts.  Padded: q, out [S, H*G, n, d], k,
+        v [S, H, n, d] bf16 (any strides), lse [S, H*G, n] fp32 or None, n_tok [S] int32 or None.
+        Packed, with first [S] int32: the same without S, and n_tok."""
+        import torch
+        c, seqs = self.cfg, ()
+        if first is None:
+            seqs = (q.shape[0],)
+        S = seqs[0] if seqs else first.numel()
+        n = q.shape[-2] if q.dim() == 3 + len(seqs) else 0
+        heads = (*seqs, c.n_kv_heads * c.group)
+        rows = [self._strided(t, name, (*seqs, x, n, c.head_dim), self._device, 0 if seqs else None, None)
+                for name, t, x in (("q", q, heads[-1]), ("k", k, c.n_kv_heads), ("v", v, c.n_kv_heads),
+                                   ("out", out, heads[-1]))]
+        if lse is not None and lse.shape != (*heads, n):
+            raise ValueError(f"lse: expected shape {(*heads, n)}, got {tuple(lse.shape)}")
+        self._check(load_library().kvc_prompt_attend(
+            self._h, rows[0], rows[1], rows[2], S, n,
+            None if first is None else self._ints(first, "first", (S,), self._device),
+            None if n_tok is None else self._ints(n_tok, "n_tok", (S,), self._device), rows[3],
+            None if lse is None else self._on(lse, torch.float32, "lse", self._device),
+            self._stream(stream)), "kvc_prompt_attend")
+
+    def keep_heaviest(self, weights, seq_len, kept_idx, n_kept, weights_out, stream=None):
+        """kvc_keep_heaviest: the tokens that an eviction keeps by weights [L, B, H, cap] fp32 of
+        sequences of seq_len [B] int32: kept_idx [L, B, H, budget], n_kept [L, B, H] int32, and
+        their weights in weights_out [L, B, H, cap] (may be weights)."""
+        import torch
+        c = self.cfg
+        if weights.dim() != 4 or weights.shape[1:3] != (c.batch, c.n_kv_heads):
+            raise ValueError(f"weights: expected shape (L, {c.batch}, {c.n_kv_heads}, cap), got "
+                             f"{tuple(weights.shape)}")
+        if weights_out.shape != weights.shape:
+            raise ValueError(f"weights_out: expected shape {tuple(weights.shape)}, got "
+                             f"{tuple(weights_out.shape)}")
+        units = tuple(weights.shape[:3])
+        self._check(load_library().kvc_keep_heaviest(
+            self._h, self._on(weights, torch.float32, "weights", self._device), units[0],
+            weights.shape[3], self._ints(seq_len, "seq_len", (c.batch,), self._device),
+            self._ints(kept_idx, "kept_idx", units + (c.budget,), self._device),
+            self._ints(n_kept, "n_kept", units, self._device),
+            self._on(weights_out, torch.float32, "weights_out", self._device),
+            self._stream(stream)), "kvc_keep_heaviest")
 
     def wait_self_test(self, stream=None):
         """kvc_wait_self_test: a bounded wait that runs out on purpose (about

@@ -377,11 +377,13 @@ int kvc_refresh_decision(kvc_handle* h, const uint16_t* q, float* q_ref, float t
  *   kvc_cache8_grow    reserve blocks for the new tokens (once a step)
  *   kvc_cache8_append  quantise a layer's new keys and values into them
  *   kvc_cache8_attend  attention of the layer's new queries over the cache
+ *   kvc_cache8_weigh   the weight that it gave each token, gathered for an eviction
  * and a compression event every few hundred steps is
  *   kvc_cache8_gather  the cache as the dense rows that kvc_mass_select takes
  *   kvc_cache8_compact the kept rows, requantised, into another cache's blocks
  *   kvc_cache8_free    the old blocks back onto the free stack.
- * kvc_cache8_fork starts further samples of a prompt from its cache.
+ * An eviction by gathered weight is kvc_keep_heaviest in place of gather and the event,
+ * then compact and free.  kvc_cache8_fork starts further samples of a prompt from its cache.
  *
  * Codes.  A code c stands for c * scale.  KVC_CACHE8_E4M3: c is an e4m3 float
  * (4 exponent bits, 3 mantissa bits, largest 448); KVC_CACHE8_INT8: c is a signed
@@ -499,6 +501,48 @@ int kvc_cache8_append(kvc_handle* h, const kvc_cache8* c, const kvc_rows* k, con
 int kvc_cache8_attend(kvc_handle* h, const kvc_cache8* c, const kvc_rows* q, int n,
                       const int32_t* n_q, const kvc_rows* out, float* lse, void* stream);
 
+/* Attention weight that the newest tokens' queries give each token of the cache, added to
+ * what it has gathered: for every layer, sequence and KV head
+ *   weights[t] = decay weights[t] + sum over the group's heads and the queries j that see
+ *                t (t <= seq_len[b] - n_q[b] + j) of exp(scale q_j . k_t - lse_j),
+ * t < seq_len[b].  With the lse of kvc_cache8_attend (or kvc_prompt_attend) the terms are
+ * the softmax weights of that attention ("H2O: Heavy-Hitter Oracle for Efficient
+ * Generative Inference of Large Language Models", the accumulated attention score).
+ *   q        as for kvc_cache8_attend, but n may be any number of tokens >= 1
+ *   first    NULL: [n_layers][B][H*G][n][d].  [B] int32: packed, the queries of sequence b
+ *            are rows first[b] .. first[b] + n_q[b] - 1 of [n_layers][H*G][n][d] (the
+ *            strides' seq is not used)
+ *   n_q      [B] int32, 0 .. seq_len[b], or NULL (not packed): n
+ *   lse      fp32, contiguous, [n_layers][B][H*G][n], packed [n_layers][H*G][n]; a query
+ *            whose lse is -inf or +inf sees no token
+ *   decay    in [0, 1]; 0 overwrites: weights are not read then
+ *   weights  [n_layers][B][H][cap] fp32, in/out; a token that is new has 0 (or whatever
+ *            it shall begin with).  Entries at and past seq_len[b] are left as they are
+ * Arithmetic: products of bf16 values with codes, accumulated in fp32; weights and their
+ * sums in fp32, in a fixed order.  A sequence whose seq_len, n_q or first is out of range, or
+ * longer than cap, is skipped; tokens in a block that is out of range count as absent and
+ * keep decay times their weight (both BAD_INDEX). */
+int kvc_cache8_weigh(kvc_handle* h, const kvc_cache8* c, const kvc_rows* q, int n,
+                     const int32_t* first, const int32_t* n_q, const float* lse, float decay,
+                     float* weights, int cap, void* stream);
+
+/* The tokens that an eviction by gathered weight keeps, per layer, sequence and KV head:
+ * with len = seq_len[b] and n = min(len, budget), the last r = min(n_recent, budget) tokens,
+ * the first min(n_sink, budget - r), and the heaviest of the others up to n in all (equal
+ * weights: the lower position first; NaN counts as lightest).
+ *   weights      [n_layers][B][H][cap] fp32 (kvc_cache8_weigh's)
+ *   seq_len      [B] int32, 0..cap
+ *   kept_idx     [n_layers][B][H][budget] int32 out: positions, ascending, -1 past n_kept
+ *   n_kept       [n_layers][B][H] int32 out = n
+ *   weights_out  [n_layers][B][H][cap] fp32 out: the kept tokens' weights in their new
+ *                places, 0 past n_kept; may be weights itself
+ * The rows follow with kvc_cache8_compact, T = cap and a pad of zeros.  budget, n_sink and
+ * n_recent are the configuration's; cap in [1, max_T].  A sequence whose length is out of
+ * range is skipped (BAD_INDEX). */
+int kvc_keep_heaviest(kvc_handle* h, const float* weights, int n_layers, int cap,
+                      const int32_t* seq_len, int32_t* kept_idx, int32_t* n_kept,
+                      float* weights_out, void* stream);
+
 /* The cache as dense, left-padded bf16 rows, as kvc_mass_select and kvc_event
  * take them: pad[b] = T - seq_len[b], slot pad[b] + t holds token t, padding is
  * zero.  Every code times its scale is a bf16 value: nothing is rounded.
@@ -542,6 +586,90 @@ int kvc_cache8_fork(kvc_handle* h, const kvc_cache8* c, int n, const int32_t* sr
  * Changes nothing, with KVC_STATUS_BAD_INDEX, where a number repeats or anything
  * is out of range. */
 int kvc_cache8_free(kvc_handle* h, const kvc_cache8* c, int n, const int32_t* seqs, void* stream);
+
+/* ---- prompts: rotary positions and attention ------------------------------
+ * How a prompt gets into a cache: kvc_rotary turns its queries and keys by their
+ * positions, kvc_prompt_attend is the attention of all its tokens, kvc_cache8_append
+ * quantises its keys and values. */
+
+/* Rotary positions.  Pair i of a row's first dim values, (x, y), is turned by
+ * pos * f_i: (x cos - y sin, x sin + y cos), times magnitude; i = 0 .. dim/2 - 1.  The
+ * pairs are values i and i + dim/2, or 2i and 2i + 1 where interleaved.  The other
+ * values of a row stay as they are.  With f = base^(-2i/dim), f_i is
+ *   KVC_ROPE_NONE    f
+ *   KVC_ROPE_LINEAR  f / factor (interpolated positions)
+ *   KVC_ROPE_NTK     that of the base times factor^(dim / (dim - 2))
+ *   KVC_ROPE_BANDS   (1 - m) f / factor + m f, m = (original f / 2pi - low) /
+ *                    (high - low) within [0, 1]: pairs that turn more than `high`
+ *                    times over `original` tokens keep f, those below `low` turns
+ *                    are interpolated ("YaRN: Efficient Context Window Extension of
+ *                    Large Language Models", 3.2, which also scales the rows by
+ *                    magnitude = 0.1 ln(factor) + 1).
+ * Positions are multiplied in 64-bit fixed point: an angle is off by 2^-29 and 2^-51 of
+ * itself at most.  Sines, products and sums are fp32, the result is rounded once. */
+#define KVC_ROPE_NONE 0
+#define KVC_ROPE_LINEAR 1
+#define KVC_ROPE_NTK 2
+#define KVC_ROPE_BANDS 3
+
+typedef struct {
+  int dim;          /* values of a row that turn: a multiple of 16, 16..128 */
+  int interleaved;  /* 0 or 1 */
+  int scaling;      /* KVC_ROPE_* */
+  double base;      /* >= 1 */
+  double factor;    /* > 0 */
+  double low, high; /* KVC_ROPE_BANDS: 0 <= low < high */
+  double original;  /* KVC_ROPE_BANDS: > 0 */
+  double magnitude; /* > 0 */
+} kvc_rope_config;
+
+/* What kvc_rotary takes; filled by kvc_rope_init, on the host, once. */
+typedef struct {
+  int dim, interleaved;
+  float magnitude;
+  uint64_t turn[64]; /* a pair's turns per token, in 2^-64 of a turn */
+} kvc_rope;
+
+int kvc_rope_init(const kvc_rope_config* cfg, kvc_rope* rope);
+
+/* Turn the rows of q and k by their tokens' positions, in place or into other rows.
+ *   q, q_out  [n_layers][n_seq][H*G][n][d] bf16 rows (kvc_rows of the 8-bit cache
+ *             above); both NULL: only keys
+ *   k, k_out  [n_layers][n_seq][H][n][d]; both NULL: only queries
+ *   pos       [n_seq][n] int32 positions, in all layers.  Negative ones turn back: a
+ *             key of position p with pos = p' - p is the key of position p' (rounded
+ *             once more)
+ *   n_tok     [n_seq] int32, 0..n, or NULL: n.  Rows past it are neither read nor
+ *             written; a sequence whose count is out of range is skipped (BAD_INDEX)
+ * Sizes are the call's own (the handle gives H, G and d): packed prompts are one
+ * sequence of all their tokens.  Output rows lie apart in memory; they are the input's
+ * (same pointer and strides) or do not overlap any input. */
+int kvc_rotary(kvc_handle* h, const kvc_rope* rope, const kvc_rows* q, const kvc_rows* k,
+               const kvc_rows* q_out, const kvc_rows* k_out, int n_layers, int n_seq, int n,
+               const int32_t* pos, const int32_t* n_tok, void* stream);
+
+/* Causal attention over whole prompts, one layer:
+ *   out_j = sum_t softmax_t(scale q_j . k_t) v_t over t <= j of the same sequence,
+ * head h*G+g of q reads KV head h; scale is the configuration's softmax_scale.
+ *   q, out  [n_seq][H*G][n][d] bf16 rows (the strides' layer is not used; out's rows
+ *           apart in memory, none of them an input's)
+ *   k, v    [n_seq][H][n][d]
+ *   first   NULL: padded, sequence b is tokens 0 .. n_tok[b]-1 of its n rows.
+ *           [n_seq] int32: packed, all sequences lie among the same n rows (the
+ *           strides' seq is not used), sequence b is rows first[b] .. first[b] +
+ *           n_tok[b] - 1.  They must not overlap
+ *   n_tok   [n_seq] int32, >= 0; NULL (padded only): n
+ *   lse     fp32, contiguous, [n_seq][H*G][n] padded, [H*G][n] packed, or NULL: the
+ *           natural logarithm of the sum of exp(scale q.k)
+ * Rows of no sequence may hold anything: they change nothing and out and lse are not
+ * written there.  A sequence that does not lie within its n rows is skipped (BAD_INDEX).
+ * Arithmetic: products of bf16 operands accumulated in fp32; maxima and sums in fp32; the
+ * softmax weights are rounded to bf16 for the product with v.  q, k and v must be finite
+ * in the rows of sequences: what is not spoils rows of its own sequence.
+ * n and n_seq * n below 2^30, H*G and H at most 65535, strides below 2^39 values. */
+int kvc_prompt_attend(kvc_handle* h, const kvc_rows* q, const kvc_rows* k, const kvc_rows* v,
+                      int n_seq, int n, const int32_t* first, const int32_t* n_tok,
+                      const kvc_rows* out, float* lse, void* stream);
 
 /* ---- failure-path self-test -------------------------------------------
  * No counterpart in the pages: a check of the library's own failure path.
