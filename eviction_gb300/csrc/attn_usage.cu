@@ -613,14 +613,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ host ----
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
-                                   void*, const cuuint64_t*, const cuuint64_t*,
-                                   const cuuint32_t*, const cuuint32_t*,
-                                   CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion,
-                                   CUtensorMapFloatOOBfill);
+}  // namespace
 
-EncodeTiledFn get_encode(std::string* err) {
+EncodeTiledFn tensor_map_encoder(std::string* err) {
   static EncodeTiledFn fn = nullptr;
   if (fn) return fn;
   void* ptr = nullptr;
@@ -635,6 +630,8 @@ EncodeTiledFn get_encode(std::string* err) {
   return fn;
 }
 
+namespace {
+
 // 3-D view of a [rows][d] bf16 tensor: x = 64 elements of a K block (128 B),
 // y = row (stride d*2 B), z = K block (stride 128 B).  A box of
 // 64 x box_rows x d/64 lands in shared memory as d/64 consecutive
@@ -643,7 +640,7 @@ EncodeTiledFn get_encode(std::string* err) {
 // the end of the tensor read as zero.
 bool make_map(CUtensorMap* m, const void* base, uint64_t rows, int d, int box_rows,
               std::string* err) {
-  EncodeTiledFn enc = get_encode(err);
+  EncodeTiledFn enc = tensor_map_encoder(err);
   if (!enc) return false;
   cuuint64_t dims[3] = {64, rows, static_cast<cuuint64_t>(d / 64)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, 128};

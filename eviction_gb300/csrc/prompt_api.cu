@@ -110,8 +110,11 @@ int kvc_prompt_attend(kvc_handle* h, const kvc_rows* q, const kvc_rows* k, const
   return guarded([&] {
     if (n_seq < 1 || n < 1) return fail(h, KVC_ERR_SHAPE, "n_seq and n must be >= 1");
     const int H = h->dims.H, Hq = H * h->dims.G, S = first ? 1 : n_seq;
-    if (n >= 1 << 30 || static_cast<long long>(n_seq) * n >= 1 << 30 || Hq > 65535)
-      return fail(h, KVC_ERR_UNSUPPORTED, "n_seq * n must be < 2^30, n_kv_heads * group < 2^16");
+    // (the kernel counts pairs of tiles of 8 tokens at least, and one more a sequence)
+    const long long tokens = static_cast<long long>(S) * n;
+    if (n_seq > 1 << 20 || tokens >= 1 << 30 || Hq > 65535 || (tokens / 16 + n_seq) * Hq > INT_MAX)
+      return fail(h, KVC_ERR_UNSUPPORTED, "n_seq must be <= 2^20, the tokens < 2^30, n_kv_heads * group < "
+                                          "2^16 and (tokens / 16 + n_seq) * n_kv_heads * group < 2^31");
     if (first && !n_tok) return fail(h, KVC_ERR_ARG, "packed sequences need n_tok");
     KVC_TRY(check_device(h));
     const struct {
@@ -124,6 +127,9 @@ int kvc_prompt_attend(kvc_handle* h, const kvc_rows* q, const kvc_rows* k, const
       const int64_t most = int64_t{1} << 39;
       if (x.r->seq >= most || x.r->head >= most || x.r->token >= most)
         return fail(h, KVC_ERR_UNSUPPORTED, std::string("strides must be < 2^39: ") + x.name);
+      if ((n > 1 && x.r->token == 0) || (x.r == q && Hq > 1 && q->head == 0))
+        return fail(h, KVC_ERR_UNSUPPORTED, std::string("rows of tokens (of q: also of heads) must not "
+                                                        "be the same: ") + x.name);
     }
     if (first && !aligned4(first)) return fail(h, KVC_ERR_ALIGN, "not 4-byte aligned: first");
     KVC_TRY(check_counts(h, n_tok));

@@ -666,7 +666,9 @@ int kvc_rotary(kvc_handle* h, const kvc_rope* rope, const kvc_rows* q, const kvc
  * Arithmetic: products of bf16 operands accumulated in fp32; maxima and sums in fp32; the
  * softmax weights are rounded to bf16 for the product with v.  q, k and v must be finite
  * in the rows of sequences: what is not spoils rows of its own sequence.
- * n and n_seq * n below 2^30, H*G and H at most 65535, strides below 2^39 values. */
+ * Limits (KVC_ERR_UNSUPPORTED): n_seq <= 2^20, tokens (n packed, n_seq n padded) < 2^30, H*G <
+ * 2^16, (tokens / 16 + n_seq) H G < 2^31, strides < 2^39 values; tokens' strides, and the
+ * heads' of q, must not be 0. */
 int kvc_prompt_attend(kvc_handle* h, const kvc_rows* q, const kvc_rows* k, const kvc_rows* v,
                       int n_seq, int n, const int32_t* first, const int32_t* n_tok,
                       const kvc_rows* out, float* lse, void* stream);
