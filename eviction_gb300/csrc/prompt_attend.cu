@@ -44,10 +44,10 @@ using cache8::div_up;
 
 constexpr int kRows = 128, kTokens = 128;  // rows of a tile, keys of a step
 constexpr int kSoftmaxWarps = 8;           // 4 a tile
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kItemWarp = 11;  // (two warps issue products)
 constexpr int kThreads = 32 * 12;
 constexpr int kItems = 4;        // items told ahead
-constexpr int kReaders = kSoftmaxWarps + 2;
+constexpr int kReaders = kSoftmaxWarps + 3;
 constexpr int kSorted = 128;     // sequences (or groups of them) in the list of items
 constexpr int kPacked = 16;      // heads in a tile at most
 constexpr float kRoom = 32.f;    // log2 of the largest weight
@@ -67,6 +67,7 @@ struct Item {
   int h, hq;        // KV head, first query head
   int len, t0;      // tokens of the sequence, first token of tile 0
   int steps[2];     // of 128 keys, of each tile; 0: no more items
+  __device__ __forceinline__ int of(int t) const { return t ? steps[1] : steps[0]; }
 };
 
 template <int D>
@@ -74,7 +75,7 @@ struct Smem {
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kQ = 0, kRing = 2 * kTile, kBars = kRing + kStages * kTile,
-                       kNumBars = 2 * kStages + 10 + 2 * kItems + 1,
+                       kNumBars = 2 * kStages + 12 + 2 * kItems + 1,
                        kItem = (kBars + kNumBars * 8 + 15) & ~15, kMisc = kItem + kItems * 32,
                        kUpTo = kMisc + 16, kCount = kUpTo + (kSorted + 1) * 4,
                        kSeq = kCount + (kSorted + 1) * 4, kBytes = kSeq + kSorted + 1024;
@@ -84,6 +85,45 @@ struct Smem {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           uint32_t* status) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
+
+// Products issued by the lanes for which `issue` holds, one of a converged warp: without a
+// branch around them their operands stay in uniform registers.  (A branch on the lane,
+// with 64-bit descriptors made for each product, took 110 cycles a product to issue;
+// 128 x 128 x 16 take 64 to compute.)  Descriptors: the low word, the high one is the same for all.
+constexpr uint32_t kDescHigh = 1024 >> 4 | 1u << 14 | 2u << 29;  // as in sw128_desc
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t block) {
+  return (addr & 0x3FFFFu) >> 4 | (block >> 4) << 16;
+}
+__device__ __forceinline__ void mma_ss_if(bool issue, uint32_t d_tmem, uint32_t a_low, uint32_t b_low,
+                                          uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(static_cast<int>(accumulate)),
+      "r"(static_cast<int>(issue)), "r"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(bool issue, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low,
+                                          uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 b, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(static_cast<int>(accumulate)),
+      "r"(static_cast<int>(issue)), "r"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(bool issue, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(static_cast<int>(issue))
+      : "memory");
 }
 
 // Tokens of sequence b, 0 where it does not lie within its rows.
@@ -111,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kBars);
   uint64_t *kv_full = bars, *kv_empty = bars + NS, *q_full = bars + 2 * NS, *q_empty = q_full + 2,
-           *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2, *i_full = o_full + 2,
+           *s_full = q_empty + 2, *p_full = s_full + 2, *o_full = p_full + 2, *turn = o_full + 2, *i_full = turn + 2,
            *i_empty = i_full + kItems, *done = bars + Sm::kNumBars - 1;
   Item* items = reinterpret_cast<Item*>(smem + Sm::kItem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sm::kMisc);
@@ -125,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&kv_empty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
@@ -133,12 +173,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 4);
       mbar_init(&o_full[t], 1);
+      mbar_init(&turn[t], 1);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&i_full[i], 1);
       mbar_init(&i_empty[i], kReaders);
     }
-    mbar_init(done, 1);
+    mbar_init(done, 2);
     *abort = 0;
     fence_barrier_init();
     prefetch_tensormap(&map_q);
@@ -228,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item it;
     for (int i = 0; read_item(i, it) && it.steps[1] > 0; ++i) {
       leave_item(i);
-      const int n_steps = it.steps[t], t0 = it.t0 + t * p.tok;
+      const int n_steps = it.of(t), t0 = it.t0 + t * p.tok;
       const int token = t0 + row_token;     // this row's token, and the last that it sees
       float m = -INFINITY, sum = 0.f;       // reference of the weights, their sum
       bool ok = true;
@@ -266,12 +307,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float keep = raise ? ex2(m - top) : 1.f;
           if (raise) m = top;
           sum *= keep;
-          if (j > 0) {  // what is there is scaled to the new references
-            if (!warp_wait(&o_full[t], (step - 1) & 1, abort, a.status)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
+          if (j > 0) {  // what is there is scaled to the new references (the last step's product
+                        // was issued before these scores: it is done)
 #pragma unroll 1
             for (int k = 0; k < D / 16; ++k) {
               uint32_t o[16];
@@ -308,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the result ----
-      if (!warp_wait(&o_full[t], (step - 1) & 1, abort, a.status)) break;
+      if (!warp_wait(&o_full[t], i & 1, abort, a.status)) break;
       tc_fence_after();
       const bool there = row_token < p.tok && token < it.len;
       const float inv = 1.f / sum;
@@ -337,82 +374,113 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
       // ------------------------------------------------------------ products
-      // (all lanes run the loop and wait converged; lane 0 issues)
+      // A warp for each tile: the tensor pipe takes a product only when the one ahead of it
+      // has begun, so that a single warp's waits (100 cycles each) left it idle.  The tiles
+      // take turns, a step's products and the next one's scores at a time: where both issued
+      // as they liked, they fell into step, products of both, then softmax of both (3780
+      // cycles a step of both tiles; the products alone are 2048).  All that a turn needs is
+      // waited for before it, and it is passed on a few products before its end.
+      // (All lanes run the loop and wait converged.)
+      const int t = warp - kMmaWarp;
       const uint32_t base = smem_u32(smem);
-      int n_p[2] = {0, 0};  // weights consumed, of each tile
-      int q_uses[2] = {0, 0};
-      int kv0 = 0;          // the item's first stage use
-      auto stage_of = [&](int use) { return base + Sm::kRing + use % NS * Sm::kTile; };
-      auto cols_of = [&](const Item& it, int t, int j) {  // columns that some row sees, in 16s
-        const int last = min(it.t0 + (t + 1) * p.tok, it.len) - 1;
-        const int n = (last - j * kTokens + 16) & ~15;
-        return n < 16 || n > kTokens ? kTokens : n;  // (a tile of no rows: all)
+      const bool lead = lane == 0;
+      const uint32_t s_tmem = tmem + t * 128, o_tmem = tmem + kOutCol + t * D;
+      const uint32_t q_low = desc_low(base + Sm::kQ + t * Sm::kTile, 16);
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_test(bar, parity)) || warp_wait(bar, parity, abort, a.status);
       };
-      auto scores = [&](const Item& it, int t, int j, int use) {  // S = Q K^T
-        if (j == 0 && !warp_wait(&q_full[t], q_uses[t]++ & 1, abort, a.status)) return false;
-        if (!warp_wait(&kv_full[use % NS], (use / NS) & 1, abort, a.status)) return false;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t idesc = idesc_bf16_f32(kRows, cols_of(it, t, j));
-          const uint32_t q = base + Sm::kQ + t * Sm::kTile, k = stage_of(use);
+      // 16s of columns that some row of the tile sees in a step
+      auto cols_of = [&](const Item& it, int j) {
+        if (j + 1 < it.of(t)) return kTokens / 16;
+        const int end = min(it.t0 + (t + 1) * p.tok, it.len) - j * kTokens;
+        return (end + 15) >> 4;
+      };
+      int st = 0;            // the next stage, and its uses' parity
+      uint32_t st_parity = 0;
+      auto take = [&](int* stage) {
+        const bool ok = wait(&kv_full[st], st_parity);
+        *stage = st;
+        if (++st == NS) st = 0, st_parity ^= 1;
+        return ok;
+      };
+      auto scores = [&](int stage, int n, bool end) {  // S = Q K^T
+        const uint32_t idesc = idesc_bf16_f32(kRows, 0) | static_cast<uint32_t>(n) << 18;
+        const uint32_t k = desc_low(base + Sm::kRing + stage * Sm::kTile, 16);
 #pragma unroll
-          for (int x = 0; x < D / 16; ++x) {
-            const uint32_t off = (x / 4) * kBlock + (x % 4) * 32;
-            mma_bf16(tmem + t * 128, sw128_desc(q + off), sw128_desc(k + off), idesc, x > 0);
-          }
-          mma_commit(&s_full[t]);
-          if (t == 1) mma_commit(&kv_empty[use % NS]);
-          if (j + 1 == it.steps[t]) mma_commit(&q_empty[t]);
+        for (int x = 0; x < D / 16; ++x) {
+          const uint32_t off = ((x / 4) * kBlock + (x % 4) * 32) >> 4;
+          mma_ss_if(lead, s_tmem, q_low + off, k + off, idesc, x > 0);
+          if (x == D / 16 - 3 && lead) mbar_arrive(&turn[t ^ 1]);
         }
-        __syncwarp();
-        return true;
+        commit_if(lead, &s_full[t]);
+        commit_if(lead, &kv_empty[stage]);
+        if (end) commit_if(lead, &q_empty[t]);
       };
-      auto output = [&](const Item& it, int t, int j, int use) {  // O += P V
-        if (!warp_wait(&kv_full[use % NS], (use / NS) & 1, abort, a.status)) return false;
-        const int rows = it.len - j * kTokens;  // of V that are the sequence's
-        if (rows < kTokens && t == (it.steps[0] == it.steps[1] ? 0 : 1)) {
-          // the rest, up to the last step of 16, is zeroed
-          const int end = min((rows + 15) & ~15, kTokens);
-          uint8_t* v = smem + Sm::kRing + use % NS * Sm::kTile;
-          for (int x = lane; x < (end - rows) * (D / 8); x += 32)
-            *reinterpret_cast<uint4*>(v + (x % (D / 8) / 8) * kBlock + (rows + x / (D / 8)) * 128 +
-                                      x % 8 * 16) = make_uint4(0, 0, 0, 0);
-          fence_async_shared();
-          __syncwarp();
-        }
-        if (!warp_wait(&p_full[t], n_p[t]++ & 1, abort, a.status)) return false;
+      uint32_t p_parity = 0, turn_parity = t ^ 1;
+      auto my_turn = [&]() {
+        const bool ok = wait(&turn[t], turn_parity);
+        turn_parity ^= 1;
         tc_fence_after();
-        if (lane == 0) {
-          constexpr uint32_t idesc = idesc_bf16_f32(kRows, D) | 1u << 16;
-          const uint32_t v = stage_of(use);
-          const int n = cols_of(it, t, j) / 16;
-          for (int x = 0; x < n; ++x)
-            mma_f16_ts(tmem + kOutCol + t * D, tmem + t * 128 + x * 8, sw128_desc_mn(v + x * 2048, kBlock),
-                       idesc, j > 0 || x > 0);
-          mma_commit(&o_full[t]);
-          if (t == 1) mma_commit(&kv_empty[use % NS]);
-        }
-        __syncwarp();
-        return true;
+        return ok;
       };
       Item it, next;
-      bool ok = read_item(0, it) && it.steps[1] > 0;
-      for (int t = 0; ok && t < 2; ++t) ok = scores(it, t, 0, 0);
+      int ks, vs;  // stages of keys, of values
+      bool ok = read_item(0, it) && it.steps[1] > 0 && wait(&q_full[t], 0) && take(&ks) && my_turn();
+      if (ok) scores(ks, cols_of(it, 0), it.of(t) == 1);
       for (int i = 0; ok; ++i) {
-        ok = read_item(i + 1, next);
-        leave_item(i);
-        const bool more = ok && next.steps[1] > 0;
-        for (int j = 0; ok && j < it.steps[1]; ++j)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (ok && j < it.steps[t]) ok = output(it, t, j, kv0 + 2 * j + 1);
-            if (ok && j + 1 < it.steps[t]) ok = scores(it, t, j + 1, kv0 + 2 * j + 2);
-            if (ok && j + 1 == it.steps[1] && more) ok = scores(next, t, 0, kv0 + 2 * j + 2);
+        const int steps = it.of(t);
+        for (int j = 0; ok && j < it.steps[1]; ++j) {
+          const bool last = j + 1 == it.steps[1], own_last = j + 1 == steps;
+          if (last) {
+            ok = read_item(i + 1, next);
+            leave_item(i);
+            if (!ok) break;
           }
-        kv0 += 2 * it.steps[1];
-        if (!more) break;
+          const bool more = !last || next.steps[1] > 0;
+          // all that this turn needs
+          ok = take(&vs);
+          const int n = cols_of(it, j), rows = it.len - j * kTokens;
+          if (ok && j < steps && rows < 16 * n) {
+            // rows of V behind the sequence, up to the last step of 16, are zeroed (by both warps)
+            uint8_t* v = smem + Sm::kRing + vs * Sm::kTile;
+            for (int x = lane; x < (16 * n - rows) * (D / 8); x += 32)
+              *reinterpret_cast<uint4*>(v + (x % (D / 8) / 8) * kBlock + (rows + x / (D / 8)) * 128 +
+                                        x % 8 * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_shared();
+            __syncwarp();
+          }
+          ok = ok && (!more || take(&ks)) && (!(last && more) || wait(&q_full[t], (i + 1) & 1));
+          if (ok && j < steps) {
+            ok = wait(&p_full[t], p_parity);
+            p_parity ^= 1;
+          }
+          if (!ok || !my_turn()) {
+            ok = false;
+            break;
+          }
+          if (j < steps) {  // O += P V
+            constexpr uint32_t idesc = idesc_bf16_f32(kRows, D) | 1u << 16;
+            const uint32_t v = desc_low(base + Sm::kRing + vs * Sm::kTile, kBlock);
+#pragma unroll
+            for (int x = 0; x < kTokens / 16; ++x)
+              mma_ts_if(lead && x < n, o_tmem, s_tmem + x * 8, v + x * (2048 >> 4), idesc, j > 0 || x > 0);
+            commit_if(lead, &kv_empty[vs]);
+            if (own_last) commit_if(lead, &o_full[t]);
+          } else if (lead) {
+            mbar_arrive(&kv_empty[vs]);
+          }
+          if (j + 1 < steps) {
+            scores(ks, cols_of(it, j + 1), j + 2 == steps);
+          } else if (last && more) {
+            scores(ks, cols_of(next, 0), next.of(t) == 1);
+          } else if (lead) {  // no scores in this turn
+            mbar_arrive(&turn[t ^ 1]);
+            if (more) mbar_arrive(&kv_empty[ks]);
+          }
+        }
+        if (!ok || next.steps[1] == 0) break;
         it = next;
       }
       if (lane == 0) mma_commit(done);
