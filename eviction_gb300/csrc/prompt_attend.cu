@@ -73,8 +73,9 @@ struct Item {
 template <int D>
 struct Smem {
   static constexpr int kTile = 128 * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr int kQ = 0, kRing = 2 * kTile, kBars = kRing + kStages * kTile,
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kQ = 0, kRing = 2 * kTile, kOut = kRing + kStages * kTile,
+                       kBars = kOut + kSoftmaxWarps * 4096,
                        kNumBars = 2 * kStages + 12 + 2 * kItems + 1,
                        kItem = (kBars + kNumBars * 8 + 15) & ~15, kMisc = kItem + kItems * 32,
                        kUpTo = kMisc + 16, kCount = kUpTo + (kSorted + 1) * 4,
@@ -262,6 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp / 4;  // tile
     const int row = threadIdx.x % 128;
     const int row_token = row / p.P, row_head = row - row_token * p.P;
+    const int warp_token0 = __shfl_sync(0xffffffffu, row_token, 0),
+              warp_token1 = __shfl_sync(0xffffffffu, row_token, 31);  // of the warp's rows
     const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
     const uint32_t s_tmem = tmem + lanes + t * 128, o_tmem = tmem + lanes + kOutCol + t * D;
     const float f = a.scale_log2;
@@ -271,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       leave_item(i);
       const int n_steps = it.of(t), t0 = it.t0 + t * p.tok;
       const int token = t0 + row_token;     // this row's token, and the last that it sees
+      const int first_token = t0 + warp_token0, last_token = t0 + warp_token1;
       float m = -INFINITY, sum = 0.f;       // reference of the weights, their sum
       bool ok = true;
       for (int j = 0; j < n_steps; ++j, ++step) {
@@ -280,27 +284,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         uint32_t v[4][32];
-        float top;
-        if (j * kTokens + kTokens - 1 <= t0) {  // all rows see all of it
-          float mx[4];
+        float mx[4];
+        const int c0 = j * kTokens;
+        if (c0 + kTokens - 1 <= first_token) {  // all rows of the warp see all of it
 #pragma unroll
           for (int k = 0; k < 4; ++k) tmem_ld32_max(s_tmem + 32 * k, v[k], mx[k]);
           tmem_ld_wait();
-          top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         } else {
-          const int seen = token - j * kTokens + 1;  // columns that this row sees
+          const int seen = token - c0 + 1;  // columns that this row sees
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld32(s_tmem + 32 * k, v[k]);
-          tmem_ld_wait();
-          top = -INFINITY;
+          for (int k = 0; k < 4; ++k) {
+            mx[k] = -INFINITY;
+            if (c0 + 32 * k + 31 <= first_token) {
+              tmem_ld32_max(s_tmem + 32 * k, v[k], mx[k]);
+              tmem_ld_wait();
+            } else if (c0 + 32 * k <= last_token) {
+              tmem_ld32(s_tmem + 32 * k, v[k]);
+              tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+              for (int x = 0; x < 32; ++x) {
+                if (32 * k + x >= seen) v[k][x] = 0xff800000u;  // -inf
+                mx[k] = fmaxf(mx[k], __uint_as_float(v[k][x]));
+              }
+            } else {  // none of them
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              if (32 * k + x >= seen) v[k][x] = 0xff800000u;  // -inf
-              top = fmaxf(top, __uint_as_float(v[k][x]));
+              for (int x = 0; x < 32; ++x) v[k][x] = 0xff800000u;
             }
+          }
         }
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         top *= f;
         const bool raise = top - m > kRoom;
         if (__any_sync(0xffffffffu, raise)) {
@@ -323,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float ref = m == -INFINITY ? 0.f : m;
         const float2 ff = make_float2(f, f), off = make_float2(-ref, -ref);
         float2 part = make_float2(0.f, 0.f);
+        uint32_t w[4][16];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t w[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             float2 z = fma2(make_float2(__uint_as_float(v[k][2 * x]), __uint_as_float(v[k][2 * x + 1])),
@@ -333,10 +345,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             z.x = ex2(z.x);
             z.y = ex2(z.y);
             part = add2(part, z);
-            w[x] = bf16x2(z.x, z.y);
+            w[k][x] = bf16x2(z.x, z.y);
           }
-          tmem_st16(s_tmem + 16 * k, w);
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_st16(s_tmem + 16 * k, w[k]);
         sum += part.x + part.y;
         tmem_st_wait();
         tc_fence_before();
@@ -349,21 +362,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool there = row_token < p.tok && token < it.len;
       const float inv = 1.f / sum;
-      uint16_t* out = a.out.at(0, it.sb, it.hq + row_head, there ? it.row0 + token : 0);
+      // 64 values of the warp's rows at a time through shared memory, so that a store
+      // writes whole lines of 4 rows (each thread its own row, 16 bytes of 32 rows a store:
+      // 6000 cycles a tile)
+      const uint64_t out = there ? reinterpret_cast<uint64_t>(
+                                       a.out.at(0, it.sb, it.hq + row_head, it.row0 + token))
+                                 : 0;
+      uint8_t* stage = smem + Sm::kOut + warp * 4096;
+      uint32_t o[DB][2][32];
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        uint32_t o[32];
-        tmem_ld32(o_tmem + 32 * k, o);
-        tmem_ld_wait();
-        if (there) {
+      for (int h = 0; h < DB; ++h)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) tmem_ld32(o_tmem + 64 * h + 32 * k, o[h][k]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int h = 0; h < DB; ++h) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             float y[8];
 #pragma unroll
-            for (int z = 0; z < 8; ++z) y[z] = __uint_as_float(o[8 * x + z]) * inv;
-            reinterpret_cast<uint4*>(out)[4 * k + x] =
+            for (int z = 0; z < 8; ++z) y[z] = __uint_as_float(o[h][k][8 * x + z]) * inv;
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * k + x) ^ (lane & 7)) << 4)) =
                 make_uint4(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]), bf16x2(y[4], y[5]), bf16x2(y[6], y[7]));
           }
+        __syncwarp();
+        uint4 y[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int r = 4 * x + lane / 8;
+          y[x] = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const uint64_t to = __shfl_sync(0xffffffffu, out, 4 * x + lane / 8);
+          if (to) reinterpret_cast<uint4*>(to)[8 * h + (lane & 7)] = y[x];
         }
         __syncwarp();
       }
