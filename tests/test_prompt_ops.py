@@ -16,7 +16,7 @@ from tests import prompt_ref as pr
 from tests.test_cache8_sources import _code, _kernels
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "eviction_gb300", "csrc")
-SOURCES = [os.path.join(CSRC, f) for f in ("rotary.cu", "prompt_attend.cu", "weigh.cu", "heaviest.cu", "prompt.cuh")]
+SOURCES = [os.path.join(CSRC, f) for f in ("rotary.cu", "prompt_attend.cu", "weigh.cu", "weigh_many.cu", "weigh.cuh", "heaviest.cu", "prompt.cuh")]
 
 
 @pytest.fixture(scope="module")
