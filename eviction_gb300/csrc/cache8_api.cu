@@ -156,6 +156,11 @@ int kvc_cache8_weigh(kvc_handle* h, const kvc_cache8* c, const kvc_rows* q, int 
     if (first && !n_q) return fail(h, KVC_ERR_ARG, "packed queries need n_q");
     const int Hq = h->dims.H * h->dims.G;
     KVC_TRY(check_rows(h, q, "q", false, c->n_layers, first ? 1 : h->dims.B, Hq, n));
+    if ((n > 1 && q->token == 0) || (Hq > 1 && q->head == 0))
+      return fail(h, KVC_ERR_UNSUPPORTED, "rows of tokens and heads must not be the same: q");
+    const int64_t most = int64_t{1} << 39;
+    if (q->layer >= most || q->seq >= most || q->head >= most || q->token >= most)
+      return fail(h, KVC_ERR_UNSUPPORTED, "strides must be < 2^39: q");
     if (first && !aligned4(first)) return fail(h, KVC_ERR_ALIGN, "not 4-byte aligned: first");
     if (n_q && !aligned4(n_q)) return fail(h, KVC_ERR_ALIGN, "not 4-byte aligned: n_q");
     KVC_REQUIRE_INTS(lse);

@@ -1,5 +1,32 @@
-// weigh.cu -- attention weight that the newest tokens' queries give each token of the 8-bit
-// paged cache, added to what it has gathered (kvc_cache8_weigh).  One thread a token.
+// weigh_many.cu -- attention weight that many queries (a prompt, or a piece of one) give each
+// token of the 8-bit paged cache, on the 5th-generation tensor cores (tcgen05 + TMEM).
+//
+//   w_t = decay w_t + sum_r 2^(f_t s_rt - y_r),  s = q_r . code_t,  f_t = scale log2(e) scale_t,
+//
+// y_r the row's log2 normaliser.  Tokens are the rows of S^T = K Q^T (TMEM lanes) and queries its
+// columns, so that a token's sum is one thread's, with its key's scale a factor of that thread.
+// Keys are codes as bf16, which holds both formats exactly, and queries are what they are in
+// memory: nothing is rounded before the product.
+//
+// A CTA has two tiles of 128 tokens and takes 256 query rows at a time for both:
+//   keys (4 warps)    codes of the item's tokens from their blocks to bf16 tiles in shared
+//                     memory, with the 128-byte swizzle; the next item's are loaded while
+//                     this one is computed;
+//   queries (1 warp)  TMA, through a ring of stages.  A group's heads lie side by side (row =
+//                     token * P + head), so that each chunk is of few tokens;
+//   sums (1 warp)     the rows' normalisers, gathered into shared memory beside their chunk;
+//   MMA (1 warp)      128 x 256 products into the tile's 256 columns of TMEM;
+//   weights (16 warps)  two warps a lane quarter and tile, a half of the columns each: scale,
+//                     exponential, sum.  One tile's exponentials run while the other's
+//                     products do.
+// Exponentials and products take the same time (512 cycles of an SM for 128 x 128), and both
+// bound this.  Chunks that a tile does not see are skipped.
+//
+// Work: pairs of tiles of all sequences, layers and heads, those with most queries first, dealt
+// to one CTA per SM in turns, back and forth.  Nothing is summed across CTAs: the result does
+// not depend on the schedule.  Every wait is bounded.
+#include <climits>
+
 #include "weigh.cuh"
 
 namespace kvc {
@@ -8,66 +35,578 @@ namespace {
 
 using namespace cache8;
 
-constexpr int kThreads = 128;
+constexpr int kTile = 128, kChunk = 256;  // tokens of a tile, query rows of a chunk
+constexpr int kWeightWarps = 16, kKeyWarp = 16, kQueryWarp = 20, kSumWarp = 21, kMmaWarp = 22,
+              kItemWarp = 23;
+constexpr int kThreads = 32 * 24;
+constexpr int kItems = 4;        // items told ahead
+constexpr int kSums = 4;         // chunks whose normalisers are told ahead
+constexpr int kReaders = kWeightWarps + 4 + 3;
+constexpr int kSorted = 128;     // sequences (or groups of them) in the list of items
+constexpr int kPacked = 16;      // heads in a chunk at most
+
+template <bool V>
+struct Bool {
+  static constexpr bool value = V;
+};
+
+struct Params {
+  WeighArgs a;
+  int P, subs, tok;   // heads in a chunk, such parts of a group, tokens of a chunk
+  int q_head, q_seq, q_layer;  // 0 where the axis' stride is 0
+};
+
+struct Item {
+  int l, b, h;        // of the cache
+  int len, nq, first;
+  int t0;             // first token of tile 0
+  int chunks;         // of a part of the group, from chunk c0 on (before it neither tile is seen)
+  int c0;             // first chunk that tile 0 sees
+  int c1;             // first chunk that tile 1 sees
+  int there;          // 0: no more items
+  int pad;
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kKeyTile = kTile * D * 2, kStage = kChunk * D * 2;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kKeys = 0, kRing = 2 * kKeyTile, kSumsAt = kRing + kStages * kStage,
+                       kFactors = kSumsAt + kSums * kChunk * 4,   // [2][2][128] f_t, by item parity
+                       kParts = kFactors + 2 * 2 * kTile * 4,     // [2][128] the second halves' sums
+                       kBars = kParts + 2 * kTile * 4,
+                       kNumBars = 2 * kStages + 2 * kSums + 2 * 6 + 2 * kItems + 1,
+                       kItem = (kBars + kNumBars * 8 + 15) & ~15, kMisc = kItem + kItems * 48,
+                       kUpTo = kMisc + 16, kCount = kUpTo + (kSorted + 1) * 4,
+                       kSeq = kCount + (kSorted + 1) * 4, kBytes = kSeq + kSorted + 1024;
+  static_assert(kBytes <= 232448, "shared memory of a block");
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          uint32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
+
+// Four codes to four bf16 (exact).
+template <int FMT>
+__device__ __forceinline__ uint2 bf16_of(uint32_t codes) {
+  float x[4];
+  decode4<FMT>(codes, x);
+  return make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
+}
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads) weigh_many_kernel(Cache c, WeighArgs a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    weigh_many_kernel(const __grid_constant__ CUtensorMap map_q, Cache c, Params p, Div by_bs) {
+#if defined(__CUDA_ARCH__) && (__CUDA_ARCH__ >= 1000)
+  using Sm = Smem<D>;
+  constexpr int DB = D / 64;
+  constexpr int NS = Sm::kStages;
+  constexpr int kKeyBlock = kTile * 128, kQueryBlock = kChunk * 128;  // bytes of 64 values of all rows
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kBars);
+  uint64_t *q_full = bars, *q_empty = bars + NS, *y_full = bars + 2 * NS, *y_empty = y_full + kSums,
+           *k_full = y_empty + kSums,
+           *k_empty = k_full + 2, *s_full = k_empty + 2, *s_empty = s_full + 2, *part_full = s_empty + 2,
+           *part_empty = part_full + 2, *i_full = part_empty + 2, *i_empty = i_full + kItems,
+           *done = i_empty + kItems;
+  static_assert(Sm::kNumBars == 2 * NS + 2 * kSums + 12 + 2 * kItems + 1, "one place for each barrier");
+  float* s_sums = reinterpret_cast<float*>(smem + Sm::kSumsAt);      // [kSums][kChunk] -y
+  float* s_factors = reinterpret_cast<float*>(smem + Sm::kFactors);  // [2][2][kTile]
+  float* s_parts = reinterpret_cast<float*>(smem + Sm::kParts);      // [2][kTile]
+  Item* items = reinterpret_cast<Item*>(smem + Sm::kItem);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sm::kMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + Sm::kMisc + 4);
+  int* s_upto = reinterpret_cast<int*>(smem + Sm::kUpTo);
+  int* s_count = reinterpret_cast<int*>(smem + Sm::kCount);
+  uint8_t* s_seq = smem + Sm::kSeq;
+  const WeighArgs& a = p.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+    }
+    for (int s = 0; s < kSums; ++s) {
+      mbar_init(&y_full[s], 1);
+      mbar_init(&y_empty[s], kWeightWarps);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&k_full[t], 4);
+      mbar_init(&k_empty[t], 1 + 8);
+      mbar_init(&s_full[t], 1);
+      mbar_init(&s_empty[t], 8);
+      mbar_init(&part_full[t], 4);
+      mbar_init(&part_empty[t], 4);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&i_full[i], 1);
+      mbar_init(&i_empty[i], kReaders);
+    }
+    mbar_init(done, 1);
+    *abort = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&map_q);
+  }
+  // query rows that no copy writes (P does not divide 256) are zeros: their products count nothing
+  for (int i = threadIdx.x; i < NS * Sm::kStage / 16; i += kThreads)
+    *reinterpret_cast<uint4*>(smem + Sm::kRing + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_async_shared();
   before_all();
-  const int per = (a.cap + kThreads - 1) / kThreads;
-  const int u = blockIdx.x / per, t = blockIdx.x % per * kThreads + threadIdx.x;
-  const int h = u % c.H, b = (u / c.H) % c.B, l = u / (c.H * c.B);
+
+  // ---- the list of items: groups of `per` sequences (one each, if they are few enough; those
+  // with most pairs of tiles first then) ----
+  const int units = c.L * c.H;
+  const int per = div_up(c.B, kSorted), groups = div_up(c.B, per);
   bool bad = false;
-  const int len = length_of(c, b, &bad);
-  const int nq = a.n_q ? a.n_q[b] : a.n, first = a.first ? a.first[b] : 0;
-  if (bad || len > a.cap || nq < 0 || nq > len || first < 0 || nq > a.n - first) {
-    if (threadIdx.x == 0 && t < kThreads) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
-    return;
+  auto pairs_of = [&](int b) { return div_up(lengths_of(c, a, b, &bad).len, 2 * kTile); };
+  if (threadIdx.x < kSorted) {
+    int n = 0;  // (cap and the sequences' number bound it: checked on the host)
+    for (int b = threadIdx.x * per; b < min((static_cast<int>(threadIdx.x) + 1) * per, c.B); ++b)
+      n += pairs_of(b);
+    s_upto[threadIdx.x] = n;
+    if (bad && blockIdx.x == 0) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
+    bad = false;
   }
-  if (t >= len) return;
-  float* w = a.w + static_cast<size_t>(u) * a.cap + t;
-  const float old = a.decay == 0.f ? 0.f : a.decay * *w;
-  const int blk = block_at(c, b, t / c.bs);
-  if (blk < 0) {
-    atomicOr(c.status, KVC_STATUS_BAD_INDEX);
-    *w = old;
-    return;
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (static_cast<int>(threadIdx.x) < groups) {  // its place: by the count, then by the number
+    const int mine = s_upto[threadIdx.x];
+    int at = per > 1 ? threadIdx.x : 0;
+    if (per == 1)
+      for (int g = 0; g < groups; ++g) {
+        const int other = s_upto[g];
+        at += other > mine || (other == mine && g < static_cast<int>(threadIdx.x));
+      }
+    s_count[at] = mine;
+    s_seq[at] = static_cast<uint8_t>(threadIdx.x);
   }
-  float k[D];
-  const uint32_t* codes =
-      reinterpret_cast<const uint32_t*>(c.pool[0] + (block_row(c, l, blk, h) + t % c.bs) * D);
+  if (threadIdx.x == 0) s_count[groups] = 0;
+  __syncthreads();
+  // s_upto[q]: items of a unit among those of the levels (the x-th pairs from the end of all
+  // sequences that have them) that more than q sequences do not reach; or, of groups of several
+  // sequences, of groups 0 .. q
+  if (warp == kItemWarp) {
+    int before = 0;
+    for (int q0 = 0; q0 < groups; q0 += 32) {
+      const int q = q0 + lane;
+      int incl = q < groups ? s_count[q] : 0;
 #pragma unroll
-  for (int i = 0; i < D / 4; ++i) {
-    float x[4];
-    decode4<FMT>(codes[i], x);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) k[4 * i + j] = x[j];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      incl += before;
+      if (q < groups) s_upto[q] = per > 1 ? incl : incl - (q + 1) * s_count[q + 1];
+      before = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    __syncwarp();
   }
-  const float f = a.scale_log2 * c.scale[0][scale_at(c, l, blk, h)];
-  const int sb = a.first ? 0 : b, S = a.first ? 1 : c.B;
-  float sum = 0.f;
-  for (int g = 0; g < a.G; ++g) {
-    const float* lse = a.lse + ((static_cast<size_t>(l) * S + sb) * c.H * a.G + h * a.G + g) * a.n + first;
-    for (int j = max(0, t - (len - nq)); j < nq; ++j) {
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q.at(l, sb, h * a.G + g, first + j));
-      float z = 0.f;
+
+  auto read_item = [&](int i, Item& it) {
+    if (!warp_wait(&i_full[i % kItems], (i / kItems) & 1, abort, c.status)) return false;
+    it = items[i % kItems];
+    return it.there != 0;
+  };
+  auto leave_item = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&i_empty[i % kItems]);
+  };
+
+  if (warp < kWeightWarps) {
+    // ------------------------------------------------------------ weights
+    // Warp 4 (2 h + t) + q: tile t, columns 128 h .. 128 h + 127, lane quarter q.
+    const int t = warp / 4 % 2, half = warp / 8, quarter = warp % 4;
+    const int row = quarter * 32 + lane;
+    const uint32_t s_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + t * 256 + half * 128;
+    int step = 0;     // products of this tile
+    uint32_t use = 0;  // chunks
+    Item it;
+    for (int i = 0; read_item(i, it); ++i) {
+      leave_item(i);
+      if (!warp_wait(&k_full[t], i & 1, abort, c.status)) break;  // (the factors come with the keys)
+      const float f = s_factors[((i & 1) * 2 + t) * kTile + row];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_empty[t]);  // (no more than one item ahead of these warps)
+      const int token = it.t0 + t * kTile + row;
+      const int jmin = token - (it.len - it.nq);   // the first query that sees this token
+      const int first_c = t ? it.c1 : it.c0;
+      const float2 ff = make_float2(f, f);
+      float2 sum = make_float2(0.f, 0.f);
+      bool ok = true;
+      for (int s = 0; ok && s < p.subs; ++s)
+        for (int ch = it.c0; ch < it.chunks; ++ch, ++use) {
+          const int st = use % kSums;
+          // (also for a chunk that the tile does not see: this warp's arrival counts for its use)
+          if (!(ok = warp_wait(&y_full[st], (use / kSums) & 1, abort, c.status))) break;
+          if (ch >= first_c) {
+            if (!(ok = warp_wait(&s_full[t], step & 1, abort, c.status))) break;
+            ++step;
+            tc_fence_after();
+            const float* y = s_sums + st * kChunk + half * 128;
+            const int j0 = ch * p.tok;
+            // columns of this half that count: [lo, hi)
+            const int lo = max(jmin - j0, 0) * p.P - half * 128;
+            const int hi = min(it.nq - j0, p.tok) * p.P - half * 128;
+            const bool whole = __all_sync(0xffffffffu, lo <= 0) && hi >= 128 - (kChunk - p.tok * p.P) * half;
+            uint32_t v[32];
+            auto add = [&](int col, auto masked) {
 #pragma unroll
-      for (int i = 0; i < D / 2; ++i) z += bf16_lo(q[i]) * k[2 * i] + bf16_hi(q[i]) * k[2 * i + 1];
-      const float y = lse[j] == -INFINITY ? INFINITY : lse[j] * 1.4426950408889634f;
-      sum += exp2f(z * f - y);
+              for (int k = 0; k < 32; k += 4) {
+                const float4 yy = *reinterpret_cast<const float4*>(y + col + k);
+                float2 e0 = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), ff,
+                                 make_float2(yy.x, yy.y));
+                float2 e1 = fma2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), ff,
+                                 make_float2(yy.z, yy.w));
+                e0.x = ex2(e0.x);
+                e0.y = ex2(e0.y);
+                e1.x = ex2(e1.x);
+                e1.y = ex2(e1.y);
+                if constexpr (decltype(masked)::value) {
+                  e0.x = col + k >= lo && col + k < hi ? e0.x : 0.f;
+                  e0.y = col + k + 1 >= lo && col + k + 1 < hi ? e0.y : 0.f;
+                  e1.x = col + k + 2 >= lo && col + k + 2 < hi ? e1.x : 0.f;
+                  e1.y = col + k + 3 >= lo && col + k + 3 < hi ? e1.y : 0.f;
+                }
+                sum = add2(sum, add2(e0, e1));
+              }
+            };
+            auto release = [&]() {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&s_empty[t]);
+            };
+            if (whole) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                tmem_ld32(s_tmem + 32 * k, v);
+                tmem_ld_wait();
+                if (k == 3) release();
+                add(32 * k, Bool<false>{});
+              }
+            } else {
+#pragma unroll 1
+              for (int k = 0; k < 4; ++k) {
+                if (hi <= 32 * k || !__any_sync(0xffffffffu, lo < 32 * k + 32)) continue;
+                tmem_ld32(s_tmem + 32 * k, v);
+                tmem_ld_wait();
+                add(32 * k, Bool<true>{});
+              }
+              release();
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&y_empty[st]);
+        }
+      if (!ok) break;
+      // the second half's sums to the first half's warps, which write the token
+      const float mine = sum.x + sum.y;
+      if (half) {
+        if (!warp_wait(&part_empty[t], (i & 1) ^ 1, abort, c.status)) break;
+        s_parts[t * kTile + row] = mine;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&part_full[t]);
+      } else {
+        float* w = a.w + (static_cast<size_t>(it.l * c.B + it.b) * c.H + it.h) * a.cap + token;
+        const bool there = token < it.len;
+        const float old = there && a.decay != 0.f ? a.decay * *w : 0.f;
+        if (!warp_wait(&part_full[t], i & 1, abort, c.status)) break;
+        const float all = mine + s_parts[t * kTile + row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&part_empty[t]);
+        if (there) *w = f < 0.f ? old : old + all;  // (an absent token)
+      }
+    }
+  } else if (warp < kQueryWarp) {
+    // ------------------------------------------------------------ keys
+    // This lane: rows (tokens) row_in + 32 k of a tile, 16-byte chunks q4 + 4 x of them; and
+    // it looks up token 32 kw + lane, which the four warps exchange through the factors.
+    const int kw = warp - kKeyWarp, q4 = lane % 4, row_in = kw * 8 + lane / 4;
+    Item it;
+    for (int i = 0; read_item(i, it); ++i) {
+      leave_item(i);
+      bool ok = true;
+      const int32_t* table = c.table + static_cast<size_t>(it.b) * c.max_blocks;
+      const uint8_t* pool = c.pool[0] + block_row(c, it.l, 0, it.h) * D;
+      const float* scale = c.scale[0] + scale_at(c, it.l, 0, it.h);
+      int rows[2][4];
+      float f[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int t0 = it.t0 + t * kTile;
+        auto row_of = [&](int token) {  // of the pool, -1: none
+          if (token >= it.len) return -1;
+          const int n = by_bs.div(token), blk = table[n];
+          return static_cast<uint32_t>(blk) < static_cast<uint32_t>(c.n_blocks)
+                     ? blk * c.H * by_bs.bs + (token - n * by_bs.bs)
+                     : -1;
+        };
+#pragma unroll
+        for (int k = 0; k < 4; ++k) rows[t][k] = row_of(t0 + row_in + 32 * k);
+        const int own = t0 + kw * 32 + lane;
+        f[t] = -1.f;  // absent
+        if (own < it.len) {
+          const int blk = table[by_bs.div(own)];
+          if (static_cast<uint32_t>(blk) < static_cast<uint32_t>(c.n_blocks))
+            f[t] = finite_factor(a.scale_log2, scale[static_cast<size_t>(blk) * c.H]);
+          else
+            bad = true;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok) continue;
+        uint4 codes[4][DB];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = rows[t][k];
+#pragma unroll
+          for (int x = 0; x < DB; ++x)
+            codes[k][x] = r >= 0 ? *reinterpret_cast<const uint4*>(pool + static_cast<size_t>(r) * D +
+                                                                   (q4 + 4 * x) * 16)
+                                 : make_uint4(0, 0, 0, 0);
+        }
+        // (the last item's products with this tile are done)
+        if (!(ok = warp_wait(&k_empty[t], (i & 1) ^ 1, abort, c.status))) continue;
+        s_factors[((i & 1) * 2 + t) * kTile + kw * 32 + lane] = f[t];
+        uint8_t* tile = smem + Sm::kKeys + t * Sm::kKeyTile + row_in * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int x = 0; x < DB; ++x) {
+            // 16 codes: values 16 (q4 + 4 x) .. + 15, the 16-byte places 2 q4, 2 q4 + 1 of block x
+            const uint2 b0 = bf16_of<FMT>(codes[k][x].x), b1 = bf16_of<FMT>(codes[k][x].y),
+                        b2 = bf16_of<FMT>(codes[k][x].z), b3 = bf16_of<FMT>(codes[k][x].w);
+            uint8_t* at = tile + x * kKeyBlock + k * 32 * 128;
+            *reinterpret_cast<uint4*>(at + (((2 * q4) ^ (row_in % 8)) << 4)) = make_uint4(b0.x, b0.y, b1.x, b1.y);
+            *reinterpret_cast<uint4*>(at + (((2 * q4 + 1) ^ (row_in % 8)) << 4)) = make_uint4(b2.x, b2.y, b3.x, b3.y);
+          }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[t]);
+      }
+      if (!ok) break;
+    }
+    if (bad) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
+  } else if (warp == kQueryWarp) {
+    // ------------------------------------------------------------ queries
+    uint32_t use = 0;
+    bool ok = true;
+    Item it;
+    for (int i = 0; ok && read_item(i, it); ++i) {
+      leave_item(i);
+      for (int s = 0; ok && s < p.subs; ++s)
+        for (int ch = it.c0; ch < it.chunks; ++ch) {
+          const int st = use % NS;
+          if (!(ok = warp_wait(&q_empty[st], ((use / NS) & 1) ^ 1, abort, c.status))) break;
+          ++use;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&q_full[st], DB * p.P * p.tok * 128);
+            for (int x = 0; x < DB; ++x)
+              tma_load_5d(smem + Sm::kRing + st * Sm::kStage + x * kQueryBlock, &map_q, 64 * x,
+                          (it.h * a.G + s * p.P) * p.q_head, it.first + ch * p.tok,
+                          a.first ? 0 : it.b * p.q_seq, it.l * p.q_layer, &q_full[st]);
+          }
+          __syncwarp();
+        }
+    }
+    volatile int never = 0;  // every copy has landed before the CTA ends
+    for (uint32_t u = use > NS ? use - NS : 0; u < use; ++u)
+      mbar_wait(&q_full[u % NS], (u / NS) & 1, &never, c.status);
+  } else if (warp == kSumWarp) {
+    // ------------------------------------------------------------ normalisers
+    uint32_t use = 0;
+    bool ok = true;
+    Item it;
+    for (int i = 0; ok && read_item(i, it); ++i) {
+      leave_item(i);
+      const int sb = a.first ? 0 : it.b, S = a.first ? 1 : c.B;
+      for (int s = 0; ok && s < p.subs; ++s) {
+        const float* lse = a.lse + ((static_cast<size_t>(it.l) * S + sb) * c.H * a.G + it.h * a.G + s * p.P) * a.n +
+                           it.first;
+        for (int ch = it.c0; ch < it.chunks; ++ch) {
+          float y[kChunk / 32];
+#pragma unroll
+          for (int k = 0; k < kChunk / 32; ++k) {
+            const int col = lane + 32 * k, j = ch * p.tok + col / p.P;
+            const bool there = col < p.tok * p.P && j < it.nq;
+            y[k] = there ? -lse_base2(lse[static_cast<size_t>(col % p.P) * a.n + j]) : -INFINITY;
+          }
+          const int st = use % kSums;
+          if (!(ok = warp_wait(&y_empty[st], ((use / kSums) & 1) ^ 1, abort, c.status))) break;
+          ++use;
+#pragma unroll
+          for (int k = 0; k < kChunk / 32; ++k) s_sums[st * kChunk + lane + 32 * k] = y[k];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&y_full[st]);
+        }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ products
+    // (all lanes run the loop and wait converged; lane 0 issues)
+    const uint32_t base = smem_u32(smem);
+    uint32_t use = 0;
+    int steps[2] = {0, 0};
+    bool ok = true;
+    Item it;
+    for (int i = 0; ok && read_item(i, it); ++i) {
+      leave_item(i);
+      const int per_sub = it.chunks - it.c0;
+      for (int s = 0; ok && s < p.subs; ++s)
+        for (int ch = it.c0; ok && ch < it.chunks; ++ch, ++use) {
+          const int st = use % NS;
+          if (!(ok = warp_wait(&q_full[st], (use / NS) & 1, abort, c.status))) break;
+          const bool begins = s == 0 && ch == it.c0, ends = s + 1 == p.subs && ch + 1 == it.chunks;
+          const int n = (min(it.nq - ch * p.tok, p.tok) * p.P + 15) & ~15;  // columns
+          const uint32_t idesc = idesc_bf16_f32(kTile, n);
+          const uint32_t q_tile = base + Sm::kRing + st * Sm::kStage;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok) continue;
+            if (begins && !(ok = warp_wait(&k_full[t], i & 1, abort, c.status))) continue;
+            const bool sees = t == 0 || ch >= it.c1;
+            if (sees) {
+              if (!(ok = warp_wait(&s_empty[t], (steps[t] & 1) ^ 1, abort, c.status))) continue;
+              ++steps[t];
+              tc_fence_after();
+              if (lane == 0) {
+                const uint32_t k_tile = base + Sm::kKeys + t * Sm::kKeyTile;
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+                  mma_bf16(tmem + t * 256, sw128_desc(k_tile + (x / 4) * kKeyBlock + (x % 4) * 32),
+                           sw128_desc(q_tile + (x / 4) * kQueryBlock + (x % 4) * 32), idesc, x > 0);
+                mma_commit(&s_full[t]);
+              }
+              __syncwarp();
+            }
+            if (ends && lane == 0) mma_commit(&k_empty[t]);
+            __syncwarp();
+          }
+          if (ok && lane == 0) mma_commit(&q_empty[st]);
+          __syncwarp();
+        }
+      if (ok && per_sub <= 0) {  // no queries: the keys are done with at once
+        for (int t = 0; t < 2; ++t) {
+          if (!(ok = warp_wait(&k_full[t], i & 1, abort, c.status))) break;
+          if (lane == 0) mbar_arrive(&k_empty[t]);
+        }
+      }
+    }
+    if (lane == 0) mma_commit(done);
+    __syncwarp();
+    volatile int never = 0;  // also after an abort: what was issued ends
+    mbar_wait(done, 0, &never, c.status);
+  } else {
+    // ------------------------------------------------------------ items
+    const int total = s_upto[groups - 1] * units;  // below 2^31: checked on the host
+    for (int i = 0;; ++i) {
+      if (!warp_wait(&i_empty[i % kItems], ((i / kItems) & 1) ^ 1, abort, c.status)) break;
+      // rounds go back and forth over the CTAs
+      const long long k = static_cast<long long>(i) * gridDim.x +
+                          (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      Item it = {};
+      if (k < total) {
+        const int at = static_cast<int>(k / units), unit = static_cast<int>(k % units);
+        int q = 0;  // the first place with s_upto[q] > at
+        for (int q0 = 0; q0 < groups; q0 += 32) {
+          const bool below = q0 + lane < groups && s_upto[q0 + lane] <= at;
+          const int n = __popc(__ballot_sync(0xffffffffu, below));
+          q += n;
+          if (n < 32) break;
+        }
+        const int in = at - (q ? s_upto[q - 1] : 0);
+        int x;  // pairs behind this one
+        if (per == 1) {
+          x = s_count[q] - 1 - in / (q + 1);
+          it.b = s_seq[in % (q + 1)];
+        } else {
+          it.b = s_seq[q] * per;
+          x = in;
+          for (int n = pairs_of(it.b); x >= n; n = pairs_of(++it.b)) x -= n;
+        }
+        const Lengths n = lengths_of(c, a, it.b, &bad);
+        it.len = n.len;
+        it.nq = n.nq;
+        it.first = n.first;
+        it.l = unit / c.H;
+        it.h = unit % c.H;
+        it.t0 = (div_up(n.len, 2 * kTile) - 1 - x) * 2 * kTile;
+        it.chunks = div_up(n.nq, p.tok);
+        const int start = n.len - n.nq;  // the first query's token
+        it.c0 = min(max(it.t0 - start, 0) / p.tok, it.chunks);
+        it.c1 = it.t0 + kTile < n.len ? min(max(it.t0 + kTile - start, 0) / p.tok, it.chunks) : it.chunks;
+        it.there = 1;
+      }
+      if (lane == 0) {
+        items[i % kItems] = it;
+        mbar_arrive(&i_full[i % kItems]);
+      }
+      __syncwarp();
+      if (!it.there) break;
     }
   }
-  *w = old + sum;
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+#endif
+}
+
+template <int D, int FMT>
+cudaError_t launch_d(const Cache& c, const WeighArgs& a, cudaStream_t s) {
+  static std::atomic<uint64_t> told{0};
+  cudaError_t e = allow_smem(weigh_many_kernel<D, FMT>, Smem<D>::kBytes, told);
+  if (e != cudaSuccess) return e;
+  Params p;
+  p.a = a;
+  p.P = a.G;
+  if (a.G > kPacked)
+    for (p.P = kPacked; a.G % p.P; --p.P) {
+    }
+  p.subs = a.G / p.P;
+  p.tok = kChunk / p.P;
+  // x = 64 values, y = head, z = token, then sequence and layer, in boxes of one block of values
+  // by P heads by tok tokens.  An axis whose stride is 0 counts as one.
+  EncodeTiledFn enc = tensor_map_encoder(nullptr);
+  if (!enc) return cudaErrorNotSupported;
+  const int seqs = a.first ? 1 : c.B, heads = c.H * a.G;
+  p.q_head = heads > 1;
+  p.q_seq = seqs > 1 && a.q.seq > 0;
+  p.q_layer = c.L > 1 && a.q.layer > 0;
+  auto bytes = [](long long stride, bool used) { return static_cast<cuuint64_t>(used ? stride * 2 : 256); };
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(a.n), static_cast<cuuint64_t>(p.q_seq ? seqs : 1),
+                              static_cast<cuuint64_t>(p.q_layer ? c.L : 1)};
+  const cuuint64_t strides[4] = {bytes(a.q.head, p.q_head), bytes(a.q.token, a.n > 1),
+                                 bytes(a.q.seq, p.q_seq), bytes(a.q.layer, p.q_layer)};
+  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(p.P), static_cast<cuuint32_t>(p.tok), 1, 1};
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  CUtensorMap q;
+  if (enc(&q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, a.q.data, dims, strides, box, one,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const long long tokens = min(a.cap, c.max_blocks * c.bs);
+  const long long most = static_cast<long long>(c.L) * c.B * c.H * ((tokens + 2 * kTile - 1) / (2 * kTile));
+  const int grid = static_cast<int>(most < a.num_sms ? most : a.num_sms);
+  return launch(weigh_many_kernel<D, FMT>, grid, kThreads, Smem<D>::kBytes, s, q, c, p, make_div(c.bs));
 }
 
 }  // namespace
 
 cudaError_t launch_weigh_many(const Cache& c, int format, const WeighArgs& a, cudaStream_t s) {
-  const int grid = c.L * c.B * c.H * ((a.cap + kThreads - 1) / kThreads);
-  auto* kernel = c.d == 64 ? (format == KVC_CACHE8_E4M3 ? weigh_many_kernel<64, KVC_CACHE8_E4M3>
-                                                        : weigh_many_kernel<64, KVC_CACHE8_INT8>)
-                           : (format == KVC_CACHE8_E4M3 ? weigh_many_kernel<128, KVC_CACHE8_E4M3>
-                                                        : weigh_many_kernel<128, KVC_CACHE8_INT8>);
-  return launch(kernel, grid, kThreads, 0, s, c, a);
+  if (c.d == 64)
+    return format == KVC_CACHE8_E4M3 ? launch_d<64, KVC_CACHE8_E4M3>(c, a, s)
+                                     : launch_d<64, KVC_CACHE8_INT8>(c, a, s);
+  return format == KVC_CACHE8_E4M3 ? launch_d<128, KVC_CACHE8_E4M3>(c, a, s)
+                                   : launch_d<128, KVC_CACHE8_INT8>(c, a, s);
 }
 
 }  // namespace prompt

@@ -512,6 +512,7 @@ int kvc_cache8_attend(kvc_handle* h, const kvc_cache8* c, const kvc_rows* q, int
  *   first    NULL: [n_layers][B][H*G][n][d].  [B] int32: packed, the queries of sequence b
  *            are rows first[b] .. first[b] + n_q[b] - 1 of [n_layers][H*G][n][d] (the
  *            strides' seq is not used)
+ *            Strides of tokens and heads must not be 0, all below 2^39 values
  *   n_q      [B] int32, 0 .. seq_len[b], or NULL (not packed): n
  *   lse      fp32, contiguous, [n_layers][B][H*G][n], packed [n_layers][H*G][n]; a query
  *            whose lse is -inf or +inf sees no token
