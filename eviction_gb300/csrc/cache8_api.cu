@@ -169,7 +169,8 @@ int kvc_cache8_weigh(kvc_handle* h, const kvc_cache8* c, const kvc_rows* q, int 
     if (units > INT_MAX / (cap / 32 + 8ll))
       return fail(h, KVC_ERR_UNSUPPORTED, "n_layers * batch * n_kv_heads * (cap / 32 + 8) must be < 2^31");
     kvc::prompt::WeighArgs a{rows(*q), first, n_q, lse, weights, n, h->dims.G, cap,
-                             kvc::scale_log2_of(h->cfg), decay, h->num_sms};
+                             kvc::scale_log2_of(h->cfg), decay, h->num_sms,
+                             h->ws.weigh};
     return run(h, kvc::kKernelCache8Weigh, "cache8 weigh", stream, [&](cudaStream_t s) {
       return kvc::prompt::launch_weigh(view(h, *c), c->format, a, s);
     });

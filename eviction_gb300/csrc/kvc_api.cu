@@ -8,6 +8,7 @@
 #include <new>
 
 #include "api_util.cuh"
+#include "prompt.cuh"
 
 namespace kvc {
 size_t attention_usage_smem_bytes(int d, int R);
@@ -365,6 +366,7 @@ int kvc_create(const kvc_config* cfg, kvc_handle** out) {
   const size_t o_ns = take(U * 4);
   const size_t o_st = take(256);
   const size_t o_at = take(kvc::cache8_attend_workspace(d.d));
+  const size_t o_we = take(kvc::prompt::weigh_workspace(h->num_sms));
   void* base = nullptr;
   if (cudaMalloc(&base, off) != cudaSuccess) {
     cudaGetLastError();
@@ -393,6 +395,7 @@ int kvc_create(const kvc_config* cfg, kvc_handle** out) {
   w.n_seg = reinterpret_cast<int32_t*>(p + o_ns);
   w.status = reinterpret_cast<uint32_t*>(p + o_st);
   w.attend = p + o_at;
+  w.weigh = p + o_we;
   if (!create_host_io(h->io)) {
     cudaFree(base);
     delete h;

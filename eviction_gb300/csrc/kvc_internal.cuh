@@ -31,6 +31,7 @@ struct Workspace {
   uint32_t* status = nullptr;   // device status bits; status[1] = the error word of
                                 // the running paged compaction or cache fork
   void* attend = nullptr;       // kvc_cache8_attend: partial results of split sequences
+  void* weigh = nullptr;        // kvc_cache8_weigh: parts of the sums over many queries
   void* base = nullptr;         // single allocation
   size_t bytes = 0;
 };

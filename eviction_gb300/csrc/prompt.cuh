@@ -43,7 +43,10 @@ struct WeighArgs {
   int n, G, cap;
   float scale_log2, decay;
   int num_sms;
+  void* workspace;  // weigh_workspace() bytes
 };
+// (cut items are fewer than two a SM, their parts fewer than four, of 256 tokens each)
+constexpr size_t weigh_workspace(int num_sms) { return static_cast<size_t>(num_sms) * 4 * 256 * sizeof(float); }
 cudaError_t launch_weigh(const cache8::Cache& c, int format, const WeighArgs& a, cudaStream_t s);
 
 struct HeaviestArgs {

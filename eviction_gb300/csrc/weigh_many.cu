@@ -53,6 +53,9 @@ struct Bool {
 struct Params {
   WeighArgs a;
   int P, subs, tok;   // heads in a chunk, such parts of a group, tokens of a chunk
+  int parts;          // of an item's queries
+  int pairs;          // of tiles that a sequence may have
+  float* part;        // [units * B][pairs][parts][2 kTile] sums, where parts > 1; -1: absent
   int q_head, q_seq, q_layer;  // 0 where the axis' stride is 0
 };
 
@@ -64,7 +67,7 @@ struct Item {
   int c0;             // first chunk that tile 0 sees
   int c1;             // first chunk that tile 1 sees
   int there;          // 0: no more items
-  int pad;
+  int part;
 };
 
 template <int D>
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- the list of items: groups of `per` sequences (one each, if they are few enough; those
   // with most pairs of tiles first then) ----
-  const int units = c.L * c.H;
+  const int units = c.L * c.H * p.parts;  // items of a pair of tiles, over layers and heads
   const int per = div_up(c.B, kSorted), groups = div_up(c.B, per);
   bool bad = false;
   auto pairs_of = [&](int b) { return div_up(lengths_of(c, a, b, &bad).len, 2 * kTile); };
@@ -314,12 +317,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         float* w = a.w + (static_cast<size_t>(it.l * c.B + it.b) * c.H + it.h) * a.cap + token;
         const bool there = token < it.len;
-        const float old = there && a.decay != 0.f ? a.decay * *w : 0.f;
+        const float old = there && a.decay != 0.f && p.parts == 1 ? a.decay * *w : 0.f;
         if (!warp_wait(&part_full[t], i & 1, abort, c.status)) break;
         const float all = mine + s_parts[t * kTile + row];
         __syncwarp();
         if (lane == 0) mbar_arrive(&part_empty[t]);
-        if (there) *w = f < 0.f ? old : old + all;  // (an absent token)
+        if (there && p.parts == 1) *w = f < 0.f ? old : old + all;  // (an absent token)
+        if (there && p.parts > 1)
+          p.part[((((static_cast<size_t>(it.l) * c.B + it.b) * c.H + it.h) * p.pairs + it.t0 / (2 * kTile)) *
+                      p.parts + it.part) * (2 * kTile) + t * kTile + row] = f < 0.f ? -1.f : all;
       }
     }
   } else if (warp < kQueryWarp) {
@@ -420,6 +426,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&q_full[u % NS], (u / NS) & 1, &never, c.status);
   } else if (warp == kSumWarp) {
     // ------------------------------------------------------------ normalisers
+    // This lane's columns lane + 32 k: head g and token j of the chunk.
+    int j[kChunk / 32], g[kChunk / 32];
+#pragma unroll
+    for (int k = 0; k < kChunk / 32; ++k) {
+      const int col = lane + 32 * k;
+      j[k] = col < p.tok * p.P ? col / p.P : INT_MAX / 2;
+      g[k] = col % p.P;
+    }
     uint32_t use = 0;
     bool ok = true;
     Item it;
@@ -431,17 +445,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                            it.first;
         for (int ch = it.c0; ch < it.chunks; ++ch) {
           float y[kChunk / 32];
+          const int j0 = ch * p.tok;
 #pragma unroll
-          for (int k = 0; k < kChunk / 32; ++k) {
-            const int col = lane + 32 * k, j = ch * p.tok + col / p.P;
-            const bool there = col < p.tok * p.P && j < it.nq;
-            y[k] = there ? -lse_base2(lse[static_cast<size_t>(col % p.P) * a.n + j]) : -INFINITY;
-          }
+          for (int k = 0; k < kChunk / 32; ++k)
+            y[k] = j[k] < it.nq - j0 ? lse[static_cast<size_t>(g[k]) * a.n + j0 + j[k]] : INFINITY;
           const int st = use % kSums;
           if (!(ok = warp_wait(&y_empty[st], ((use / kSums) & 1) ^ 1, abort, c.status))) break;
           ++use;
 #pragma unroll
-          for (int k = 0; k < kChunk / 32; ++k) s_sums[st * kChunk + lane + 32 * k] = y[k];
+          for (int k = 0; k < kChunk / 32; ++k) s_sums[st * kChunk + lane + 32 * k] = -lse_base2(y[k]);
           __syncwarp();
           if (lane == 0) mbar_arrive(&y_full[st]);
         }
@@ -534,13 +546,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.len = n.len;
         it.nq = n.nq;
         it.first = n.first;
-        it.l = unit / c.H;
-        it.h = unit % c.H;
+        it.part = unit % p.parts;
+        it.l = unit / p.parts / c.H;
+        it.h = unit / p.parts % c.H;
         it.t0 = (div_up(n.len, 2 * kTile) - 1 - x) * 2 * kTile;
         it.chunks = div_up(n.nq, p.tok);
         const int start = n.len - n.nq;  // the first query's token
         it.c0 = min(max(it.t0 - start, 0) / p.tok, it.chunks);
         it.c1 = it.t0 + kTile < n.len ? min(max(it.t0 + kTile - start, 0) / p.tok, it.chunks) : it.chunks;
+        if (p.parts > 1) {  // this part's share of the chunks
+          const int n_ch = it.chunks - it.c0, lo = it.c0;
+          it.c0 = lo + n_ch * it.part / p.parts;
+          it.chunks = lo + n_ch * (it.part + 1) / p.parts;
+        }
         it.there = 1;
       }
       if (lane == 0) {
@@ -558,6 +576,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 #endif
 }
+
+// Adds the parts of items up, in their order.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) weigh_join_kernel(Cache c, Params p) {
+  before_all();
+  const WeighArgs& a = p.a;
+  const int pair = blockIdx.x % p.pairs, u = blockIdx.x / p.pairs;
+  const int b = u / c.H % c.B, token = pair * 2 * kTile + threadIdx.x;
+  bool bad = false;
+  if (token >= lengths_of(c, a, b, &bad).len) return;
+  const float* part = p.part + static_cast<size_t>(blockIdx.x) * p.parts * (2 * kTile) + threadIdx.x;
+  float* w = a.w + static_cast<size_t>(u) * a.cap + token;
+  const float old = a.decay != 0.f ? a.decay * *w : 0.f;
+  float sum = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.parts; ++s) sum += part[s * 2 * kTile];
+  *w = sum < 0.f ? old : old + sum;
+}
+static_assert(kJoinThreads == 2 * kTile, "a thread for each token of a pair of tiles");
 
 template <int D, int FMT>
 cudaError_t launch_d(const Cache& c, const WeighArgs& a, cudaStream_t s) {
@@ -593,10 +630,21 @@ cudaError_t launch_d(const Cache& c, const WeighArgs& a, cudaStream_t s) {
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  const long long tokens = min(a.cap, c.max_blocks * c.bs);
-  const long long most = static_cast<long long>(c.L) * c.B * c.H * ((tokens + 2 * kTile - 1) / (2 * kTile));
-  const int grid = static_cast<int>(most < a.num_sms ? most : a.num_sms);
-  return launch(weigh_many_kernel<D, FMT>, grid, kThreads, Smem<D>::kBytes, s, q, c, p, make_div(c.bs));
+  // Pairs of tiles that fill the GPU less than twice have their queries cut into parts, which a
+  // second launch adds up.  8 sequences of 1536 tokens, all queries (192 pairs): XX us uncut.
+  const int tokens = min(a.cap, c.max_blocks * c.bs);
+  p.pairs = (tokens + 2 * kTile - 1) / (2 * kTile);
+  const long long most = static_cast<long long>(c.L) * c.B * c.H * p.pairs;
+  const int chunks = (a.n + p.tok - 1) / p.tok;
+  p.parts = 1;
+  if (most < 2ll * a.num_sms)
+    p.parts = static_cast<int>(min(2ll * a.num_sms / most + 1, min(static_cast<long long>(chunks), 16ll)));
+  p.part = static_cast<float*>(a.workspace);
+  const long long items = most * p.parts;
+  const int grid = static_cast<int>(items < a.num_sms ? items : a.num_sms);
+  e = launch(weigh_many_kernel<D, FMT>, grid, kThreads, Smem<D>::kBytes, s, q, c, p, make_div(c.bs));
+  if (e != cudaSuccess || p.parts == 1) return e;
+  return launch(weigh_join_kernel, static_cast<int>(most), kJoinThreads, 0, s, c, p);
 }
 
 }  // namespace
