@@ -60,5 +60,48 @@ struct HeaviestArgs {
 };
 cudaError_t launch_heaviest(const HeaviestArgs& a, cudaStream_t s);
 
+#if defined(__CUDACC__)
+
+// Products issued by the lanes for which `issue` holds, one of a converged warp: without a
+// branch around them their operands stay in uniform registers.  (A branch on the lane,
+// with 64-bit descriptors made for each product, took 110 cycles a product to issue;
+// 128 x 128 x 16 take 64 to compute.)  Descriptors: the low word, the high one is the same for all.
+constexpr uint32_t kDescHigh = 1024 >> 4 | 1u << 14 | 2u << 29;  // as in sw128_desc
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t block) {
+  return (addr & 0x3FFFFu) >> 4 | (block >> 4) << 16;
+}
+__device__ __forceinline__ void mma_ss_if(bool issue, uint32_t d_tmem, uint32_t a_low, uint32_t b_low,
+                                          uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(static_cast<int>(accumulate)),
+      "r"(static_cast<int>(issue)), "r"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(bool issue, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low,
+                                          uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 b, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(static_cast<int>(accumulate)),
+      "r"(static_cast<int>(issue)), "r"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(bool issue, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(static_cast<int>(issue))
+      : "memory");
+}
+
+#endif  // __CUDACC__
+
 }  // namespace prompt
 }  // namespace kvc

@@ -8,14 +8,16 @@
 // Keys are codes as bf16, which holds both formats exactly, and queries are what they are in
 // memory: nothing is rounded before the product.
 //
-// A CTA has two tiles of 128 tokens and takes 256 query rows at a time for both:
-//   keys (4 warps)    codes of the item's tokens from their blocks to bf16 tiles in shared
-//                     memory, with the 128-byte swizzle; the next item's are loaded while
-//                     this one is computed;
-//   queries (1 warp)  TMA, through a ring of stages.  A group's heads lie side by side (row =
-//                     token * P + head), so that each chunk is of few tokens;
-//   sums (1 warp)     the rows' normalisers, gathered into shared memory beside their chunk;
-//   MMA (1 warp)      128 x 256 products into the tile's 256 columns of TMEM;
+// A CTA has two tiles of 128 tokens and takes 192 query rows at a time for both:
+//   keys (4 warps)    codes of the item's tokens from their blocks to bf16 rows in TMEM, a
+//                     thread a token; the next item's are loaded while this one is computed;
+//   queries (1 warp)  TMA, through a ring of stages, and the rows' normalisers beside them.  A
+//                     group's heads lie side by side (row = token * P + head), so that each
+//                     chunk is of few tokens;
+//   MMA (1 warp)      128 x 192 products into the tile's columns of TMEM, with the keys read
+//                     from there: from shared memory, keys, queries, copies and normalisers
+//                     together asked for more than its bandwidth (98 us with 128 columns a
+//                     product, 84 us with 256, of what is XX us below);
 //   weights (16 warps)  two warps a lane quarter and tile, a half of the columns each: scale,
 //                     exponential, sum.  One tile's exponentials run while the other's
 //                     products do.
@@ -35,13 +37,16 @@ namespace {
 
 using namespace cache8;
 
-constexpr int kTile = 128, kChunk = 256;  // tokens of a tile, query rows of a chunk
-constexpr int kWeightWarps = 16, kKeyWarp = 16, kQueryWarp = 20, kSumWarp = 21, kMmaWarp = 22,
-              kItemWarp = 23;
-constexpr int kThreads = 32 * 24;
+constexpr int kTile = 128, kChunk = 192;  // tokens of a tile, query rows of a chunk
+constexpr int kHalf = kChunk / 2;         // columns of a weight warp
+constexpr uint32_t kKeyCol = 2 * kChunk;  // the keys' first TMEM column, after the products'
+constexpr int kWeightWarps = 16, kKeyWarp = 16, kQueryWarp = 20, kMmaWarp = 21, kItemWarp = 22;
+constexpr int kThreads = 32 * 23;
+// (a warp reads and writes the quarter of TMEM's lanes that its number tells)
+static_assert(kWeightWarps == 16 && kKeyWarp % 4 == 0, "groups of four warps");
 constexpr int kItems = 4;        // items told ahead
 constexpr int kSums = 4;         // chunks whose normalisers are told ahead
-constexpr int kReaders = kWeightWarps + 4 + 3;
+constexpr int kReaders = kWeightWarps + 4 + 2;
 constexpr int kSorted = 128;     // sequences (or groups of them) in the list of items
 constexpr int kPacked = 16;      // heads in a chunk at most
 
@@ -72,9 +77,8 @@ struct Item {
 
 template <int D>
 struct Smem {
-  static constexpr int kKeyTile = kTile * D * 2, kStage = kChunk * D * 2;
-  static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kKeys = 0, kRing = 2 * kKeyTile, kSumsAt = kRing + kStages * kStage,
+  static constexpr int kStage = kChunk * D * 2, kStages = D == 128 ? 4 : 8;
+  static constexpr int kRing = 0, kSumsAt = kRing + kStages * kStage,
                        kFactors = kSumsAt + kSums * kChunk * 4,   // [2][2][128] f_t, by item parity
                        kParts = kFactors + 2 * 2 * kTile * 4,     // [2][128] the second halves' sums
                        kBars = kParts + 2 * kTile * 4,
@@ -90,12 +94,28 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
 }
 
-// Four codes to four bf16 (exact).
+// Four codes to four bf16 (exact), without the conversions from fp16, which the exponentials'
+// unit does.  e4m3: sign, exponent and mantissa in their places of a bf16 are the value times
+// 2^-120 (subnormals too).  Integers: biased to 0..255 they are the last bits of 2^23 + u.
 template <int FMT>
 __device__ __forceinline__ uint2 bf16_of(uint32_t codes) {
-  float x[4];
-  decode4<FMT>(codes, x);
-  return make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
+  if constexpr (FMT == KVC_CACHE8_E4M3) {
+    uint32_t r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t x = __byte_perm(codes, 0, i ? 0x3424 : 0x1404);  // codes in the high bytes
+      const uint32_t bits = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(bits), "r"(0x7b807b80u));  // 2^120
+    }
+    return make_uint2(r[0], r[1]);
+  } else {
+    const uint32_t u = codes ^ 0x80808080u;
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + i)) - 8388736.f;
+    return make_uint2(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]));
+  }
 }
 
 template <int D, int FMT>
@@ -105,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Sm = Smem<D>;
   constexpr int DB = D / 64;
   constexpr int NS = Sm::kStages;
-  constexpr int kKeyBlock = kTile * 128, kQueryBlock = kChunk * 128;  // bytes of 64 values of all rows
+  constexpr int kQueryBlock = kChunk * 128;  // bytes of 64 values of all rows
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kBars);
@@ -153,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
     prefetch_tensormap(&map_q);
   }
-  // query rows that no copy writes (P does not divide 256) are zeros: their products count nothing
+  // query rows that no copy writes (P does not divide 192) are zeros: their products count nothing
   for (int i = threadIdx.x; i < NS * Sm::kStage / 16; i += kThreads)
     *reinterpret_cast<uint4*>(smem + Sm::kRing + i * 16) = make_uint4(0, 0, 0, 0);
   fence_async_shared();
@@ -223,10 +243,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kWeightWarps) {
     // ------------------------------------------------------------ weights
-    // Warp 4 (2 h + t) + q: tile t, columns 128 h .. 128 h + 127, lane quarter q.
+    // Warp 4 (2 h + t) + q: tile t, half h of the columns, lane quarter q.
     const int t = warp / 4 % 2, half = warp / 8, quarter = warp % 4;
     const int row = quarter * 32 + lane;
-    const uint32_t s_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + t * 256 + half * 128;
+    const uint32_t s_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + t * kChunk + half * kHalf;
     int step = 0;     // products of this tile
     uint32_t use = 0;  // chunks
     Item it;
@@ -251,14 +271,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = warp_wait(&s_full[t], step & 1, abort, c.status))) break;
             ++step;
             tc_fence_after();
-            const float* y = s_sums + st * kChunk + half * 128;
+            const float* y = s_sums + st * kChunk + half * kHalf;
             const int j0 = ch * p.tok;
             // columns of this half that count: [lo, hi)
-            const int lo = max(jmin - j0, 0) * p.P - half * 128;
-            const int hi = min(it.nq - j0, p.tok) * p.P - half * 128;
-            const bool whole = __all_sync(0xffffffffu, lo <= 0) && hi >= 128 - (kChunk - p.tok * p.P) * half;
-            uint32_t v[32];
-            auto add = [&](int col, auto masked) {
+            const int lo = max(jmin - j0, 0) * p.P - half * kHalf;
+            const int hi = min(it.nq - j0, p.tok) * p.P - half * kHalf;
+            const bool whole = __all_sync(0xffffffffu, lo <= 0) && hi >= kHalf - (kChunk - p.tok * p.P) * half;
+            uint32_t va[32], vb[32], valid = 0;
+            auto add = [&](const uint32_t (&v)[32], int col, auto masked) {
 #pragma unroll
               for (int k = 0; k < 32; k += 4) {
                 const float4 yy = *reinterpret_cast<const float4*>(y + col + k);
@@ -271,10 +291,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 e1.x = ex2(e1.x);
                 e1.y = ex2(e1.y);
                 if constexpr (decltype(masked)::value) {
-                  e0.x = col + k >= lo && col + k < hi ? e0.x : 0.f;
-                  e0.y = col + k + 1 >= lo && col + k + 1 < hi ? e0.y : 0.f;
-                  e1.x = col + k + 2 >= lo && col + k + 2 < hi ? e1.x : 0.f;
-                  e1.y = col + k + 3 >= lo && col + k + 3 < hi ? e1.y : 0.f;
+                  e0.x = valid & 1u << k ? e0.x : 0.f;
+                  e0.y = valid & 2u << k ? e0.y : 0.f;
+                  e1.x = valid & 4u << k ? e1.x : 0.f;
+                  e1.y = valid & 8u << k ? e1.y : 0.f;
                 }
                 sum = add2(sum, add2(e0, e1));
               }
@@ -285,20 +305,29 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (lane == 0) mbar_arrive(&s_empty[t]);
             };
             if (whole) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                tmem_ld32(s_tmem + 32 * k, v);
-                tmem_ld_wait();
-                if (k == 3) release();
-                add(32 * k, Bool<false>{});
-              }
+              tmem_ld32(s_tmem, va);
+              tmem_ld_wait();
+              tmem_ld32(s_tmem + 32, vb);
+              add(va, 0, Bool<false>{});
+              tmem_ld_wait();
+              tmem_ld32(s_tmem + 64, va);
+              add(vb, 32, Bool<false>{});
+              tmem_ld_wait();
+              release();
+              add(va, 64, Bool<false>{});
             } else {
 #pragma unroll 1
-              for (int k = 0; k < 4; ++k) {
-                if (hi <= 32 * k || !__any_sync(0xffffffffu, lo < 32 * k + 32)) continue;
-                tmem_ld32(s_tmem + 32 * k, v);
+              for (int k = 0; k < kHalf / 32; ++k) {
+                // this lane's columns of the block that count, a bit each
+                const int from = max(lo - 32 * k, 0), to = min(hi - 32 * k, 32);
+                valid = from < to ? (0xffffffffu >> (32 - to)) & (0xffffffffu << from) : 0u;
+                if (!__any_sync(0xffffffffu, valid)) continue;
+                tmem_ld32(s_tmem + 32 * k, va);
                 tmem_ld_wait();
-                add(32 * k, Bool<true>{});
+                if (__all_sync(0xffffffffu, valid == 0xffffffffu))
+                  add(va, 32 * k, Bool<false>{});
+                else
+                  add(va, 32 * k, Bool<true>{});
               }
               release();
             }
@@ -330,69 +359,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kQueryWarp) {
     // ------------------------------------------------------------ keys
-    // This lane: rows (tokens) row_in + 32 k of a tile, 16-byte chunks q4 + 4 x of them; and
-    // it looks up token 32 kw + lane, which the four warps exchange through the factors.
-    const int kw = warp - kKeyWarp, q4 = lane % 4, row_in = kw * 8 + lane / 4;
+    // This thread: token 32 kw + lane of each tile, a lane of TMEM.
+    const int kw = warp - kKeyWarp;
+    const uint32_t key_tmem = tmem + (static_cast<uint32_t>(kw * 32) << 16) + kKeyCol;
     Item it;
     for (int i = 0; read_item(i, it); ++i) {
       leave_item(i);
       bool ok = true;
       const int32_t* table = c.table + static_cast<size_t>(it.b) * c.max_blocks;
-      const uint8_t* pool = c.pool[0] + block_row(c, it.l, 0, it.h) * D;
-      const float* scale = c.scale[0] + scale_at(c, it.l, 0, it.h);
-      int rows[2][4];
+      int row[2];
       float f[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int t0 = it.t0 + t * kTile;
-        auto row_of = [&](int token) {  // of the pool, -1: none
-          if (token >= it.len) return -1;
-          const int n = by_bs.div(token), blk = table[n];
-          return static_cast<uint32_t>(blk) < static_cast<uint32_t>(c.n_blocks)
-                     ? blk * c.H * by_bs.bs + (token - n * by_bs.bs)
-                     : -1;
-        };
-#pragma unroll
-        for (int k = 0; k < 4; ++k) rows[t][k] = row_of(t0 + row_in + 32 * k);
-        const int own = t0 + kw * 32 + lane;
+        const int own = it.t0 + t * kTile + kw * 32 + lane;
+        row[t] = -1;
         f[t] = -1.f;  // absent
         if (own < it.len) {
-          const int blk = table[by_bs.div(own)];
-          if (static_cast<uint32_t>(blk) < static_cast<uint32_t>(c.n_blocks))
-            f[t] = finite_factor(a.scale_log2, scale[static_cast<size_t>(blk) * c.H]);
-          else
+          const int n = by_bs.div(own), blk = table[n];
+          if (static_cast<uint32_t>(blk) < static_cast<uint32_t>(c.n_blocks)) {
+            f[t] = finite_factor(a.scale_log2, c.scale[0][scale_at(c, it.l, blk, it.h)]);
+            row[t] = blk * c.H * by_bs.bs + (own - n * by_bs.bs);  // < 2^31: checked on the host
+          } else {
             bad = true;
+          }
         }
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (!ok) continue;
-        uint4 codes[4][DB];
+        uint4 codes[D / 16];
+        const uint4* from = reinterpret_cast<const uint4*>(
+            c.pool[0] + (block_row(c, it.l, 0, it.h) + max(row[t], 0)) * D);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = rows[t][k];
-#pragma unroll
-          for (int x = 0; x < DB; ++x)
-            codes[k][x] = r >= 0 ? *reinterpret_cast<const uint4*>(pool + static_cast<size_t>(r) * D +
-                                                                   (q4 + 4 * x) * 16)
-                                 : make_uint4(0, 0, 0, 0);
-        }
+        for (int x = 0; x < D / 16; ++x) codes[x] = row[t] >= 0 ? from[x] : make_uint4(0, 0, 0, 0);
         // (the last item's products with this tile are done)
         if (!(ok = warp_wait(&k_empty[t], (i & 1) ^ 1, abort, c.status))) continue;
+        tc_fence_after();
         s_factors[((i & 1) * 2 + t) * kTile + kw * 32 + lane] = f[t];
-        uint8_t* tile = smem + Sm::kKeys + t * Sm::kKeyTile + row_in * 128;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int x = 0; x < D / 32; ++x) {
+          uint32_t v[16];
 #pragma unroll
-          for (int x = 0; x < DB; ++x) {
-            // 16 codes: values 16 (q4 + 4 x) .. + 15, the 16-byte places 2 q4, 2 q4 + 1 of block x
-            const uint2 b0 = bf16_of<FMT>(codes[k][x].x), b1 = bf16_of<FMT>(codes[k][x].y),
-                        b2 = bf16_of<FMT>(codes[k][x].z), b3 = bf16_of<FMT>(codes[k][x].w);
-            uint8_t* at = tile + x * kKeyBlock + k * 32 * 128;
-            *reinterpret_cast<uint4*>(at + (((2 * q4) ^ (row_in % 8)) << 4)) = make_uint4(b0.x, b0.y, b1.x, b1.y);
-            *reinterpret_cast<uint4*>(at + (((2 * q4 + 1) ^ (row_in % 8)) << 4)) = make_uint4(b2.x, b2.y, b3.x, b3.y);
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t w[4] = {codes[2 * x + k].x, codes[2 * x + k].y, codes[2 * x + k].z, codes[2 * x + k].w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const uint2 y = bf16_of<FMT>(w[z]);
+              v[8 * k + 2 * z] = y.x;
+              v[8 * k + 2 * z + 1] = y.y;
+            }
           }
-        fence_async_shared();
+          tmem_st16(key_tmem + t * (D / 2) + 16 * x, v);
+        }
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[t]);
       }
@@ -401,32 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (bad) atomicOr(c.status, KVC_STATUS_BAD_INDEX);
   } else if (warp == kQueryWarp) {
     // ------------------------------------------------------------ queries
-    uint32_t use = 0;
-    bool ok = true;
-    Item it;
-    for (int i = 0; ok && read_item(i, it); ++i) {
-      leave_item(i);
-      for (int s = 0; ok && s < p.subs; ++s)
-        for (int ch = it.c0; ch < it.chunks; ++ch) {
-          const int st = use % NS;
-          if (!(ok = warp_wait(&q_empty[st], ((use / NS) & 1) ^ 1, abort, c.status))) break;
-          ++use;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&q_full[st], DB * p.P * p.tok * 128);
-            for (int x = 0; x < DB; ++x)
-              tma_load_5d(smem + Sm::kRing + st * Sm::kStage + x * kQueryBlock, &map_q, 64 * x,
-                          (it.h * a.G + s * p.P) * p.q_head, it.first + ch * p.tok,
-                          a.first ? 0 : it.b * p.q_seq, it.l * p.q_layer, &q_full[st]);
-          }
-          __syncwarp();
-        }
-    }
-    volatile int never = 0;  // every copy has landed before the CTA ends
-    for (uint32_t u = use > NS ? use - NS : 0; u < use; ++u)
-      mbar_wait(&q_full[u % NS], (u / NS) & 1, &never, c.status);
-  } else if (warp == kSumWarp) {
-    // ------------------------------------------------------------ normalisers
-    // This lane's columns lane + 32 k: head g and token j of the chunk.
+    // A chunk's rows by TMA, and its rows' normalisers beside them, from this lane's columns
+    // lane + 32 k: head g and token j of the chunk.
     int j[kChunk / 32], g[kChunk / 32];
 #pragma unroll
     for (int k = 0; k < kChunk / 32; ++k) {
@@ -449,19 +445,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kChunk / 32; ++k)
             y[k] = j[k] < it.nq - j0 ? lse[static_cast<size_t>(g[k]) * a.n + j0 + j[k]] : INFINITY;
-          const int st = use % kSums;
-          if (!(ok = warp_wait(&y_empty[st], ((use / kSums) & 1) ^ 1, abort, c.status))) break;
-          ++use;
-#pragma unroll
-          for (int k = 0; k < kChunk / 32; ++k) s_sums[st * kChunk + lane + 32 * k] = -lse_base2(y[k]);
+          const int st = use % NS, sy = use % kSums;
+          if (!(ok = warp_wait(&q_empty[st], ((use / NS) & 1) ^ 1, abort, c.status))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&q_full[st], DB * p.P * p.tok * 128);
+            for (int x = 0; x < DB; ++x)
+              tma_load_5d(smem + Sm::kRing + st * Sm::kStage + x * kQueryBlock, &map_q, 64 * x,
+                          (it.h * a.G + s * p.P) * p.q_head, it.first + j0, a.first ? 0 : it.b * p.q_seq,
+                          it.l * p.q_layer, &q_full[st]);
+          }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&y_full[st]);
+          ++use;
+          if (!(ok = warp_wait(&y_empty[sy], (((use - 1) / kSums) & 1) ^ 1, abort, c.status))) break;
+#pragma unroll
+          for (int k = 0; k < kChunk / 32; ++k) s_sums[sy * kChunk + lane + 32 * k] = -lse_base2(y[k]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&y_full[sy]);
         }
       }
     }
+    volatile int never = 0;  // every copy has landed before the CTA ends
+    for (uint32_t u = use > NS ? use - NS : 0; u < use; ++u)
+      mbar_wait(&q_full[u % NS], (u / NS) & 1, &never, c.status);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
-    // (all lanes run the loop and wait converged; lane 0 issues)
+    // (all lanes run the loop and wait converged)
+    const bool lead = lane == 0;
     const uint32_t base = smem_u32(smem);
     uint32_t use = 0;
     int steps[2] = {0, 0};
@@ -477,31 +486,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool begins = s == 0 && ch == it.c0, ends = s + 1 == p.subs && ch + 1 == it.chunks;
           const int n = (min(it.nq - ch * p.tok, p.tok) * p.P + 15) & ~15;  // columns
           const uint32_t idesc = idesc_bf16_f32(kTile, n);
-          const uint32_t q_tile = base + Sm::kRing + st * Sm::kStage;
+          const uint32_t q_low = desc_low(base + Sm::kRing + st * Sm::kStage, 16);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (!ok) continue;
             if (begins && !(ok = warp_wait(&k_full[t], i & 1, abort, c.status))) continue;
-            const bool sees = t == 0 || ch >= it.c1;
-            if (sees) {
+            if (t == 0 || ch >= it.c1) {
               if (!(ok = warp_wait(&s_empty[t], (steps[t] & 1) ^ 1, abort, c.status))) continue;
               ++steps[t];
               tc_fence_after();
-              if (lane == 0) {
-                const uint32_t k_tile = base + Sm::kKeys + t * Sm::kKeyTile;
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x)
-                  mma_bf16(tmem + t * 256, sw128_desc(k_tile + (x / 4) * kKeyBlock + (x % 4) * 32),
-                           sw128_desc(q_tile + (x / 4) * kQueryBlock + (x % 4) * 32), idesc, x > 0);
-                mma_commit(&s_full[t]);
-              }
-              __syncwarp();
+              for (int x = 0; x < D / 16; ++x)
+                mma_ts_if(lead, tmem + t * kChunk, tmem + kKeyCol + t * (D / 2) + x * 8,
+                          q_low + (((x / 4) * kQueryBlock + (x % 4) * 32) >> 4), idesc, x > 0);
+              commit_if(lead, &s_full[t]);
             }
-            if (ends && lane == 0) mma_commit(&k_empty[t]);
-            __syncwarp();
+            if (ends) commit_if(lead, &k_empty[t]);
           }
-          if (ok && lane == 0) mma_commit(&q_empty[st]);
-          __syncwarp();
+          if (ok) commit_if(lead, &q_empty[st]);
         }
       if (ok && per_sub <= 0) {  // no queries: the keys are done with at once
         for (int t = 0; t < 2; ++t) {
