@@ -8,7 +8,8 @@
 //
 // The rows are read and written once, which bounds the call.  A CTA has a few tokens and all
 // (or a share) of their heads: it computes their sines and cosines once into shared memory,
-// then each thread turns two 16-byte chunks at a time, those that its pairs lie in.
+// then each thread turns two 16-byte chunks of a row at a time, those that its pairs lie in.
+#include "cache8_attend.cuh"
 #include "prompt.cuh"
 
 namespace kvc {
@@ -21,7 +22,8 @@ using cache8::bf16_lo;
 using cache8::bf16x2;
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 4;  // of a CTA
+constexpr int kTokens = 8;  // of a CTA at most
+constexpr int kBatch = 4;   // rows of a thread whose loads are in flight together
 
 __device__ __forceinline__ uint32_t turn_x(uint32_t x, uint32_t y, float2 a, float2 b) {
   return bf16x2(fmaf(bf16_lo(x), a.x, -bf16_lo(y) * a.y), fmaf(bf16_hi(x), b.x, -bf16_hi(y) * b.y));
@@ -42,80 +44,129 @@ __device__ __forceinline__ float2 angle_of(const kvc_rope& r, int i, int pos) {
   return make_float2(c * r.magnitude, s * r.magnitude);
 }
 
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a,
-                                                          int shares) {
-  __shared__ __align__(16) float2 s_cs[kTokens][64];
-  __shared__ int s_n[kTokens];  // 1: the token is there
-  before_all();
-  const long long t0 = static_cast<long long>(blockIdx.x) * kTokens, all = static_cast<long long>(a.S) * a.n;
-  const int l = blockIdx.z, pairs = a.rope.dim / 2;
-  if (threadIdx.x < kTokens) {
-    const long long t = t0 + threadIdx.x;
-    int there = t < all;
-    if (there && a.n_tok) {
-      const int b = static_cast<int>(t / a.n), j = static_cast<int>(t % a.n), m = a.n_tok[b];
-      if (m < 0 || m > a.n) {
-        there = 0;
-        if (j == 0 && l == 0 && blockIdx.y == 0) atomicOr(a.status, KVC_STATUS_BAD_INDEX);
-      } else {
-        there = j < m;
-      }
-    }
-    s_n[threadIdx.x] = there;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kTokens * pairs; i += kThreads) {
-    const int k = i / pairs;
-    if (s_n[k]) s_cs[k][i % pairs] = angle_of(a.rope, i % pairs, a.pos[t0 + k]);
-  }
-  __syncthreads();
-  const int units = a.d / 16, turned = a.rope.dim / 16;  // two 16-byte chunks each
-  const int heads = a.heads[0] + a.heads[1];
-  for (int i = threadIdx.x + blockIdx.y * kThreads; i < kTokens * heads * units;
-       i += kThreads * shares) {
-    const int u = i % units, row = i / units, head = row % heads, k = row / heads;
-    if (!s_n[k]) continue;
-    const int w = head < a.heads[0] ? 0 : 1;
-    if (u >= turned && a.in_place[w]) continue;
-    const long long t = t0 + k;
-    const int b = static_cast<int>(t / a.n), j = static_cast<int>(t % a.n);
-    const int h = w ? head - a.heads[0] : head;
-    // chunks of a turned unit: dim / 2 values apart; of the rest: side by side
-    const int c0 = u < turned ? u : 2 * u, c1 = u < turned ? u + turned : 2 * u + 1;
-    const uint4* from = reinterpret_cast<const uint4*>(a.in[w].at(l, b, h, j));
-    uint4 x = from[c0], y = from[c1];
-    if (u < turned) {
-      const float4* cs0 = reinterpret_cast<const float4*>(s_cs[k]);
-      if (a.rope.interleaved) {
-        const float4 p = cs0[2 * c0], q = cs0[2 * c0 + 1], r = cs0[2 * c1], s = cs0[2 * c1 + 1];
-        x = make_uint4(turn_pair(x.x, make_float2(p.x, p.y)), turn_pair(x.y, make_float2(p.z, p.w)),
-                       turn_pair(x.z, make_float2(q.x, q.y)), turn_pair(x.w, make_float2(q.z, q.w)));
-        y = make_uint4(turn_pair(y.x, make_float2(r.x, r.y)), turn_pair(y.y, make_float2(r.z, r.w)),
-                       turn_pair(y.z, make_float2(s.x, s.y)), turn_pair(y.w, make_float2(s.z, s.w)));
-      } else {
-        uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w}, xo[4], yo[4];
+// Both chunks of a unit turned: pairs of chunk c0's values and chunk c1's, or of side by side values.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn(uint4& x, uint4& y, const float4* cs, int c0, int c1) {
+  uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const float4 p = cs0[4 * c0 + z];
-          xo[z] = turn_x(xs[z], ys[z], make_float2(p.x, p.y), make_float2(p.z, p.w));
-          yo[z] = turn_y(xs[z], ys[z], make_float2(p.x, p.y), make_float2(p.z, p.w));
-        }
-        x = make_uint4(xo[0], xo[1], xo[2], xo[3]);
-        y = make_uint4(yo[0], yo[1], yo[2], yo[3]);
+  for (int z = 0; z < 4; z += INTERLEAVED ? 2 : 1) {
+    if constexpr (INTERLEAVED) {
+      const float4 p = cs[2 * c0 + z / 2], q = cs[2 * c1 + z / 2];
+      xs[z] = turn_pair(xs[z], make_float2(p.x, p.y));
+      xs[z + 1] = turn_pair(xs[z + 1], make_float2(p.z, p.w));
+      ys[z] = turn_pair(ys[z], make_float2(q.x, q.y));
+      ys[z + 1] = turn_pair(ys[z + 1], make_float2(q.z, q.w));
+    } else {
+      const float4 p = cs[4 * c0 + z];
+      const float2 a = make_float2(p.x, p.y), b = make_float2(p.z, p.w);
+      const uint32_t first = turn_x(xs[z], ys[z], a, b);
+      ys[z] = turn_y(xs[z], ys[z], a, b);
+      xs[z] = first;
+    }
+  }
+  x = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+  y = make_uint4(ys[0], ys[1], ys[2], ys[3]);
+}
+
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a,
+                                                          int tokens, int shares, cache8::Div by_heads) {
+  constexpr int kUnits = D / 16;                 // of a row: two 16-byte chunks each
+  constexpr int kRows = kThreads / kUnits;       // rows that the CTA's threads take at a time
+  __shared__ __align__(16) float2 s_cs[kTokens][64];
+  __shared__ long long s_at[4][kTokens];         // a token's place in the rows of in, in, out, out
+  __shared__ int s_pos[kTokens], s_there[kTokens];
+  before_all();
+  const long long t0 = static_cast<long long>(blockIdx.x) * tokens, all = static_cast<long long>(a.S) * a.n;
+  const int l = blockIdx.z, pairs = a.rope.dim / 2, turned = a.rope.dim / 16;
+  if (threadIdx.x < tokens) {
+    const long long t = t0 + threadIdx.x;
+    int there = t < all, pos = 0;
+    if (there) {
+      pos = a.pos[t];
+      const int b = static_cast<int>(t / a.n), j = static_cast<int>(t % a.n);
+      if (a.n_tok) {
+        const int m = a.n_tok[b];
+        there = j < m && m <= a.n;
+        if ((m < 0 || m > a.n) && j == 0 && l == 0 && blockIdx.y == 0)
+          atomicOr(a.status, KVC_STATUS_BAD_INDEX);
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        s_at[w][threadIdx.x] = l * a.in[w].layer + b * a.in[w].seq + j * a.in[w].token;
+        s_at[w + 2][threadIdx.x] = l * a.out[w].layer + b * a.out[w].seq + j * a.out[w].token;
       }
     }
-    uint4* to = reinterpret_cast<uint4*>(a.out[w].at(l, b, h, j));
-    to[c0] = x;
-    to[c1] = y;
+    s_there[threadIdx.x] = there;
+    s_pos[threadIdx.x] = pos;
+  }
+  __syncthreads();
+  // This thread: unit u of rows (token, head) i, i + kRows, ...; a few rows' loads together, the
+  // first ones before the angles.
+  const int u = threadIdx.x % kUnits, heads = a.heads[0] + a.heads[1], total = tokens * heads;
+  // chunks of a turned unit: dim / 2 values apart; of the rest: side by side
+  const int c0 = u < turned ? u : 2 * u, c1 = u < turned ? u + turned : 2 * u + 1;
+  uint4 x[kBatch], y[kBatch];
+  auto row_of = [&](int i, int* k, int* w) {  // its head among its kind; -1: nothing to do
+    if (i >= total) return -1;
+    *k = by_heads.div(i);
+    const int head = i - *k * heads;
+    *w = head >= a.heads[0];
+    if (!s_there[*k] || (u >= turned && a.in_place[*w])) return -1;
+    return *w ? head - a.heads[0] : head;
+  };
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int z = 0; z < kBatch; ++z) {
+      int k, w;
+      const int h = row_of(i0 + z * kRows, &k, &w);
+      if (h < 0) continue;
+      const Rows& r = w ? a.in[1] : a.in[0];
+      const uint4* from = reinterpret_cast<const uint4*>(r.data + s_at[w][k] + h * r.head);
+      x[z] = from[c0];
+      y[z] = from[c1];
+    }
+  };
+  const int step = kRows * kBatch * shares;
+  int i0 = threadIdx.x / kUnits + blockIdx.y * (kRows * kBatch);
+  load(i0);
+  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+    const int k = i / pairs;
+    if (s_there[k]) s_cs[k][i % pairs] = angle_of(a.rope, i % pairs, s_pos[k]);
+  }
+  __syncthreads();
+  for (; i0 < total; i0 += step) {
+#pragma unroll
+    for (int z = 0; z < kBatch; ++z) {
+      int k, w;
+      const int h = row_of(i0 + z * kRows, &k, &w);
+      if (h < 0) continue;
+      if (u < turned) turn<INTERLEAVED>(x[z], y[z], reinterpret_cast<const float4*>(s_cs[k]), c0, c1);
+      const Rows& r = w ? a.out[1] : a.out[0];
+      uint4* to = reinterpret_cast<uint4*>(r.data + s_at[w + 2][k] + h * r.head);
+      to[c0] = x[z];
+      to[c1] = y[z];
+    }
+    if (i0 + step < total) load(i0 + step);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
-  const long long groups = (static_cast<long long>(a.S) * a.n + kTokens - 1) / kTokens;
-  return cache8::launch(rotary_kernel, dim3(static_cast<unsigned>(groups), 1, a.L), kThreads, 0, s, a,
-                        1);
+  // As many tokens a CTA as give each thread a batch of rows; fewer, and a token's rows over several
+  // CTAs, where there are not two CTAs for each SM.
+  const long long all = static_cast<long long>(a.S) * a.n;
+  const int heads = a.heads[0] + a.heads[1], rows = kThreads / (a.d / 16) * kBatch;
+  int tokens = min(max(rows / heads, 1), kTokens);
+  while (tokens > 1 && (all + tokens - 1) / tokens * a.L < 2 * a.num_sms) tokens /= 2;
+  const long long groups = (all + tokens - 1) / tokens;
+  const int batches = (tokens * heads + rows - 1) / rows;
+  const int shares = groups * a.L < 2 * a.num_sms ? min(batches, 16) : 1;
+  auto* kernel = a.d == 64 ? (a.rope.interleaved ? rotary_kernel<64, true> : rotary_kernel<64, false>)
+                           : (a.rope.interleaved ? rotary_kernel<128, true> : rotary_kernel<128, false>);
+  return cache8::launch(kernel, dim3(static_cast<unsigned>(groups), shares, a.L), kThreads, 0, s, a,
+                        tokens, shares, cache8::make_div(heads));
 }
 
 }  // namespace prompt

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass, fields
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -143,6 +144,8 @@ class _CRope(ctypes.Structure):
     _fields_ = [("dim", ctypes.c_int), ("interleaved", ctypes.c_int),
                 ("magnitude", ctypes.c_float), ("turn", ctypes.c_uint64 * 64)]
 
+
+_pack_rows = struct.Struct("@P4q").pack  # a kvc_rows, as bytes
 
 _lib = None
 _P = ctypes.c_void_p
@@ -347,6 +350,7 @@ class Handle:
             raise KvcError(rc, "kvc_create failed")
         self._h = h
         import torch
+        self._torch = torch
         self._device = torch.device("cuda", torch.cuda.current_device())
 
     # -- helpers -------------------------------------------------------------
@@ -621,40 +625,46 @@ class Handle:
         """kvc_cache8_weigh: weights [L, B, H, cap] fp32 (in place) gather what the newest tokens'
         queries give them.  q [L, B, H*G, n, d] bf16 (any strides), lse [L, B, H*G, n] fp32, n_q
         [B] int32 or None; packed, with first [B] int32: q [L, H*G, n, d], lse [L, H*G, n]."""
-        import torch
-        ref = self._cache8(cache)
-        L, B = cache.n_layers, cache.batch
+        ref, torch = self._cache8(cache), self._torch
+        L, B, H = cache.n_layers, cache.batch, cache.n_kv_heads
         seqs = () if first is not None else (B,)
         n = q.shape[-2] if q.dim() == 4 + len(seqs) else 0
-        shape = (L, *seqs, cache.n_kv_heads * self.cfg.group, n, cache.head_dim)
-        if lse.shape != shape[:-1]:
-            raise ValueError(f"lse: expected shape {shape[:-1]}, got {tuple(lse.shape)}")
-        if weights.dim() != 4 or weights.shape[:3] != (L, B, cache.n_kv_heads):
-            raise ValueError(f"weights: expected shape {(L, B, cache.n_kv_heads)} + (cap,), got "
-                             f"{tuple(weights.shape)}")
+        shape = (L, *seqs, H * self.cfg.group, n, cache.head_dim)
+        cap = weights.shape[-1] if weights.dim() == 4 else 0
         self._check(load_library().kvc_cache8_weigh(
-            self._h, ref, self._strided(q, "q", shape, cache.device, 1 if seqs else None), n,
-            None if first is None else self._ints(first, "first", (B,), cache.device),
-            None if n_q is None else self._ints(n_q, "n_q", (B,), cache.device),
-            self._on(lse, torch.float32, "lse", cache.device), decay,
-            self._on(weights, torch.float32, "weights", cache.device), weights.shape[3],
+            self._h, ref, self._strided(q, "q", shape, 1 if seqs else None), n,
+            None if first is None else self._dense(first, torch.int32, "first", (B,)),
+            None if n_q is None else self._dense(n_q, torch.int32, "n_q", (B,)),
+            self._dense(lse, torch.float32, "lse", shape[:-1]), decay,
+            self._dense(weights, torch.float32, "weights", (L, B, H, cap)), cap,
             self._stream(stream)), "kvc_cache8_weigh")
 
     # -- prompts ---------------------------------------------------------------
-    @staticmethod
-    def _strided(t, name, shape, device, seq_axis, layer_axis=0):
+    # (These calls may be a few microseconds on the GPU, so that their checks count: a tensor that is
+    # right takes one pass over its attributes, and kvc_rows are packed, not built as structures.)
+    def _strided(self, t, name, shape, seq_axis, layer_axis=0):
         """kvc_rows of a bf16 tensor of `shape`, (..., heads, n, d), of any strides, d contiguous;
         the axes of layers and sequences, None where there is none."""
-        import torch
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        torch = self._torch
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
             raise TypeError(f"{name}: expected a torch.bfloat16 tensor")
-        if t.device != device:
-            raise ValueError(f"{name}: on {t.device}, expected {device}")
-        if t.shape != shape or t.stride(-1) != 1:
-            raise ValueError(f"{name}: expected shape {shape}, the last axis contiguous")
+        if t.get_device() != self._device.index:
+            raise ValueError(f"{name}: on {t.device}, the handle on {self._device}")
         s = t.stride()
-        return ctypes.byref(_Rows(t.data_ptr(), 0 if layer_axis is None else s[layer_axis],
-                                  0 if seq_axis is None else s[seq_axis], s[-3], s[-2]))
+        if t.shape != shape or s[-1] != 1:
+            raise ValueError(f"{name}: expected shape {shape}, the last axis contiguous")
+        return _pack_rows(t.data_ptr(), 0 if layer_axis is None else s[layer_axis],
+                          0 if seq_axis is None else s[seq_axis], s[-3], s[-2])
+
+    def _dense(self, t, dtype, name, shape):
+        """Pointer to a contiguous tensor of `shape` on the handle's device."""
+        if not isinstance(t, self._torch.Tensor) or t.dtype is not dtype:
+            raise TypeError(f"{name}: expected {dtype}")
+        if t.get_device() != self._device.index:
+            raise ValueError(f"{name}: on {t.device}, the handle on {self._device} (a CUDA tensor is needed)")
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, contiguous, got {tuple(t.shape)}")
+        return t.data_ptr()
 
     def rotary(self, rope, pos, q=None, k=None, q_out=None, k_out=None, n_tok=None, stream=None):
         """kvc_rotary: rows of q [L, S, H*G, n, d] and k [L, S, H, n, d] bf16 (any strides; either
@@ -662,67 +672,61 @@ class Handle:
         int32 or None.  S sequences of the call's own: packed prompts are one."""
         if not isinstance(rope, Rope):
             raise TypeError("rope: expected a Rope")
-        c = self.cfg
+        c, i32 = self.cfg, self._torch.int32
         one = q if q is not None else k
         if one is None:
             raise ValueError("q, k or both")
         L, S, _, n = one.shape[:4] if one.dim() == 5 else (0,) * 4
-        rows = []
-        for name, t, out, heads in (("q", q, q_out, c.n_kv_heads * c.group),
-                                    ("k", k, k_out, c.n_kv_heads)):
-            if t is None and out is not None:
+        rows = [None] * 4
+        for w, (name, t, out, heads) in enumerate((("q", q, q_out, c.n_kv_heads * c.group),
+                                                   ("k", k, k_out, c.n_kv_heads))):
+            if t is not None:
+                shape = (L, S, heads, n, c.head_dim)
+                rows[w] = self._strided(t, name, shape, 1)
+                rows[w + 2] = rows[w] if out is None else self._strided(out, name + "_out", shape, 1)
+            elif out is not None:
                 raise ValueError(f"{name}_out without {name}")
-            shape = (L, S, heads, n, c.head_dim)
-            rows.append([None if x is None else self._strided(x, nm, shape, self._device, 1)
-                         for nm, x in ((name, t), (name + "_out", t if out is None else out))])
         self._check(load_library().kvc_rotary(
-            self._h, rope._ref, rows[0][0], rows[1][0], rows[0][1], rows[1][1], L, S, n,
-            self._ints(pos, "pos", (S, n), self._device),
-            None if n_tok is None else self._ints(n_tok, "n_tok", (S,), self._device),
+            self._h, rope._ref, rows[0], rows[1], rows[2], rows[3], L, S, n,
+            self._dense(pos, i32, "pos", (S, n)),
+            None if n_tok is None else self._dense(n_tok, i32, "n_tok", (S,)),
             self._stream(stream)), "kvc_rotary")
 
     def prompt_attend(self, q, k, v, out, lse=None, first=None, n_tok=None, stream=None):
         """kvc_prompt_attend: causal attention over whole prompts.  Padded: q, out [S, H*G, n, d], k,
         v [S, H, n, d] bf16 (any strides), lse [S, H*G, n] fp32 or None, n_tok [S] int32 or None.
         Packed, with first [S] int32: the same without S, and n_tok."""
-        import torch
-        c, seqs = self.cfg, ()
-        if first is None:
-            seqs = (q.shape[0],)
+        c, torch = self.cfg, self._torch
+        seqs = (q.shape[0],) if first is None else ()
         S = seqs[0] if seqs else first.numel()
         n = q.shape[-2] if q.dim() == 3 + len(seqs) else 0
-        heads = (*seqs, c.n_kv_heads * c.group)
-        rows = [self._strided(t, name, (*seqs, x, n, c.head_dim), self._device, 0 if seqs else None, None)
-                for name, t, x in (("q", q, heads[-1]), ("k", k, c.n_kv_heads), ("v", v, c.n_kv_heads),
-                                   ("out", out, heads[-1]))]
-        if lse is not None and lse.shape != (*heads, n):
-            raise ValueError(f"lse: expected shape {(*heads, n)}, got {tuple(lse.shape)}")
+        seq = 0 if seqs else None
+        many, few = (*seqs, c.n_kv_heads * c.group, n, c.head_dim), (*seqs, c.n_kv_heads, n, c.head_dim)
         self._check(load_library().kvc_prompt_attend(
-            self._h, rows[0], rows[1], rows[2], S, n,
-            None if first is None else self._ints(first, "first", (S,), self._device),
-            None if n_tok is None else self._ints(n_tok, "n_tok", (S,), self._device), rows[3],
-            None if lse is None else self._on(lse, torch.float32, "lse", self._device),
+            self._h, self._strided(q, "q", many, seq, None), self._strided(k, "k", few, seq, None),
+            self._strided(v, "v", few, seq, None), S, n,
+            None if first is None else self._dense(first, torch.int32, "first", (S,)),
+            None if n_tok is None else self._dense(n_tok, torch.int32, "n_tok", (S,)),
+            self._strided(out, "out", many, seq, None),
+            None if lse is None else self._dense(lse, torch.float32, "lse", many[:-1]),
             self._stream(stream)), "kvc_prompt_attend")
 
     def keep_heaviest(self, weights, seq_len, kept_idx, n_kept, weights_out, stream=None):
         """kvc_keep_heaviest: the tokens that an eviction keeps by weights [L, B, H, cap] fp32 of
         sequences of seq_len [B] int32: kept_idx [L, B, H, budget], n_kept [L, B, H] int32, and
         their weights in weights_out [L, B, H, cap] (may be weights)."""
-        import torch
-        c = self.cfg
-        if weights.dim() != 4 or weights.shape[1:3] != (c.batch, c.n_kv_heads):
+        c, torch = self.cfg, self._torch
+        shape = weights.shape
+        if len(shape) != 4 or shape[1:3] != (c.batch, c.n_kv_heads):
             raise ValueError(f"weights: expected shape (L, {c.batch}, {c.n_kv_heads}, cap), got "
-                             f"{tuple(weights.shape)}")
-        if weights_out.shape != weights.shape:
-            raise ValueError(f"weights_out: expected shape {tuple(weights.shape)}, got "
-                             f"{tuple(weights_out.shape)}")
-        units = tuple(weights.shape[:3])
+                             f"{tuple(shape)}")
+        L, B, H, cap = shape
         self._check(load_library().kvc_keep_heaviest(
-            self._h, self._on(weights, torch.float32, "weights", self._device), units[0],
-            weights.shape[3], self._ints(seq_len, "seq_len", (c.batch,), self._device),
-            self._ints(kept_idx, "kept_idx", units + (c.budget,), self._device),
-            self._ints(n_kept, "n_kept", units, self._device),
-            self._on(weights_out, torch.float32, "weights_out", self._device),
+            self._h, self._dense(weights, torch.float32, "weights", shape), L, cap,
+            self._dense(seq_len, torch.int32, "seq_len", (B,)),
+            self._dense(kept_idx, torch.int32, "kept_idx", (L, B, H, c.budget)),
+            self._dense(n_kept, torch.int32, "n_kept", (L, B, H)),
+            self._dense(weights_out, torch.float32, "weights_out", shape),
             self._stream(stream)), "kvc_keep_heaviest")
 
     def wait_self_test(self, stream=None):

@@ -149,7 +149,7 @@ def test_rotary_refuses():
     with pytest.raises(kvc.KvcError, match="16-byte aligned"):
         h.rotary(rope, pos, q=odd[1:1 + q.numel()].reshape(q.shape))
     lib, n = kvc.load_library(), ctypes.c_void_p(0)
-    r = h._strided(q, "q", q.shape, q.device, 1)
+    r = h._strided(q, "q", q.shape, 1)
     p = ctypes.c_void_p(pos.data_ptr())
     assert lib.kvc_rotary(h._h, None, r, n, r, n, 1, 2, 3, p, n, n) == -1
     assert lib.kvc_rotary(h._h, rope._ref, n, n, n, n, 1, 2, 3, p, n, n) == -1
@@ -395,7 +395,7 @@ def test_prompt_refuses():
     with pytest.raises(kvc.KvcError, match="rows overlap"):
         p.h.prompt_attend(**dict(ok, out=p.q[:, :1].expand_as(p.q)), n_tok=n_tok)
     lib, z = kvc.load_library(), ctypes.c_void_p(0)
-    r = {k: p.h._strided(t, k, tuple(t.shape), t.device, 0, None) for k, t in ok.items()}
+    r = {k: p.h._strided(t, k, tuple(t.shape), 0, None) for k, t in ok.items()}
     c = ctypes.c_void_p(n_tok.data_ptr())
     call = lambda S, n, q=r["q"], f=z, t=c: lib.kvc_prompt_attend(  # noqa: E731
         p.h._h, q, r["k"], r["v"], S, n, f, t, r["out"], z, z)

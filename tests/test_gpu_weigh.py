@@ -231,7 +231,7 @@ def test_weigh_refuses():
     with pytest.raises(kvc.KvcError, match="need n_q"):
         p.h.cache8_weigh(p.c, p.q[:, 0], p.lse[:, 0], p.old, first=_ints([0, 1]))
     lib, z = kvc.load_library(), ctypes.c_void_p(0)
-    q = p.h._strided(p.q, "q", tuple(p.q.shape), p.q.device, 1)
+    q = p.h._strided(p.q, "q", tuple(p.q.shape), 1)
     l, w = ctypes.c_void_p(p.lse.data_ptr()), ctypes.c_void_p(p.old.data_ptr())
     call = lambda n=2, lse=l, wt=w, cap=p.cap, c=p.c._ref: lib.kvc_cache8_weigh(  # noqa: E731
         p.h._h, c, q, n, z, z, lse, 1.0, wt, cap, z)
