@@ -23,7 +23,7 @@ using cache8::bf16x2;
 
 constexpr int kThreads = 256;
 constexpr int kTokens = 8;  // of a CTA at most
-constexpr int kBatch = 4;   // rows of a thread whose loads are in flight together
+constexpr int kBatch = 4;   // heads of a thread whose loads are in flight together
 
 __device__ __forceinline__ uint32_t turn_x(uint32_t x, uint32_t y, float2 a, float2 b) {
   return bf16x2(fmaf(bf16_lo(x), a.x, -bf16_lo(y) * a.y), fmaf(bf16_hi(x), b.x, -bf16_hi(y) * b.y));
@@ -44,21 +44,19 @@ __device__ __forceinline__ float2 angle_of(const kvc_rope& r, int i, int pos) {
   return make_float2(c * r.magnitude, s * r.magnitude);
 }
 
-// Both chunks of a unit turned: pairs of chunk c0's values and chunk c1's, or of side by side values.
+// Both chunks of a unit turned, with its eight pairs' (cos, sin): those of chunk c0's values and
+// chunk c1's, or of chunk c0 and then of chunk c1.
 template <bool INTERLEAVED>
-__device__ __forceinline__ void turn(uint4& x, uint4& y, const float4* cs, int c0, int c1) {
+__device__ __forceinline__ void turn(uint4& x, uint4& y, const float4 (&cs)[4]) {
   uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int z = 0; z < 4; z += INTERLEAVED ? 2 : 1) {
+  for (int z = 0; z < 4; ++z) {
+    const float2 a = make_float2(cs[z].x, cs[z].y), b = make_float2(cs[z].z, cs[z].w);
     if constexpr (INTERLEAVED) {
-      const float4 p = cs[2 * c0 + z / 2], q = cs[2 * c1 + z / 2];
-      xs[z] = turn_pair(xs[z], make_float2(p.x, p.y));
-      xs[z + 1] = turn_pair(xs[z + 1], make_float2(p.z, p.w));
-      ys[z] = turn_pair(ys[z], make_float2(q.x, q.y));
-      ys[z + 1] = turn_pair(ys[z + 1], make_float2(q.z, q.w));
+      uint32_t* v = z < 2 ? &xs[2 * z] : &ys[2 * z - 4];
+      v[0] = turn_pair(v[0], a);
+      v[1] = turn_pair(v[1], b);
     } else {
-      const float4 p = cs[4 * c0 + z];
-      const float2 a = make_float2(p.x, p.y), b = make_float2(p.z, p.w);
       const uint32_t first = turn_x(xs[z], ys[z], a, b);
       ys[z] = turn_y(xs[z], ys[z], a, b);
       xs[z] = first;
@@ -69,11 +67,11 @@ __device__ __forceinline__ void turn(uint4& x, uint4& y, const float4* cs, int c
 }
 
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a,
-                                                          int tokens, int shares, cache8::Div by_heads) {
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotaryArgs a,
+                                                          int tokens, int slots, cache8::Div by_slots) {
   constexpr int kUnits = D / 16;                 // of a row: two 16-byte chunks each
   constexpr int kRows = kThreads / kUnits;       // rows that the CTA's threads take at a time
-  __shared__ __align__(16) float2 s_cs[kTokens][64];
+  __shared__ __align__(16) float4 s_cs[kTokens][4][kUnits];  // two pairs each, of a unit's eight
   __shared__ long long s_at[4][kTokens];         // a token's place in the rows of in, in, out, out
   __shared__ int s_pos[kTokens], s_there[kTokens];
   before_all();
@@ -101,72 +99,80 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     s_pos[threadIdx.x] = pos;
   }
   __syncthreads();
-  // This thread: unit u of rows (token, head) i, i + kRows, ...; a few rows' loads together, the
-  // first ones before the angles.
-  const int u = threadIdx.x % kUnits, heads = a.heads[0] + a.heads[1], total = tokens * heads;
+  // This thread: unit u of a token's heads slot, slot + slots, ...: their sines and cosines are
+  // the same.  Their loads go out together, the first ones before the angles.
+  const int u = threadIdx.x % kUnits, heads = a.heads[0] + a.heads[1], total = tokens * slots;
   // chunks of a turned unit: dim / 2 values apart; of the rest: side by side
   const int c0 = u < turned ? u : 2 * u, c1 = u < turned ? u + turned : 2 * u + 1;
   uint4 x[kBatch], y[kBatch];
-  auto row_of = [&](int i, int* k, int* w) {  // its head among its kind; -1: nothing to do
-    if (i >= total) return -1;
-    *k = by_heads.div(i);
-    const int head = i - *k * heads;
-    *w = head >= a.heads[0];
-    if (!s_there[*k] || (u >= turned && a.in_place[*w])) return -1;
-    return *w ? head - a.heads[0] : head;
+  auto row_at = [&](const Rows (&of)[2], int side, int k, int head) {  // null: nothing to do
+    const int w = head >= a.heads[0];
+    if (head >= heads || (u >= turned && a.in_place[w])) return static_cast<uint4*>(nullptr);
+    return reinterpret_cast<uint4*>((w ? of[1].data : of[0].data) + s_at[2 * side + w][k] +
+                                    (w ? (head - a.heads[0]) * of[1].head : head * of[0].head));
   };
-  auto load = [&](int i0) {
+  auto load = [&](int s) {
+    const int k = by_slots.div(s), slot = s - k * slots;
+    if (s >= total || !s_there[k]) return;
 #pragma unroll
     for (int z = 0; z < kBatch; ++z) {
-      int k, w;
-      const int h = row_of(i0 + z * kRows, &k, &w);
-      if (h < 0) continue;
-      const Rows& r = w ? a.in[1] : a.in[0];
-      const uint4* from = reinterpret_cast<const uint4*>(r.data + s_at[w][k] + h * r.head);
+      const uint4* from = row_at(a.in, 0, k, slot + z * slots);
+      if (!from) continue;
       x[z] = from[c0];
       y[z] = from[c1];
     }
   };
-  const int step = kRows * kBatch * shares;
-  int i0 = threadIdx.x / kUnits + blockIdx.y * (kRows * kBatch);
-  load(i0);
+  int s = threadIdx.x / kUnits + blockIdx.y * kRows;
+  load(s);
   for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
-    const int k = i / pairs;
-    if (s_there[k]) s_cs[k][i % pairs] = angle_of(a.rope, i % pairs, s_pos[k]);
+    const int k = i / pairs, pair = i % pairs;
+    if (!s_there[k]) continue;
+    // its unit and place there: units have pairs 8 u .. + 7, or those of their two chunks
+    int unit = pair / 8, at = pair % 8;
+    if constexpr (INTERLEAVED) {
+      const int chunk = pair / 4;
+      unit = chunk < turned ? chunk : chunk - turned;
+      at = pair % 4 + (chunk < turned ? 0 : 4);
+    }
+    reinterpret_cast<float2*>(&s_cs[k][at / 2][unit])[at % 2] = angle_of(a.rope, pair, s_pos[k]);
   }
   __syncthreads();
-  for (; i0 < total; i0 += step) {
+  for (; s < total; s += kRows * gridDim.y) {
+    const int k = by_slots.div(s), slot = s - k * slots;
+    if (s_there[k]) {
+      float4 cs[4];
 #pragma unroll
-    for (int z = 0; z < kBatch; ++z) {
-      int k, w;
-      const int h = row_of(i0 + z * kRows, &k, &w);
-      if (h < 0) continue;
-      if (u < turned) turn<INTERLEAVED>(x[z], y[z], reinterpret_cast<const float4*>(s_cs[k]), c0, c1);
-      const Rows& r = w ? a.out[1] : a.out[0];
-      uint4* to = reinterpret_cast<uint4*>(r.data + s_at[w + 2][k] + h * r.head);
-      to[c0] = x[z];
-      to[c1] = y[z];
+      for (int z = 0; z < 4; ++z) cs[z] = s_cs[k][z][u];
+#pragma unroll
+      for (int z = 0; z < kBatch; ++z) {
+        uint4* to = row_at(a.out, 1, k, slot + z * slots);
+        if (!to) continue;
+        if (u < turned) turn<INTERLEAVED>(x[z], y[z], cs);
+        to[c0] = x[z];
+        to[c1] = y[z];
+      }
     }
-    if (i0 + step < total) load(i0 + step);
+    load(s + kRows * gridDim.y);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s) {
-  // As many tokens a CTA as give each thread a batch of rows; fewer, and a token's rows over several
-  // CTAs, where there are not two CTAs for each SM.
+  // Slots of kBatch heads each; as many tokens a CTA as its threads have slots for, fewer where
+  // there are not two CTAs for each SM, and a token's slots over several CTAs then.
   const long long all = static_cast<long long>(a.S) * a.n;
-  const int heads = a.heads[0] + a.heads[1], rows = kThreads / (a.d / 16) * kBatch;
-  int tokens = min(max(rows / heads, 1), kTokens);
+  const int heads = a.heads[0] + a.heads[1], rows = kThreads / (a.d / 16);
+  const int slots = (heads + kBatch - 1) / kBatch;
+  int tokens = min(max(rows / slots, 1), kTokens);
   while (tokens > 1 && (all + tokens - 1) / tokens * a.L < 2 * a.num_sms) tokens /= 2;
   const long long groups = (all + tokens - 1) / tokens;
-  const int batches = (tokens * heads + rows - 1) / rows;
-  const int shares = groups * a.L < 2 * a.num_sms ? min(batches, 16) : 1;
+  const int passes = (tokens * slots + rows - 1) / rows;
+  const int shares = groups * a.L < 2 * a.num_sms ? min(passes, 16) : 1;
   auto* kernel = a.d == 64 ? (a.rope.interleaved ? rotary_kernel<64, true> : rotary_kernel<64, false>)
                            : (a.rope.interleaved ? rotary_kernel<128, true> : rotary_kernel<128, false>);
   return cache8::launch(kernel, dim3(static_cast<unsigned>(groups), shares, a.L), kThreads, 0, s, a,
-                        tokens, shares, cache8::make_div(heads));
+                        tokens, slots, cache8::make_div(slots));
 }
 
 }  // namespace prompt
