@@ -2,13 +2,14 @@
 // per unit the last and the first tokens and the heaviest of the others, in order.
 //
 // One CTA a unit.  The least weight that is kept is found by a radix select over
-// order-preserving 32-bit keys: a histogram of a digit's values in shared memory, the bin that
-// the wanted rank falls into, then the next digit of the keys in that bin, 11 bits a time.  The
-// first digit starts at the highest bit in which the unit's keys differ (a minimum and a
-// maximum), so that it tells them apart: with the sign and all of the exponent in it most keys
-// of a warp would add to a few bins.  What is left after it, a few percent, goes to a list that the
-// other digits come from.  Keys above the least one are kept, and of those equal to it
-// the first ones.
+// order-preserving 32-bit keys: a histogram of a digit of 11 bits in shared memory, and the bin
+// that the wanted rank falls into.  The first digit starts at the highest bit in which the unit's
+// keys differ (a minimum and a maximum), so that it tells them apart: with the sign and all of the
+// exponent in it most keys of a warp would add to a few bins.  What is left after it, a few percent,
+// goes to a list, whose keys are ranked by comparing each with each, or by further digits where
+// they are many.  Keys above the least one are kept, and of those equal to it the first ones.
+// (Two more digits over all keys took 9.6 and 16 us for 1112 and 1536 tokens, of what is 7.0 and 12
+// below; a first digit of 8 bits leaves too many to rank: 10 and 20 us.)
 //
 // Weights are read once and stay in registers, as keys: thread i has elements 4 (r NT + i) .. + 3 of round
 // r.  Places come from one scan of the counts, a byte a round, over the warp and one over the warps.
@@ -25,6 +26,7 @@ using cache8::before_all;
 constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kMaxRounds = 8;
 constexpr int kListed = 2048;  // keys that are left after the first digit, in shared memory
+constexpr int kRanked = 256;   // of them, that are compared each with each
 
 // Larger weight, larger key; NaN below all, -0 as 0.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -96,38 +98,41 @@ __device__ __forceinline__ int prefix(int v, int* s_warp, int* all) {
   return before + incl - v;
 }
 
-struct Shared {
+struct __align__(16) Shared {
   int hist[kBins];
   int warp[32];
   uint32_t low[32], high[32];
   int rounds[kMaxRounds * 32];
   uint32_t list[kListed];
   uint32_t prefix;
-  int want, same, listed;
+  int want, same, listed, ranked_want;
 };
 
-// Of the CTA's keys, which each(f) calls f with (and with zeros, which are none), between low and high (this thread's): the
-// want-th largest (want >= 1, there are as many) in *least, how many keys equal to it belong
-// to the want largest, and how many there are.
-template <class Each>
-__device__ __forceinline__ void select(Shared& s, Each each, uint32_t low, uint32_t high, int want,
-                                       uint32_t* least, int* equal, int* same) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+// The least and the largest of the CTA's values.  A barrier inside, and one owed before the next call.
+__device__ __forceinline__ void range(Shared& s, uint32_t& low, uint32_t& high) {
+  const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
   low = __reduce_min_sync(0xffffffffu, low);
   high = __reduce_max_sync(0xffffffffu, high);
-  if (lane == 0) s.low[warp] = low, s.high[warp] = high;
-  for (int i = threadIdx.x; i < kBins; i += blockDim.x) s.hist[i] = 0;
+  if (lane == 0) s.low[threadIdx.x / 32] = low, s.high[threadIdx.x / 32] = high;
   __syncthreads();
   low = __reduce_min_sync(0xffffffffu, lane < warps ? s.low[lane] : 0xffffffffu);
   high = __reduce_max_sync(0xffffffffu, lane < warps ? s.high[lane] : 0u);
+}
+
+// Of the CTA's keys, which each(f) calls f with (and with zeros, which are none), all of them
+// between low and high, and with s.hist zero: the want-th largest (want >= 1, there are as many) in
+// *least, how many keys equal to it belong to the want largest, and how many there are.
+template <class Each>
+__device__ __forceinline__ void select(Shared& s, Each each, uint32_t low, uint32_t high, int want,
+                                       uint32_t* least, int* equal, int* same) {
   uint32_t so_far = high;             // the bits above `rest` are the least key's
   int rest = 32 - __clz(low ^ high);  // bits that are not known yet
   *same = 0;
-  // the bin of digit `shift`, of `bits` bits, that the want-th key falls into
+  // the bin of the digit at `shift`, of `bits` bits, that the want-th key falls into
   auto settle = [&](int shift, int bits) {
     __syncthreads();
-    const int mask = (1 << bits) - 1;
     // thread i: the bins from mask - i per down, heaviest first
+    const int mask = (1 << bits) - 1;
     const int per = (mask + blockDim.x) / blockDim.x, first = mask - static_cast<int>(threadIdx.x) * per;
     int mine = 0, all;
     for (int i = 0; i < per && first - i >= 0; ++i) mine += s.hist[first - i];
@@ -146,8 +151,6 @@ __device__ __forceinline__ void select(Shared& s, Each each, uint32_t low, uint3
     want = s.want;
     *same = s.same;
     rest = shift;
-    if (rest > 0)
-      for (int i = threadIdx.x; i < kBins; i += blockDim.x) s.hist[i] = 0;
   };
   if (rest > 0) {
     const int bits = min(rest, kBits), shift = rest - bits;
@@ -155,16 +158,42 @@ __device__ __forceinline__ void select(Shared& s, Each each, uint32_t low, uint3
     each([&](uint32_t k) { count_if(k != 0, &s.hist[(k >> shift) & mask]); });
     settle(shift, bits);
   }
-  // What is left is few keys most often: they are listed then.
+  // What is left is few keys most often: they are listed, and ranked among one another if they
+  // are a few for each lane of a warp.
   const bool list = rest > 0 && *same <= kListed;
   const int n = *same;
-  if (list)
+  if (list) {
     each([&](uint32_t k) { list_if(k >> rest == so_far >> rest && k != 0, &s.listed, s.list, k); });
-  if (rest > 0) __syncthreads();
+    __syncthreads();
+    if (n <= kRanked) {
+      for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const uint32_t k = s.list[i];
+        int more = 0, alike = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+          const uint32_t other = s.list[j];
+          more += other > k;
+          alike += other == k;
+        }
+        if (more < want && more + alike >= want) {  // (all that are equal to it write the same)
+          s.prefix = k;
+          s.ranked_want = want - more;
+          s.same = alike;
+        }
+      }
+      __syncthreads();
+      *least = s.prefix;
+      *equal = s.ranked_want;
+      *same = s.same;
+      return;
+    }
+  }
   while (rest > 0) {
+    for (int i = threadIdx.x; i < kBins; i += blockDim.x) s.hist[i] = 0;
+    __syncthreads();
     const int bits = min(rest, kBits), shift = rest - bits;
     const uint32_t mask = (1u << bits) - 1;
-    auto count = [&](uint32_t k) {  // (in the list, or with the first digit, the top bits agree)
+    auto count = [&](uint32_t k) {
       count_if((k ^ so_far) >> shift <= mask && k != 0, &s.hist[(k >> shift) & mask]);
     };
     if (list)
@@ -172,7 +201,6 @@ __device__ __forceinline__ void select(Shared& s, Each each, uint32_t low, uint3
     else
       each(count);
     settle(shift, bits);
-    if (rest > 0) __syncthreads();
   }
   *least = so_far;
   *equal = want;
@@ -222,35 +250,39 @@ __global__ void __launch_bounds__(MaxThreads) heaviest_kernel(HeaviestArgs a) {
       for (int c = 0; c < 4; ++c) x[r][c] = t + c < p.len ? __float_as_uint(w[t + c]) : 0u;
     }
   }
-  uint32_t most = 0;
+  for (int i = threadIdx.x; i < kBins; i += NT) s.hist[i] = 0;
+  auto limits = [&](uint32_t& low, uint32_t& high) {  // of the keys (a zero less one is no minimum)
+    low = 0xffffffffu, high = 0;
 #pragma unroll
-  for (int r = 0; r < R; ++r) most = max(max(most, max(x[r][0], x[r][1])), max(x[r][2], x[r][3]));
-  // (-0 is the one negative value that must not be told apart from another)
-  const bool plain = !__syncthreads_or(most > 0x7f800000u);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) low = min(low, x[r][c] - 1), high = max(high, x[r][c]);
+    range(s, low, high);
+    ++low;
+  };
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int t0 = 4 * (r * NT + 32 * warp);  // the warp's elements are 128 from here on
+    if (t0 >= p.head && t0 + 128 <= p.tail) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[r][c] = min(x[r][c], 0xfffffffeu) + 1;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        x[r][c] = index(r) + c >= p.head && index(r) + c < p.tail ? min(x[r][c], 0xfffffffeu) + 1 : 0u;
+    }
+  }
+  uint32_t low, high;
+  limits(low, high);
+  const bool plain = high <= 0x7f800001u;  // (so for all threads)
   if (!plain) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[r][c] = key_of(__uint_as_float(x[r][c]));
-  }
-  uint32_t low = 0xffffffffu, high = 0;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) ++x[r][c];
-    const int t0 = 4 * (r * NT + 32 * warp);  // the warp's elements are 128 from here on
-    if (t0 >= p.head && t0 + 128 <= p.tail) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) low = min(low, x[r][c]), high = max(high, x[r][c]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const bool other = index(r) + c >= p.head && index(r) + c < p.tail;
-        if (!other) x[r][c] = 0;
-        low = min(low, other ? x[r][c] : 0xffffffffu);
-        high = max(high, x[r][c]);
-      }
-    }
+      for (int c = 0; c < 4; ++c)
+        if (x[r][c]) x[r][c] = key_of(__uint_as_float(x[r][c] - 1)) + 1;
+    __syncthreads();
+    limits(low, high);
   }
   // ---- the least key that is kept (all of them: 1) ----
   uint32_t least = p.want > 0 ? 1u : 0xffffffffu;
@@ -389,6 +421,8 @@ __global__ void __launch_bounds__(kStreamThreads) heaviest_stream_kernel(Heavies
       low = min(low, k);
       high = max(high, k);
     });
+    for (int i = threadIdx.x; i < kBins; i += kStreamThreads) s.hist[i] = 0;
+    range(s, low, high);
     select(s, each, low, high, p.want, &least, &equal, &same);
   }
   // (where weights_out is weights: a chunk is read before what it keeps is written, to
