@@ -17,7 +17,7 @@
 //   MMA (1 warp)      128 x 192 products into the tile's columns of TMEM, with the keys read
 //                     from there: from shared memory, keys, queries, copies and normalisers
 //                     together asked for more than its bandwidth (98 us with 128 columns a
-//                     product, 84 us with 256, of what is XX us below);
+//                     product, 84 us with 256, of what is 82 us below);
 //   weights (16 warps)  two warps a lane quarter and tile, a half of the columns each: scale,
 //                     exponential, sum.  One tile's exponentials run while the other's
 //                     products do.
@@ -632,15 +632,17 @@ cudaError_t launch_d(const Cache& c, const WeighArgs& a, cudaStream_t s) {
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  // Pairs of tiles that fill the GPU less than twice have their queries cut into parts, which a
-  // second launch adds up.  8 sequences of 1536 tokens, all queries (192 pairs): XX us uncut.
+  // Where there are few pairs of tiles, their queries are cut into parts of 8 chunks and more, for
+  // two items an SM, which a second launch adds up.  Prompts of 1536 tokens, whole and cut: 24
+  // pairs 82 and 24 us, 96 pairs 82 and 48, 192 pairs 85 and 82, but 288 pairs 105 and 113; and
+  // parts of less cost more than they save (64 queries, 192 pairs: 18 and 22 us).
   const int tokens = min(a.cap, c.max_blocks * c.bs);
   p.pairs = (tokens + 2 * kTile - 1) / (2 * kTile);
   const long long most = static_cast<long long>(c.L) * c.B * c.H * p.pairs;
   const int chunks = (a.n + p.tok - 1) / p.tok;
   p.parts = 1;
-  if (most < 2ll * a.num_sms)
-    p.parts = static_cast<int>(min(2ll * a.num_sms / most + 1, min(static_cast<long long>(chunks), 16ll)));
+  if (2 * most < 3ll * a.num_sms)
+    p.parts = static_cast<int>(max(1ll, min(2ll * a.num_sms / most + 1, min(chunks / 8ll, 16ll))));
   p.part = static_cast<float*>(a.workspace);
   const long long items = most * p.parts;
   const int grid = static_cast<int>(items < a.num_sms ? items : a.num_sms);
