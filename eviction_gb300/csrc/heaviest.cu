@@ -8,8 +8,15 @@
 // exponent in it most keys of a warp would add to a few bins.  What is left after it, a few percent,
 // goes to a list, whose keys are ranked by comparing each with each, or by further digits where
 // they are many.  Keys above the least one are kept, and of those equal to it the first ones.
-// (Two more digits over all keys took 9.6 and 16 us for 1112 and 1536 tokens, of what is 7.0 and 12
-// below; a first digit of 8 bits leaves too many to rank: 10 and 20 us.)
+// (For 64 x 8 units of 1112 tokens and 28 x 8 x 4 of 1536, with two more digits over all keys
+// instead of the list: 9.6 and 16 us, of 7.0 and 12; with a first digit of 8 bits, which leaves too
+// many to rank: 10 and 20.)
+//
+// The call reads weights once and writes them, and the budget's positions, once; instructions on
+// registers and on shared memory bound it, a scan, a digit and a ranking deep.  Measured: 6.1 us for
+// 64 x 8 x 1112 -> 512, 8.8 us for 28 x 8 x 4 x 1536 -> 1024, 58 us for 28 x 4 x 4 x 32768 -> 4096
+// (118 MB; the choice 17 us of them, places 6, what is kept 5, the zeros behind it 12).  A CTA that
+// takes units in turns with the next one's weights on their way to shared memory took 85 us there.
 //
 // Weights are read once and stay in registers, as keys: thread i has elements 4 (r NT + i) .. + 3 of round
 // r.  Places come from one scan of the counts, a byte a round, over the warp and one over the warps.
@@ -224,8 +231,8 @@ __device__ __forceinline__ void write_rest(const HeaviestArgs& a, const Plan& p,
 // Units of at most 4 R blockDim.x tokens.  Keys are above 0; 0 stands for what is kept anyway, or
 // not there.  Where no weight is negative or NaN, as sums of softmax weights are, a weight's bits
 // are its order and its key is these plus one: nothing to convert.
-template <int R, int MaxThreads>
-__global__ void __launch_bounds__(MaxThreads) heaviest_kernel(HeaviestArgs a) {
+template <int R, int MaxThreads, int MinCtas>
+__global__ void __launch_bounds__(MaxThreads, MinCtas) heaviest_kernel(HeaviestArgs a) {
   __shared__ Shared s;
   before_all();
   const int u = blockIdx.x, b = (u / a.H) % a.B;
@@ -458,10 +465,13 @@ cudaError_t launch_heaviest(const HeaviestArgs& a, cudaStream_t s) {
     const int n = (a.cap + 4 * rounds - 1) / (4 * rounds);
     return (n + 31) / 32 * 32;
   };
-  if (a.cap <= 2048) return cache8::launch(heaviest_kernel<1, 512>, grid, threads(1), 0, s, a);
-  if (a.cap <= 4096) return cache8::launch(heaviest_kernel<2, 512>, grid, threads(2), 0, s, a);
-  if (a.cap <= 8192) return cache8::launch(heaviest_kernel<4, 512>, grid, threads(4), 0, s, a);
-  if (a.cap <= 32768) return cache8::launch(heaviest_kernel<8, 1024>, grid, threads(8), 0, s, a);
+  // Few registers, so that an SM has several units under way (28 x 8 x 4 units of 1536, 4096 and
+  // 8192 tokens: 8.8, 15.2 and 25.7 us, of 12.3, 19.6 and 27.4 without a limit to registers).  The
+  // stream kernel takes more than twice as long wherever registers hold a unit (16384 tokens: 70 us
+  // and 31, 32768: 132 and 58).
+  if (a.cap <= 2048) return cache8::launch(heaviest_kernel<2, 256, 5>, grid, threads(2), 0, s, a);
+  if (a.cap <= 8192) return cache8::launch(heaviest_kernel<4, 512, 3>, grid, threads(4), 0, s, a);
+  if (a.cap <= 32768) return cache8::launch(heaviest_kernel<8, 1024, 1>, grid, threads(8), 0, s, a);
   return cache8::launch(heaviest_stream_kernel, grid, kStreamThreads, 0, s, a);
 }
 
