@@ -15,7 +15,7 @@
 // The call reads weights once and writes them, and the budget's positions, once; instructions on
 // registers and on shared memory bound it, a scan, a digit and a ranking deep.  Measured: 6.1 us for
 // 64 x 8 x 1112 -> 512, 8.8 us for 28 x 8 x 4 x 1536 -> 1024, 58 us for 28 x 4 x 4 x 32768 -> 4096
-// (118 MB; the choice 17 us of them, places 6, what is kept 5, the zeros behind it 12).  A CTA that
+// (125 MB; the choice 17 us of them, places 6, what is kept 5, the zeros behind it 12).  A CTA that
 // takes units in turns with the next one's weights on their way to shared memory took 85 us there.
 //
 // Weights are read once and stay in registers, as keys: thread i has elements 4 (r NT + i) .. + 3 of round

@@ -8,9 +8,9 @@
 // it and a group's keys are read once.  A CTA has two such tiles, of consecutive tokens,
 // and takes 128 keys and values at a time for both:
 //   load (1 warp)     Q, K and V by TMA, keys and values through a ring of stages;
-//   MMA (1 warp)      S = Q K^T (128 x 128, in TMEM), then O += P V with P read from TMEM,
-//                     where it has taken the place of S; the tiles take turns, so that one
-//                     tile's products run during the other's softmax;
+//   MMA (2 warps)     a warp a tile: S = Q K^T (128 x 128, in TMEM), then O += P V with P read
+//                     from TMEM, where it has taken the place of S; the tiles take turns, so
+//                     that one tile's products run during the other's softmax;
 //   softmax (4 + 4 warps)  one thread a row: weights, their sum in fp32, P to TMEM as bf16,
 //                     and at the end the row's result;
 //   items (1 warp)    which tiles come next, a few ahead of the others.
@@ -20,7 +20,12 @@
 // its first tile's largest logit, moves only when a later one passes it by 2^32 (and O is
 // scaled then, by the softmax warps themselves).  The maximum comes with the TMEM load.
 //
-// The arithmetic bounds this: 4 d operations a pair of tokens and head.  The last tile of
+// The arithmetic bounds this: 4 d operations a pair of tokens and head.  Measured, d = 128: one
+// sequence of 16384 tokens, 28 heads, 1.2 ms (1600 TFLOP/s; a step of both tiles 2900 cycles, its
+// 32 products alone 2048: S = Q K^T reads both operands at all of shared memory's bandwidth, beside
+// the copies); 16 sequences of 612 to 1112 tokens, 32 heads, 106 us, a quarter of it the changes of
+// items (a result written beside the next item's products slows those more than it hides: 111 us).
+// The last tile of
 // keys is cut to the columns (steps of 16) that some row of the tile sees, in both products.
 // Rows of V behind a sequence's end are zeroed in shared memory first (their weights are
 // 0, and what stands there need not be finite).

@@ -11,10 +11,15 @@
 // The list of all heads' steps is cut into equal stretches, one a warp, whatever the lengths
 // are.  A warp has a ring of stages in shared memory, filled by bulk copies of the rows that
 // lie side by side in a block, two steps ahead; blocks are looked up a step ahead of the
-// copies, and a next head's queries are on their way one step before they are needed.  Per 16 tokens a warp computes S^T = K Q^T
-// (m16n8k16, tokens on the M axis, 8 NT query rows), with the codes converted to fp16, which
-// holds both formats exactly, and a query row divided by a power of two that its largest
-// magnitude brings to [1, 4).
+// copies, and a next head's queries are on their way one step before they are needed.  Per 16
+// tokens a warp computes S^T = K Q^T (m16n8k16, tokens on the M axis, 8 NT query rows), with
+// the codes converted to fp16, which holds both formats exactly, and a query row divided by a
+// power of two that its largest magnitude brings to [1, 4).
+//
+// Measured: 64 sequences of 612 to 1112 tokens, 8 heads of 128 (e4m3, 61 MB) 15.5 us, 4 of 32768,
+// 4 heads (int8, 71 MB) 16 us, of which launch, the first copies' latency and the last stretch's end
+// are 6 us.  Up to 32 query rows: the other kernel takes 54 us for 12 to 32 rows of the former, this
+// one 19 to 28.
 #include "weigh.cuh"
 
 namespace kvc {
