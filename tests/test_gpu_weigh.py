@@ -211,6 +211,50 @@ def test_weigh_same_bits_twice_and_replayed():
         assert torch.equal(w, a)
 
 
+@pytest.mark.parametrize("d,fmt", [(64, "int8"), (128, "e4m3")])
+def test_weigh_long_pieces_of_few_heads(d, fmt):
+    """Few pairs of tiles and many queries: their queries are cut into parts, which are added up."""
+    lens = [520, 0, 300, 257]
+    p = Weigh(2, 4, 1, d, 16, 33, fmt, G=16, max_T=64, window=1)
+    p.fill(lens)
+    for n_q, packed, decay in ((lens, True, 0.5), (lens, False, 1.0), ([400, 0, 7, 256], False, 0.0),
+                               ([200, 0, 0, 1], True, 1.0)):
+        p.prepare(max(n_q), n_q, packed=packed)
+        p.run(decay)
+        p.check(decay)
+    p.prepare(520, lens)
+    p.c.table[0, 3] = 10 ** 6
+    p.c.table[3, 16] = -1
+    absent = np.zeros((4, 528), bool)
+    absent[0, 48:64] = True
+    absent[3, 256:] = True
+    p.run(0.5)
+    p.check(0.5, status=2, absent=absent)
+
+
+def test_weigh_parts_of_two_captured_calls():
+    """Two graphs whose parts lie in the same workspace, replayed in turn and in the other order."""
+    p = Weigh(1, 2, 1, 128, 16, 20, "int8", G=16, max_T=64, window=1)
+    p.fill([300, 280])
+    calls = []
+    for n in (280, 200):
+        p.prepare(n)
+        want = p.run().clone()
+        w, graph, stream = p.old.clone(), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream), torch.cuda.graph(graph, stream=stream):
+            p.h.cache8_weigh(p.c, p.q, p.lse, w)
+        calls.append((graph, w, p.old.clone(), want, p.q, p.lse))
+    for order in ((0, 1), (1, 0, 0)):
+        for i in order:
+            calls[i][1].copy_(calls[i][2])
+            calls[i][0].replay()
+        torch.cuda.synchronize()
+        for i in order:
+            assert torch.equal(calls[i][1], calls[i][3])
+    assert p.h.device_status() == 0
+
+
 def test_weigh_refuses():
     import eviction_gb300 as kvc
     p = Weigh(1, 2, 2, 64, 16, 8, "e4m3", G=2, max_T=64, window=1)
