@@ -13,9 +13,9 @@
 // many to rank: 10 and 20.)
 //
 // The call reads weights once and writes them, and the budget's positions, once; instructions on
-// registers and on shared memory bound it, a scan, a digit and a ranking deep.  Measured: 6.1 us for
-// 64 x 8 x 1112 -> 512, 8.8 us for 28 x 8 x 4 x 1536 -> 1024, 58 us for 28 x 4 x 4 x 32768 -> 4096
-// (125 MB; the choice 17 us of them, places 6, what is kept 5, the zeros behind it 12).  A CTA that
+// registers and on shared memory bound it, a scan, a digit and a ranking deep.  Measured: 6.0 us for
+// 64 x 8 x 1112 -> 512, 8.8 us for 28 x 8 x 4 x 1536 -> 1024, 56 us for 28 x 4 x 4 x 32768 -> 4096
+// (125 MB; the choice 17 us of them, places 6, what is kept 5, the zeros behind it 10, by stores or by bulk copies).  A CTA that
 // takes units in turns with the next one's weights on their way to shared memory took 85 us there.
 //
 // Weights are read once and stay in registers, as keys: thread i has elements 4 (r NT + i) .. + 3 of round
@@ -257,6 +257,11 @@ __global__ void __launch_bounds__(MaxThreads, MinCtas) heaviest_kernel(HeaviestA
       for (int c = 0; c < 4; ++c) x[r][c] = t + c < p.len ? __float_as_uint(w[t + c]) : 0u;
     }
   }
+  // (what does not depend on the choice is written while the weights are on their way, unless
+  // it lies in their place)
+  int32_t* kept = a.kept + static_cast<size_t>(u) * a.budget;
+  float* out = a.out + static_cast<size_t>(u) * a.cap;
+  if (out != w) write_rest(a, p, u, kept, out);
   for (int i = threadIdx.x; i < kBins; i += NT) s.hist[i] = 0;
   auto limits = [&](uint32_t& low, uint32_t& high) {  // of the keys (a zero less one is no minimum)
     low = 0xffffffffu, high = 0;
@@ -364,8 +369,6 @@ __global__ void __launch_bounds__(MaxThreads, MinCtas) heaviest_kernel(HeaviestA
     }
   }
   places();  // (all weights of others are read)
-  int32_t* kept = a.kept + static_cast<size_t>(u) * a.budget;
-  float* out = a.out + static_cast<size_t>(u) * a.cap;
   if (!plain) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(MaxThreads, MinCtas) heaviest_kernel(HeaviestA
     }
     __syncthreads();
   }
-  write_rest(a, p, u, kept, out);
+  if (out == w) write_rest(a, p, u, kept, out);
 }
 
 // Units of any length.
@@ -468,7 +471,7 @@ cudaError_t launch_heaviest(const HeaviestArgs& a, cudaStream_t s) {
   // Few registers, so that an SM has several units under way (28 x 8 x 4 units of 1536, 4096 and
   // 8192 tokens: 8.8, 15.2 and 25.7 us, of 12.3, 19.6 and 27.4 without a limit to registers).  The
   // stream kernel takes more than twice as long wherever registers hold a unit (16384 tokens: 70 us
-  // and 31, 32768: 132 and 58).
+  // and 31, 32768: 132 and 56).
   if (a.cap <= 2048) return cache8::launch(heaviest_kernel<2, 256, 5>, grid, threads(2), 0, s, a);
   if (a.cap <= 8192) return cache8::launch(heaviest_kernel<4, 512, 3>, grid, threads(4), 0, s, a);
   if (a.cap <= 32768) return cache8::launch(heaviest_kernel<8, 1024, 1>, grid, threads(8), 0, s, a);

@@ -45,7 +45,7 @@ struct WeighArgs {
   int num_sms;
   void* workspace;  // weigh_workspace() bytes
 };
-// (cut items are fewer than two a SM, their parts fewer than four, of 256 tokens each)
+// (what is cut is fewer than 1.5 pairs of tiles an SM, in fewer than 3.5 parts, of 256 tokens each)
 constexpr size_t weigh_workspace(int num_sms) { return static_cast<size_t>(num_sms) * 4 * 256 * sizeof(float); }
 cudaError_t launch_weigh(const cache8::Cache& c, int format, const WeighArgs& a, cudaStream_t s);
 
