@@ -49,8 +49,9 @@ cudaError_t launch_grow(const Cache& c, const int32_t* n_new, cudaStream_t s);
 cudaError_t launch_free(const Cache& c, int n, const int32_t* seqs, cudaStream_t s);
 cudaError_t launch_fork(const Cache& c, int n, const int32_t* src, const int32_t* dst,
                         int num_sms, cudaStream_t s);
+// row0: first row of each sequence (their seq stride is 0 then), or nullptr
 cudaError_t launch_append(const Cache& c, int format, const Rows& k, const Rows& v, int n,
-                          const int32_t* n_new, cudaStream_t s);
+                          const int32_t* row0, const int32_t* n_new, cudaStream_t s);
 cudaError_t launch_gather(const Cache& c, int format, int T, uint16_t* k_out, uint16_t* v_out,
                           int32_t* pad, cudaStream_t s);
 cudaError_t launch_compact(const Cache& src, int src_format, const Cache& dst, int dst_format,

@@ -65,6 +65,25 @@ kvc::cache8::Rows rows(const kvc_rows& r) {
   return {r.data, r.layer, r.seq, r.head, r.token};
 }
 
+// Both forms of append: `seqs` sequences of n rows each, or all among n rows, from row0[b] on.
+int append(kvc_handle* h, const kvc_cache8* c, const kvc_rows* k, const kvc_rows* v, int n, int seqs,
+           const int32_t* row0, const int32_t* n_new, void* stream) {
+  KVC_TRY(check(h, c));
+  if (n < 1) return fail(h, KVC_ERR_SHAPE, "n must be >= 1");
+  KVC_TRY(check_rows(h, k, "k", false, c->n_layers, seqs, h->dims.H, n));
+  KVC_TRY(check_rows(h, v, "v", false, c->n_layers, seqs, h->dims.H, n));
+  KVC_REQUIRE_INTS(n_new);
+  const long long units = static_cast<long long>(c->n_layers) * h->dims.B * h->dims.H;
+  const long long most = std::min<long long>(n, static_cast<long long>(c->max_blocks) * c->block_size);
+  if (units > INT_MAX / ((most + c->block_size - 2) / c->block_size + 1))
+    return fail(h, KVC_ERR_UNSUPPORTED, "too many blocks to write in one call");
+  kvc::cache8::Rows kr = rows(*k), vr = rows(*v);
+  if (row0) kr.seq = vr.seq = 0;
+  return run(h, kvc::kKernelCache8Append, "cache8 append", stream, [&](cudaStream_t s) {
+    return kvc::cache8::launch_append(view(h, *c), c->format, kr, vr, n, row0, n_new, s);
+  });
+}
+
 }  // namespace
 
 extern "C" {
@@ -98,19 +117,15 @@ int kvc_cache8_grow(kvc_handle* h, const kvc_cache8* c, const int32_t* n_new, vo
 int kvc_cache8_append(kvc_handle* h, const kvc_cache8* c, const kvc_rows* k, const kvc_rows* v,
                       int n, const int32_t* n_new, void* stream) {
   if (!h) return KVC_ERR_ARG;
+  return guarded([&] { return append(h, c, k, v, n, h->dims.B, nullptr, n_new, stream); });
+}
+
+int kvc_cache8_append_packed(kvc_handle* h, const kvc_cache8* c, const kvc_rows* k, const kvc_rows* v,
+                             int n, const int32_t* first, const int32_t* n_new, void* stream) {
+  if (!h) return KVC_ERR_ARG;
   return guarded([&] {
-    KVC_TRY(check(h, c));
-    if (n < 1) return fail(h, KVC_ERR_SHAPE, "n must be >= 1");
-    KVC_TRY(check_rows(h, k, "k", false, c->n_layers, h->dims.B, h->dims.H, n));
-    KVC_TRY(check_rows(h, v, "v", false, c->n_layers, h->dims.B, h->dims.H, n));
-    KVC_REQUIRE_INTS(n_new);
-    const long long units = static_cast<long long>(c->n_layers) * h->dims.B * h->dims.H;
-    const long long most = std::min<long long>(n, static_cast<long long>(c->max_blocks) * c->block_size);
-    if (units > INT_MAX / ((most + c->block_size - 2) / c->block_size + 1))
-      return fail(h, KVC_ERR_UNSUPPORTED, "too many blocks to write in one call");
-    return run(h, kvc::kKernelCache8Append, "cache8 append", stream, [&](cudaStream_t s) {
-      return kvc::cache8::launch_append(view(h, *c), c->format, rows(*k), rows(*v), n, n_new, s);
-    });
+    KVC_REQUIRE_INTS(first);
+    return append(h, c, k, v, n, 1, first, n_new, stream);
   });
 }
 

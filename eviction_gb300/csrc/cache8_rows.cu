@@ -105,7 +105,8 @@ __device__ __forceinline__ int exp_of(float scale) {
 // registers for 6 CTAs on an SM: 4000 tokens to 8 sequences of 8 heads 39 us, 41 with 82.)
 template <int D, int FMT>
 __global__ void __launch_bounds__(32 * kWarps, 6)
-    append_kernel(Cache c, Rows k_new, Rows v_new, int n, int per_seq, const int32_t* n_new) {
+    append_kernel(Cache c, Rows k_new, Rows v_new, int n, int per_seq, const int32_t* row0,
+                  const int32_t* n_new) {
   constexpr int CH = D / 8;  // 16-byte chunks of a bf16 row
   before_all();
   const int lane = threadIdx.x % 32;
@@ -117,10 +118,10 @@ __global__ void __launch_bounds__(32 * kWarps, 6)
   const uint32_t t2 = t1 / per_seq;
   const int b = t2 % c.B, l = t2 / c.B;
   if (l >= c.L) return;
-  const int nn = n_new[b];
+  const int nn = n_new[b], at = row0 ? row0[b] : 0;  // the sequence's first row
   bool bad = false;
   const int len = length_of(c, b, &bad);
-  if (bad || nn < 0 || nn > n || nn > len) {
+  if (bad || nn < 0 || at < 0 || nn > n - at || nn > len) {
     if (lane == 0) report(c, KVC_STATUS_BAD_INDEX);
     return;
   }
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(32 * kWarps, 6)
   const int first = i * c.bs;
   const int lo = max(first, start), hi = min(len, first + c.bs);
   const bool values = blockIdx.y != 0;
-  const uint16_t* x = values ? v_new.at(l, b, h, lo - start) : k_new.at(l, b, h, lo - start);
+  const uint16_t* x = values ? v_new.at(l, b, h, at + lo - start) : k_new.at(l, b, h, at + lo - start);
   const long long stride = values ? v_new.token : k_new.token;
   const int total = (hi - lo) * CH;
   auto load = [&](int idx) {
@@ -423,7 +424,7 @@ int ctas(long long tasks) { return static_cast<int>((tasks + kWarps - 1) / kWarp
 }  // namespace
 
 cudaError_t launch_append(const Cache& c, int format, const Rows& k, const Rows& v, int n,
-                          const int32_t* n_new, cudaStream_t s) {
+                          const int32_t* row0, const int32_t* n_new, cudaStream_t s) {
   const int most = min(n, c.max_blocks * c.bs);  // a sequence has no more new tokens than that
   const int per_seq = (most - 1 + c.bs - 1) / c.bs + 1;  // blocks that they can touch
   const dim3 grid(ctas(static_cast<long long>(c.L) * c.B * c.H * per_seq), 2);
@@ -431,7 +432,7 @@ cudaError_t launch_append(const Cache& c, int format, const Rows& k, const Rows&
                                                         : append_kernel<64, KVC_CACHE8_INT8>)
                            : (format == KVC_CACHE8_E4M3 ? append_kernel<128, KVC_CACHE8_E4M3>
                                                         : append_kernel<128, KVC_CACHE8_INT8>);
-  return launch(kernel, grid, 32 * kWarps, 0, s, c, k, v, n, per_seq, n_new);
+  return launch(kernel, grid, 32 * kWarps, 0, s, c, k, v, n, per_seq, row0, n_new);
 }
 
 cudaError_t launch_gather(const Cache& c, int format, int T, uint16_t* k_out, uint16_t* v_out,

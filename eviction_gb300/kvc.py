@@ -25,7 +25,8 @@ ENTRY_POINTS = ("kvc_default_config", "kvc_create", "kvc_destroy", "kvc_stage_si
                 "kvc_event_host", "kvc_mass_select", "kvc_cache8_check", "kvc_cache8_grow",
                 "kvc_cache8_append", "kvc_cache8_attend", "kvc_cache8_gather",
                 "kvc_cache8_compact", "kvc_cache8_fork", "kvc_cache8_free", "kvc_rope_init",
-                "kvc_rotary", "kvc_prompt_attend", "kvc_cache8_weigh", "kvc_keep_heaviest")
+                "kvc_rotary", "kvc_prompt_attend", "kvc_cache8_append_packed", "kvc_cache8_weigh",
+                "kvc_keep_heaviest")
 
 STATUS = {0: "KVC_OK", -1: "KVC_ERR_ARG", -2: "KVC_ERR_SHAPE", -3: "KVC_ERR_ALIGN",
           -4: "KVC_ERR_NOMEM", -5: "KVC_ERR_CUDA", -6: "KVC_ERR_DEVICE", -7: "KVC_ERR_TIMEOUT",
@@ -192,6 +193,7 @@ def load_library():
     L.kvc_cache8_check.argtypes = [ctypes.POINTER(_CConfig), _P, ctypes.POINTER(ctypes.c_char_p)]
     L.kvc_cache8_grow.argtypes = [_P] * 4
     L.kvc_cache8_append.argtypes = [_P, _P, _P, _P, _I, _P, _P]
+    L.kvc_cache8_append_packed.argtypes = [_P, _P, _P, _P, _I, _P, _P, _P]
     L.kvc_cache8_attend.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P]
     L.kvc_cache8_gather.argtypes = [_P, _P, _I, _P, _P, _P, _P]
     L.kvc_cache8_compact.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P, _P, _P]
@@ -540,10 +542,13 @@ class Handle:
             self._h, self._cache8(cache), self._ints(n_new, "n_new", (cache.batch,), cache.device),
             self._stream(stream)), "kvc_cache8_grow")
 
-    def cache8_append(self, cache, k, v, n_new, stream=None):
+    def cache8_append(self, cache, k, v, n_new, stream=None, first=None):
         """kvc_cache8_append: quantise the newest tokens' rows k, v [L, B, H, n, d] bf16 (any
-        strides) into their blocks; n_new [B] int32 of them for each sequence."""
+        strides) into their blocks; n_new [B] int32 of them for each sequence.  Packed, with
+        first [B] int32 (kvc_cache8_append_packed): k, v [L, H, n, d]."""
         ref = self._cache8(cache)
+        if first is not None:
+            return self._append_packed(cache, ref, k, v, n_new, first, stream)
         n = k.shape[3] if k.dim() == 5 else 0
         shape = (cache.n_layers, cache.batch, cache.n_kv_heads, n, cache.head_dim)
         self._check(load_library().kvc_cache8_append(
@@ -638,6 +643,15 @@ class Handle:
             self._dense(lse, torch.float32, "lse", shape[:-1]), decay,
             self._dense(weights, torch.float32, "weights", (L, B, H, cap)), cap,
             self._stream(stream)), "kvc_cache8_weigh")
+
+    def _append_packed(self, cache, ref, k, v, n_new, first, stream):
+        i32, B = self._torch.int32, cache.batch
+        n = k.shape[2] if k.dim() == 4 else 0
+        shape = (cache.n_layers, cache.n_kv_heads, n, cache.head_dim)
+        self._check(load_library().kvc_cache8_append_packed(
+            self._h, ref, self._strided(k, "k", shape, None), self._strided(v, "v", shape, None), n,
+            self._dense(first, i32, "first", (B,)), self._dense(n_new, i32, "n_new", (B,)),
+            self._stream(stream)), "kvc_cache8_append_packed")
 
     # -- prompts ---------------------------------------------------------------
     # (These calls may be a few microseconds on the GPU, so that their checks count: a tensor that is

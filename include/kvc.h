@@ -473,6 +473,13 @@ int kvc_cache8_grow(kvc_handle* h, const kvc_cache8* c, const int32_t* n_new, vo
 int kvc_cache8_append(kvc_handle* h, const kvc_cache8* c, const kvc_rows* k, const kvc_rows* v,
                       int n, const int32_t* n_new, void* stream);
 
+/* The same from packed rows, as kvc_prompt_attend takes them: k, v [n_layers][H][n][d] (the
+ * strides' seq is not used), the new tokens of sequence b are rows first[b] .. first[b] +
+ * n_new[b] - 1 of all n.  first [B] int32; a sequence that does not lie within the n rows is
+ * skipped (BAD_INDEX). */
+int kvc_cache8_append_packed(kvc_handle* h, const kvc_cache8* c, const kvc_rows* k, const kvc_rows* v,
+                             int n, const int32_t* first, const int32_t* n_new, void* stream);
+
 /* Attention of the newest tokens' queries over the cache:
  *   out_j = sum_t softmax_t(scale q_j . k_t) v_t over t <= seq_len[b] - n_q[b] + j,
  * for the H*G query heads (head h*G+g reads KV head h); scale is the
@@ -590,8 +597,8 @@ int kvc_cache8_free(kvc_handle* h, const kvc_cache8* c, int n, const int32_t* se
 
 /* ---- prompts: rotary positions and attention ------------------------------
  * How a prompt gets into a cache: kvc_rotary turns its queries and keys by their
- * positions, kvc_prompt_attend is the attention of all its tokens, kvc_cache8_append
- * quantises its keys and values. */
+ * positions, kvc_prompt_attend is the attention of all its tokens, kvc_cache8_append (or
+ * _append_packed) quantises its keys and values. */
 
 /* Rotary positions.  Pair i of a row's first dim values, (x, y), is turned by
  * pos * f_i: (x cos - y sin, x sin + y cos), times magnitude; i = 0 .. dim/2 - 1.  The

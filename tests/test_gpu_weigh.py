@@ -298,6 +298,61 @@ def _choose(w, lens, budget, n_sink=4, n_recent=64, max_T=None, in_place=False):
     return kept, n_kept, out, h.device_status()
 
 
+@pytest.mark.parametrize("d,fmt,bs", [(64, "e4m3", 16), (128, "int8", 8), (128, "e4m3", 128)])
+def test_packed_rows_are_appended_as_padded_ones(d, fmt, bs):
+    """Packed and padded appends leave the same bytes; rows of no sequence are not read."""
+    B, H, M = 4, 3, -(-210 // bs)
+    pair = [Weigh(2, B, H, d, bs, M, fmt, seed=7, max_T=64, window=1) for _ in range(2)]
+    rng = np.random.default_rng(3)
+    for counts in ([37, 0, 1, 100], [1, 1, 1, 1], [90, 64, 0, 9]):
+        first = list(np.cumsum([1] + [m + 2 for m in counts[:-1]]))
+        n = int(first[-1]) + counts[-1] + 3
+        rows = [_bf(rng, (2, n, 2 * H, d), 3.0)[:, :, w * H:(w + 1) * H].transpose(1, 2) for w in (0, 1)]
+        inside = torch.zeros(n, dtype=torch.bool, device="cuda")
+        padded = [torch.full((2, B, H, max(counts), d), math.nan, dtype=torch.bfloat16, device="cuda") for _ in rows]
+        for b, m in enumerate(counts):
+            inside[first[b]:first[b] + m] = True
+            for x, y in zip(rows, padded):
+                y[:, b, :, :m] = x[:, :, first[b]:first[b] + m]
+        for x in rows:
+            x.masked_fill_(~inside[None, None, :, None], math.nan)
+        for p in pair:
+            p.h.cache8_grow(p.c, _ints(counts))
+        pair[0].h.cache8_append(pair[0].c, *rows, _ints(counts), first=_ints(first))
+        pair[1].h.cache8_append(pair[1].c, *padded, _ints(counts))
+        for name in ("k_pool", "v_pool", "k_scale", "v_scale"):
+            a, b = (getattr(p.c, name).view(torch.uint8) for p in pair)
+            assert torch.equal(a, b), name
+        assert [p.h.device_status() for p in pair] == [0, 0]
+
+
+def test_packed_rows_out_of_range_are_skipped_and_refused():
+    import eviction_gb300 as kvc
+    p = Weigh(1, 4, 1, 64, 16, 4, "e4m3", max_T=64, window=1)
+    counts = _ints([5, 5, 5, 5])
+    p.h.cache8_grow(p.c, counts)
+    x = _bf(np.random.default_rng(1), (1, 1, 30, 64))
+    old = p.c.k_pool.view(torch.uint8).clone()
+    p.h.cache8_append(p.c, x, x, counts, first=_ints([26, -1, 2 ** 31 - 1, 25]))
+    assert p.h.device_status() == 2
+    blocks = p.c.table[:, 0].long()
+    now = p.c.k_pool.view(torch.uint8)
+    for b in range(3):
+        assert torch.equal(now[0, blocks[b]], old[0, blocks[b]])
+    want = p.c.k_pool.float()[0, blocks[3], 0, :5] * p.c.k_scale[0, blocks[3], 0]
+    assert ((want - x[0, 0, 25:].float()).abs() <= 2.0 ** -4 * x[0, 0, 25:].float().abs() + 2.0 ** -10).all()
+    now = now.clone()
+    with pytest.raises(ValueError):
+        p.h.cache8_append(p.c, x[None], x[None], counts, first=_ints([0, 5, 10, 15]))
+    with pytest.raises(ValueError):
+        p.h.cache8_append(p.c, x, x, counts, first=_ints([0, 5, 10]))
+    with pytest.raises(TypeError):
+        p.h.cache8_append(p.c, x, x, counts, first=counts.long())
+    with pytest.raises(kvc.KvcError):
+        p.h.cache8_append(p.c, x[..., :0, :], x[..., :0, :], counts, first=_ints([0, 0, 0, 0]))
+    assert torch.equal(p.c.k_pool.view(torch.uint8), now) and p.h.device_status() == 0
+
+
 def _check_choice(w, lens, budget, n_sink=4, n_recent=64, **kw):
     for in_place in (False, True):
         kept, n_kept, out, status = _choose(w, lens, budget, n_sink, n_recent, in_place=in_place, **kw)
@@ -418,7 +473,10 @@ def test_prompt_to_eviction(packed):
             got, gl = (out[g, at:at + m], lse[g, at:at + m]) if packed else (out[b, g, :m], lse[b, g, :m])
             assert ((got.double() - o).abs() <= tol).all() and ((gl.double() - l).abs() <= ltol).all()
     h.cache8_grow(cache, n_tok)
-    h.cache8_append(cache, k[None], v[None], n_tok)
+    if packed:
+        h.cache8_append(cache, pk[None], pv[None], n_tok, first=first)
+    else:
+        h.cache8_append(cache, k[None], v[None], n_tok)
     weights = torch.zeros((L, B, H, cap), device="cuda")
     if packed:
         h.cache8_weigh(cache, pq[None], lse[None], weights, n_q=n_tok, first=first)

@@ -86,6 +86,10 @@ def test_null_arguments(lib):
     assert lib.kvc_keep_heaviest(None, None, 1, 1, None, None, None, None, None) == -1
 
 
+def test_packed_append_without_a_handle(lib):
+    assert lib.kvc_cache8_append_packed(None, None, None, None, 1, None, None, None) == -1
+
+
 def test_plain_rotation_is_a_rotation():
     g = torch.Generator().manual_seed(0)
     x = torch.randn((3, 5, 64), generator=g, dtype=torch.float64)
