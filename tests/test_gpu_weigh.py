@@ -211,6 +211,20 @@ def test_weigh_same_bits_twice_and_replayed():
         assert torch.equal(w, a)
 
 
+@pytest.mark.parametrize("n", [1, 40])
+def test_weigh_many_sequences(n):
+    """More sequences than are sorted by their lengths: groups of several."""
+    B = 270
+    lens = [(37 * b) % 71 for b in range(B)]
+    lens[200] = 300
+    p = Weigh(1, B, 1, 64, 16, 19, "e4m3", n_blocks=1300, G=1, max_T=64, window=1)
+    p.fill(lens)
+    for packed in (False, True):
+        p.prepare(n, [min(n, m) for m in lens], packed=packed)
+        p.run(0.5)
+        p.check(0.5)
+
+
 @pytest.mark.parametrize("d,fmt", [(64, "int8"), (128, "e4m3")])
 def test_weigh_long_pieces_of_few_heads(d, fmt):
     """Few pairs of tiles and many queries: their queries are cut into parts, which are added up."""
