@@ -352,8 +352,11 @@ class Handle:
             raise KvcError(rc, "kvc_create failed")
         self._h = h
         import torch
-        self._torch = torch
         self._device = torch.device("cuda", torch.cuda.current_device())
+        # (looked up once: the checks of a short call take longer than its kernel)
+        self._index = self._device.index
+        self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
 
     # -- helpers -------------------------------------------------------------
     def _check(self, rc, what):
@@ -497,8 +500,7 @@ class Handle:
         a 5 us call)."""
         if stream is not None:
             return stream.cuda_stream
-        import torch
-        return torch._C._cuda_getCurrentRawStream(self._device.index)
+        return self._raw_stream(self._index)
 
     def _cache8(self, cache, name="cache"):
         if not isinstance(cache, Cache8):
@@ -630,7 +632,7 @@ class Handle:
         """kvc_cache8_weigh: weights [L, B, H, cap] fp32 (in place) gather what the newest tokens'
         queries give them.  q [L, B, H*G, n, d] bf16 (any strides), lse [L, B, H*G, n] fp32, n_q
         [B] int32 or None; packed, with first [B] int32: q [L, H*G, n, d], lse [L, H*G, n]."""
-        ref, torch = self._cache8(cache), self._torch
+        ref, i32 = self._cache8(cache), self._i32
         L, B, H = cache.n_layers, cache.batch, cache.n_kv_heads
         seqs = () if first is not None else (B,)
         n = q.shape[-2] if q.dim() == 4 + len(seqs) else 0
@@ -638,14 +640,14 @@ class Handle:
         cap = weights.shape[-1] if weights.dim() == 4 else 0
         self._check(load_library().kvc_cache8_weigh(
             self._h, ref, self._strided(q, "q", shape, 1 if seqs else None), n,
-            None if first is None else self._dense(first, torch.int32, "first", (B,)),
-            None if n_q is None else self._dense(n_q, torch.int32, "n_q", (B,)),
-            self._dense(lse, torch.float32, "lse", shape[:-1]), decay,
-            self._dense(weights, torch.float32, "weights", (L, B, H, cap)), cap,
+            None if first is None else self._dense(first, i32, "first", (B,)),
+            None if n_q is None else self._dense(n_q, i32, "n_q", (B,)),
+            self._dense(lse, self._f32, "lse", shape[:-1]), decay,
+            self._dense(weights, self._f32, "weights", (L, B, H, cap)), cap,
             self._stream(stream)), "kvc_cache8_weigh")
 
     def _append_packed(self, cache, ref, k, v, n_new, first, stream):
-        i32, B = self._torch.int32, cache.batch
+        i32, B = self._i32, cache.batch
         n = k.shape[2] if k.dim() == 4 else 0
         shape = (cache.n_layers, cache.n_kv_heads, n, cache.head_dim)
         self._check(load_library().kvc_cache8_append_packed(
@@ -659,10 +661,9 @@ class Handle:
     def _strided(self, t, name, shape, seq_axis, layer_axis=0):
         """kvc_rows of a bf16 tensor of `shape`, (..., heads, n, d), of any strides, d contiguous;
         the axes of layers and sequences, None where there is none."""
-        torch = self._torch
-        if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
+        if getattr(t, "dtype", None) is not self._bf16:
             raise TypeError(f"{name}: expected a torch.bfloat16 tensor")
-        if t.get_device() != self._device.index:
+        if t.get_device() != self._index:
             raise ValueError(f"{name}: on {t.device}, the handle on {self._device}")
         s = t.stride()
         if t.shape != shape or s[-1] != 1:
@@ -672,9 +673,9 @@ class Handle:
 
     def _dense(self, t, dtype, name, shape):
         """Pointer to a contiguous tensor of `shape` on the handle's device."""
-        if not isinstance(t, self._torch.Tensor) or t.dtype is not dtype:
-            raise TypeError(f"{name}: expected {dtype}")
-        if t.get_device() != self._device.index:
+        if getattr(t, "dtype", None) is not dtype:
+            raise TypeError(f"{name}: expected a {dtype} tensor")
+        if t.get_device() != self._index:
             raise ValueError(f"{name}: on {t.device}, the handle on {self._device} (a CUDA tensor is needed)")
         if t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name}: expected shape {tuple(shape)}, contiguous, got {tuple(t.shape)}")
@@ -686,23 +687,29 @@ class Handle:
         int32 or None.  S sequences of the call's own: packed prompts are one."""
         if not isinstance(rope, Rope):
             raise TypeError("rope: expected a Rope")
-        c, i32 = self.cfg, self._torch.int32
-        one = q if q is not None else k
+        c, i32 = self.cfg, self._i32
+        one = k if q is None else q
         if one is None:
             raise ValueError("q, k or both")
-        L, S, _, n = one.shape[:4] if one.dim() == 5 else (0,) * 4
-        rows = [None] * 4
-        for w, (name, t, out, heads) in enumerate((("q", q, q_out, c.n_kv_heads * c.group),
-                                                   ("k", k, k_out, c.n_kv_heads))):
-            if t is not None:
-                shape = (L, S, heads, n, c.head_dim)
-                rows[w] = self._strided(t, name, shape, 1)
-                rows[w + 2] = rows[w] if out is None else self._strided(out, name + "_out", shape, 1)
-            elif out is not None:
-                raise ValueError(f"{name}_out without {name}")
+        shape = one.shape
+        L, S, n = (shape[0], shape[1], shape[3]) if len(shape) == 5 else (0, 0, 0)
+        q_rows = k_rows = q_to = k_to = None
+        if q is not None:
+            shape = (L, S, c.n_kv_heads * c.group, n, c.head_dim)
+            q_rows = q_to = self._strided(q, "q", shape, 1)
+            if q_out is not None:
+                q_to = self._strided(q_out, "q_out", shape, 1)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if k is not None:
+            shape = (L, S, c.n_kv_heads, n, c.head_dim)
+            k_rows = k_to = self._strided(k, "k", shape, 1)
+            if k_out is not None:
+                k_to = self._strided(k_out, "k_out", shape, 1)
+        elif k_out is not None:
+            raise ValueError("k_out without k")
         self._check(load_library().kvc_rotary(
-            self._h, rope._ref, rows[0], rows[1], rows[2], rows[3], L, S, n,
-            self._dense(pos, i32, "pos", (S, n)),
+            self._h, rope._ref, q_rows, k_rows, q_to, k_to, L, S, n, self._dense(pos, i32, "pos", (S, n)),
             None if n_tok is None else self._dense(n_tok, i32, "n_tok", (S,)),
             self._stream(stream)), "kvc_rotary")
 
@@ -710,7 +717,7 @@ class Handle:
         """kvc_prompt_attend: causal attention over whole prompts.  Padded: q, out [S, H*G, n, d], k,
         v [S, H, n, d] bf16 (any strides), lse [S, H*G, n] fp32 or None, n_tok [S] int32 or None.
         Packed, with first [S] int32: the same without S, and n_tok."""
-        c, torch = self.cfg, self._torch
+        c = self.cfg
         seqs = (q.shape[0],) if first is None else ()
         S = seqs[0] if seqs else first.numel()
         n = q.shape[-2] if q.dim() == 3 + len(seqs) else 0
@@ -719,28 +726,28 @@ class Handle:
         self._check(load_library().kvc_prompt_attend(
             self._h, self._strided(q, "q", many, seq, None), self._strided(k, "k", few, seq, None),
             self._strided(v, "v", few, seq, None), S, n,
-            None if first is None else self._dense(first, torch.int32, "first", (S,)),
-            None if n_tok is None else self._dense(n_tok, torch.int32, "n_tok", (S,)),
+            None if first is None else self._dense(first, self._i32, "first", (S,)),
+            None if n_tok is None else self._dense(n_tok, self._i32, "n_tok", (S,)),
             self._strided(out, "out", many, seq, None),
-            None if lse is None else self._dense(lse, torch.float32, "lse", many[:-1]),
+            None if lse is None else self._dense(lse, self._f32, "lse", many[:-1]),
             self._stream(stream)), "kvc_prompt_attend")
 
     def keep_heaviest(self, weights, seq_len, kept_idx, n_kept, weights_out, stream=None):
         """kvc_keep_heaviest: the tokens that an eviction keeps by weights [L, B, H, cap] fp32 of
         sequences of seq_len [B] int32: kept_idx [L, B, H, budget], n_kept [L, B, H] int32, and
         their weights in weights_out [L, B, H, cap] (may be weights)."""
-        c, torch = self.cfg, self._torch
+        c, i32, f32 = self.cfg, self._i32, self._f32
         shape = weights.shape
         if len(shape) != 4 or shape[1:3] != (c.batch, c.n_kv_heads):
             raise ValueError(f"weights: expected shape (L, {c.batch}, {c.n_kv_heads}, cap), got "
                              f"{tuple(shape)}")
         L, B, H, cap = shape
         self._check(load_library().kvc_keep_heaviest(
-            self._h, self._dense(weights, torch.float32, "weights", shape), L, cap,
-            self._dense(seq_len, torch.int32, "seq_len", (B,)),
-            self._dense(kept_idx, torch.int32, "kept_idx", (L, B, H, c.budget)),
-            self._dense(n_kept, torch.int32, "n_kept", (L, B, H)),
-            self._dense(weights_out, torch.float32, "weights_out", shape),
+            self._h, self._dense(weights, f32, "weights", shape), L, cap,
+            self._dense(seq_len, i32, "seq_len", (B,)),
+            self._dense(kept_idx, i32, "kept_idx", (L, B, H, c.budget)),
+            self._dense(n_kept, i32, "n_kept", (L, B, H)),
+            self._dense(weights_out, f32, "weights_out", shape),
             self._stream(stream)), "kvc_keep_heaviest")
 
     def wait_self_test(self, stream=None):
