@@ -16,9 +16,12 @@
 //   items (1 warp)    which tiles come next, a few ahead of the others.
 // P is rounded to bf16 because V is bf16 (both operands of a product have one type): half
 // a step of 2^-8 a weight, less than that in their sum, which is taken before rounding.
-// bf16 has fp32's exponents: a weight may lie far above 1, so that the reference m of a row,
-// its first tile's largest logit, moves only when a later one passes it by 2^32 (and O is
-// scaled then, by the softmax warps themselves).  The maximum comes with the TMEM load.
+// bf16 has fp32's exponents: a weight may lie above 1, so that the reference m of a row,
+// its first tile's largest logit, moves only when a later one passes it by 14 in base 2 (and O is
+// scaled then, by the softmax warps themselves).  O holds sums of weights times values before they
+// are divided: what weights may grow by is missing there (at 2^32 values of 8e28 were too large).
+// Less room costs more moves: 16384 tokens with keys and queries of uneven length 1282 us with 20
+// or 32, 1298 with 14, 1340 with 8.  The maximum comes with the TMEM load.
 //
 // The arithmetic bounds this: 4 d operations a pair of tokens and head.  Measured, d = 128: one
 // sequence of 16384 tokens, 28 heads, 1.2 ms (1600 TFLOP/s; a step of both tiles 2900 cycles, its
@@ -55,7 +58,7 @@ constexpr int kItems = 4;        // items told ahead
 constexpr int kReaders = kSoftmaxWarps + 3;
 constexpr int kSorted = 128;     // sequences (or groups of them) in the list of items
 constexpr int kPacked = 16;      // heads in a tile at most
-constexpr float kRoom = 32.f;    // log2 of the largest weight
+constexpr float kRoom = 14.f;    // log2 of the largest weight
 // Registers: 168 a thread at launch, moved to where a row of S is held.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "more registers than the block has");
