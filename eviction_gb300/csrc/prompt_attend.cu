@@ -59,6 +59,11 @@ constexpr int kReaders = kSoftmaxWarps + 3;
 constexpr int kSorted = 128;     // sequences (or groups of them) in the list of items
 constexpr int kPacked = 16;      // heads in a tile at most
 constexpr float kRoom = 14.f;    // log2 of the largest weight
+// A row's weights are 2^(s f - r), r = m f rounded, m the largest score so far: all of them are off by
+// the factor that r is rounded by, which the sum takes out again, but from |r| = 2^30 on it is
+// infinite or zero.  From 2^29 on f is a power of two instead: r is exact then, and scores
+// that are not the same are 64 apart in base 2, 42 with that f, so that weights are 1 or nothing.
+constexpr float kExactRef = 536870912.f;
 // Registers: 168 a thread at launch, moved to where a row of S is held.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "more registers than the block has");
@@ -236,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               warp_token1 = __shfl_sync(0xffffffffu, row_token, 31);  // of the warp's rows
     const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
     const uint32_t s_tmem = tmem + lanes + t * 128, o_tmem = tmem + lanes + kOutCol + t * D;
-    const float f = a.scale_log2;
+    const float f = a.scale_log2;  // and the power of two next to it
+    const float near_f = __uint_as_float((__float_as_uint(f) + 0x400000u) & 0x7f800000u);
     int step = 0;  // of all items
     Item it;
     for (int i = 0; read_item(i, it) && it.steps[1] > 0; ++i) {
@@ -244,7 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_steps = it.of(t), t0 = it.t0 + t * p.tok;
       const int token = t0 + row_token;     // this row's token, and the last that it sees
       const int first_token = t0 + warp_token0, last_token = t0 + warp_token1;
-      float m = -INFINITY, sum = 0.f;       // reference of the weights, their sum
+      float m = -INFINITY, sum = 0.f;       // score that the weights refer to, their sum
+      float own_f = f;
       bool ok = true;
       for (int j = 0; j < n_steps; ++j, ++step) {
         if (!warp_wait(&s_full[t], step & 1, abort, a.status)) {
@@ -281,12 +288,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        top *= f;
-        const bool raise = top - m > kRoom;
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool raise = (top - m) * f > kRoom;
         if (__any_sync(0xffffffffu, raise)) {
-          const float keep = raise ? ex2(m - top) : 1.f;
-          if (raise) m = top;
+          const float keep = raise ? ex2((m - top) * f) : 1.f;
+          if (raise) {
+            m = top;
+            own_f = fabsf(top * f) < kExactRef ? f : near_f;
+          }
           sum *= keep;
           if (j > 0) {  // what is there is scaled to the new references (the last step's product
                         // was issued before these scores: it is done)
@@ -301,8 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float ref = m == -INFINITY ? 0.f : m;
-        const float2 ff = make_float2(f, f), off = make_float2(-ref, -ref);
+        const float ref = m == -INFINITY ? 0.f : __fmul_rn(m, own_f);
+        const float2 ff = make_float2(own_f, own_f), off = make_float2(-ref, -ref);
         float2 part = make_float2(0.f, 0.f);
         uint32_t w[4][16];
 #pragma unroll
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (there && a.lse)
         a.lse[(static_cast<size_t>(it.sb) * a.H * a.G + it.hq + row_head) * a.n + it.row0 + token] =
-            (m + __log2f(sum)) * 0.6931471805599453f;
+            (__fmul_rn(m, f) + __log2f(sum)) * 0.6931471805599453f;
       tc_fence_before();  // (the next item's P is told after this: O may be written again then)
     }
   } else {

@@ -673,9 +673,11 @@ int kvc_rotary(kvc_handle* h, const kvc_rope* rope, const kvc_rows* q, const kvc
  * written there.  A sequence that does not lie within its n rows is skipped (BAD_INDEX).
  * Arithmetic: products of bf16 operands accumulated in fp32; maxima and sums in fp32; the
  * softmax weights are rounded to bf16 for the product with v.  q, k and v must be finite
- * in the rows of sequences: what is not spoils rows of its own sequence.  Magnitudes of v must
+ * in the rows of sequences: what is not spoils rows of its own sequence.  Logits are exact to
+ * fp32's rounding as long as q.k and scale q.k log2(e) stay finite in fp32.  Magnitudes of v must
  * stay below 2^112 / n_tok (sums of them, times weights of up to 2^14, are held in fp32 before
- * they are divided; the cache's own largest value is 448 2^64).
+ * they are divided; the cache's own largest value is 448 2^64), below 2^96 / n_tok where logits reach
+ * 2^23.
  * Limits (KVC_ERR_UNSUPPORTED): n_seq <= 2^20, tokens (n packed, n_seq n padded) < 2^30, H*G <
  * 2^16, (tokens / 16 + n_seq) H G < 2^31, strides < 2^39 values; tokens' strides, and the
  * heads' of q, must not be 0. */

@@ -28,3 +28,29 @@ def test_prompt_large_values_of_later_keys(at, rise, d):
     p.k[:, :, at] = rise * math.log(2) / math.sqrt(d)
     p.run()
     p.check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_logits_of_any_size(d):
+    """Logits of 2^13 to 2^100 that are all but equal (a few of fp32's steps apart, one step is 2^16 and
+    more of a weight from 2^27 on): the output stays within the values, and lse with the logits."""
+    n = 400
+    p = Prompts([n], 1, 2, d, False, gap=0)
+    steps = torch.randint(-100, 101, (n,), generator=torch.Generator().manual_seed(d)).cuda()
+    v = p.v.double()[0, 0]
+    low, high = v.cummin(0).values, v.cummax(0).values
+    room = 2.0 ** -7 * v.abs().cummax(0).values  # (weights and the result are rounded to bf16)
+    for exp in range(10, 98):
+        for sign in (1.0, -1.0):
+            p.q, p.k = torch.zeros_like(p.q), torch.zeros_like(p.k)
+            p.q[..., 0], p.q[..., 1] = sign * 8 * 1.25, 8 * 2.0 ** -21
+            p.q[:, 1, :, 0] *= 1.5
+            p.k[..., 0], p.k[..., 1] = 1.5 * 2.0 ** exp, steps * 2.0 ** exp
+            out, lse = p.run()
+            assert p.h.device_status() == 0
+            for g in (0, 1):
+                got, gl = out[0, g].double(), lse[0, g].double()
+                assert torch.isfinite(got).all() and torch.isfinite(gl).all(), exp
+                assert ((got <= high + room) & (got >= low - room)).all(), exp
+                z = float(p.q[0, g, 0, 0]) * 1.5 * 2.0 ** exp * d ** -0.5
+                assert ((gl - z).abs() <= 2.0 ** -12 * abs(z) + math.log(n)).all(), exp
