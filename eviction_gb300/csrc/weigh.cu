@@ -233,7 +233,15 @@ __global__ void __launch_bounds__(32 * kWarps) weigh_few_kernel(Cache c, WeighAr
     if (fresh) {  // queries as fp16, in the order of the key reads
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const auto& v = raw[nt];
+        auto& v = raw[nt];
+        // a row that sees no token may hold anything: zeros, so that its scores are no NaN (the lse of
+        // row g is with the lanes whose q4 is g / 2)
+        const float lse0 = __shfl_sync(0xffffffffu, raw_lse[nt][0], g / 2);
+        const float lse1 = __shfl_sync(0xffffffffu, raw_lse[nt][1], g / 2);
+        if (sees_nothing(g % 2 ? lse1 : lse0)) {
+#pragma unroll
+          for (int k = 0; k < KV; ++k) v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
+        }
         float mx = 0.f;
 #pragma unroll
         for (int k = 0; k < KV; ++k)

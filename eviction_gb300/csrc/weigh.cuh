@@ -30,8 +30,9 @@ __device__ __forceinline__ Lengths lengths_of(const cache8::Cache& c, const Weig
 cudaError_t launch_weigh_many(const cache8::Cache& c, int format, const WeighArgs& a, cudaStream_t s);
 
 // A query's lse in base 2 as the weights take it: 2^(z - y); no token for one that saw none.
+__device__ __forceinline__ bool sees_nothing(float lse) { return fabsf(lse) == INFINITY; }
 __device__ __forceinline__ float lse_base2(float lse) {
-  return fabsf(lse) == INFINITY ? INFINITY : lse * 1.4426950408889634f;
+  return sees_nothing(lse) ? INFINITY : lse * 1.4426950408889634f;
 }
 
 }  // namespace prompt

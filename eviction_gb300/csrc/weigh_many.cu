@@ -86,7 +86,7 @@ struct Smem {
                        kFactors = kSumsAt + kSums * kChunk * 4,   // [2][2][128] f_t, by item parity
                        kParts = kFactors + 2 * 2 * kTile * 4,     // [2][128] the second halves' sums
                        kBars = kParts + 2 * kTile * 4,
-                       kNumBars = 2 * kStages + 2 * kSums + 2 * 6 + 2 * kItems + 1,
+                       kNumBars = 2 * kStages + 2 * kSums + 2 * 6 + 2 * kItems + 2,
                        kItem = (kBars + kNumBars * 8 + 15) & ~15, kMisc = kItem + kItems * 48,
                        kUpTo = kMisc + 16, kCount = kUpTo + (kSorted + 1) * 4,
                        kSeq = kCount + (kSorted + 1) * 4, kBytes = kSeq + kSorted + 1024;
@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(kThreads, 1)
            *k_full = y_empty + kSums,
            *k_empty = k_full + 2, *s_full = k_empty + 2, *s_empty = s_full + 2, *part_full = s_empty + 2,
            *part_empty = part_full + 2, *i_full = part_empty + 2, *i_empty = i_full + kItems,
-           *done = i_empty + kItems;
-  static_assert(Sm::kNumBars == 2 * NS + 2 * kSums + 12 + 2 * kItems + 1, "one place for each barrier");
+           *done = i_empty + kItems, *odd_full = done + 1;
+  static_assert(Sm::kNumBars == 2 * NS + 2 * kSums + 12 + 2 * kItems + 2, "one place for each barrier");
   float* s_sums = reinterpret_cast<float*>(smem + Sm::kSumsAt);      // [kSums][kChunk] -y
   float* s_factors = reinterpret_cast<float*>(smem + Sm::kFactors);  // [2][2][kTile]
   float* s_parts = reinterpret_cast<float*>(smem + Sm::kParts);      // [2][kTile]
@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&i_empty[i], kReaders);
     }
     mbar_init(done, 1);
+    mbar_init(odd_full, 1);
     *abort = 0;
     fence_barrier_init();
     prefetch_tensormap(&map_q);
@@ -426,7 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kQueryWarp) {
     // ------------------------------------------------------------ queries
     // A chunk's rows by TMA, and its rows' normalisers beside them, from this lane's columns
-    // lane + 32 k: head g and token j of the chunk.
+    // lane + 32 k: head g and token j of the chunk.  A query that sees no token may hold anything: where
+    // there is one, this warp waits for the copy itself and writes zeros in its place, so that
+    // its products are no NaN.
     int j[kChunk / 32], g[kChunk / 32];
 #pragma unroll
     for (int k = 0; k < kChunk / 32; ++k) {
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       j[k] = col < p.tok * p.P ? col / p.P : INT_MAX / 2;
       g[k] = col % p.P;
     }
-    uint32_t use = 0;
+    uint32_t use = 0, odd = 0;
     bool ok = true;
     Item it;
     for (int i = 0; ok && read_item(i, it); ++i) {
@@ -450,15 +453,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < kChunk / 32; ++k)
             y[k] = j[k] < it.nq - j0 ? lse[static_cast<size_t>(g[k]) * a.n + j0 + j[k]] : INFINITY;
           const int st = use % NS, sy = use % kSums;
+          auto blind = [&](int k) { return sees_nothing(y[k]) && j[k] < it.nq - j0; };
+          bool any = false;
+#pragma unroll
+          for (int k = 0; k < kChunk / 32; ++k) any = any || blind(k);
+          any = __any_sync(0xffffffffu, any);
           if (!(ok = warp_wait(&q_empty[st], ((use / NS) & 1) ^ 1, abort, c.status))) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(&q_full[st], DB * p.P * p.tok * 128);
+            uint64_t* full = any ? odd_full : &q_full[st];
+            mbar_arrive_expect_tx(full, DB * p.P * p.tok * 128);
             for (int x = 0; x < DB; ++x)
               tma_load_5d(smem + Sm::kRing + st * Sm::kStage + x * kQueryBlock, &map_q, 64 * x,
                           (it.h * a.G + s * p.P) * p.q_head, it.first + j0, a.first ? 0 : it.b * p.q_seq,
-                          it.l * p.q_layer, &q_full[st]);
+                          it.l * p.q_layer, full);
           }
           __syncwarp();
+          if (any) {
+            volatile int never = 0;  // (the copy lands before the CTA ends)
+            if (!(ok = warp_wait(odd_full, odd++ & 1, &never, c.status))) {
+              *abort = 1;
+              break;
+            }
+#pragma unroll
+            for (int k = 0; k < kChunk / 32; ++k)
+              if (blind(k))
+                for (int x = 0; x < DB * 8; ++x)
+                  *reinterpret_cast<uint4*>(smem + Sm::kRing + st * Sm::kStage + x / 8 * kQueryBlock +
+                                            (lane + 32 * k) * 128 + x % 8 * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[st]);
+          }
           ++use;
           if (!(ok = warp_wait(&y_empty[sy], (((use - 1) / kSums) & 1) ^ 1, abort, c.status))) break;
 #pragma unroll

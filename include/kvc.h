@@ -522,7 +522,7 @@ int kvc_cache8_attend(kvc_handle* h, const kvc_cache8* c, const kvc_rows* q, int
  *            Strides of tokens and heads must not be 0, all below 2^39 values
  *   n_q      [B] int32, 0 .. seq_len[b], or NULL (not packed): n
  *   lse      fp32, contiguous, [n_layers][B][H*G][n], packed [n_layers][H*G][n]; a query
- *            whose lse is -inf or +inf sees no token
+ *            whose lse is -inf or +inf sees no token, and its row of q may hold anything
  *   decay    in [0, 1]; 0 overwrites: weights are not read then
  *   weights  [n_layers][B][H][cap] fp32, in/out; a token that is new has 0 (or whatever
  *            it shall begin with).  Entries at and past seq_len[b] are left as they are
