@@ -1,5 +1,6 @@
 // prompt_api.cu -- host side of rotary positions, prompt attention and the choice of the
 // heaviest tokens: argument checks and the entry points.
+#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -42,12 +43,17 @@ int kvc_rope_init(const kvc_rope_config* c, kvc_rope* r) {
   if (c->scaling == KVC_ROPE_BANDS &&
       (!(c->low >= 0) || !std::isfinite(c->high) || c->high <= c->low || !positive(c->original)))
     return KVC_ERR_ARG;
+  // (what a float holds as a normal number)
+  if (!(c->magnitude >= FLT_MIN && c->magnitude <= FLT_MAX)) return KVC_ERR_ARG;
   constexpr double kTurn = 6.283185307179586476925;
-  r->dim = c->dim;
-  r->interleaved = c->interleaved;
-  r->magnitude = static_cast<float>(c->magnitude);
+  constexpr double kFastest = 4294967296.0;  // turns a token: 20 bits of a turn are left in a double
   double base = c->base;
   if (c->scaling == KVC_ROPE_NTK) base *= std::pow(c->factor, c->dim / (c->dim - 2.0));
+  if (!positive(base)) return KVC_ERR_ARG;
+  kvc_rope made = {};
+  made.dim = c->dim;
+  made.interleaved = c->interleaved;
+  made.magnitude = static_cast<float>(c->magnitude);
   for (int i = 0; i < 64; ++i) {
     double turns = 0;  // per token
     if (i < c->dim / 2) turns = std::pow(base, -2.0 * i / c->dim) / kTurn;
@@ -56,9 +62,11 @@ int kvc_rope_init(const kvc_rope_config* c, kvc_rope* r) {
       const double m = std::fmin(std::fmax((c->original * turns - c->low) / (c->high - c->low), 0.0), 1.0);
       turns = (1 - m) * turns / c->factor + m * turns;
     }
+    if (!(turns >= 0 && turns < kFastest)) return KVC_ERR_ARG;
     turns -= std::floor(turns);
-    r->turn[i] = turns < 1 ? static_cast<uint64_t>(std::ldexp(turns, 64)) : 0;
+    made.turn[i] = static_cast<uint64_t>(std::ldexp(turns, 64));
   }
+  *r = made;
   return KVC_OK;
 }
 

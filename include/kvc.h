@@ -628,7 +628,7 @@ typedef struct {
   double factor;    /* > 0 */
   double low, high; /* KVC_ROPE_BANDS: 0 <= low < high */
   double original;  /* KVC_ROPE_BANDS: > 0 */
-  double magnitude; /* > 0 */
+  double magnitude; /* > 0, a normal number as a float */
 } kvc_rope_config;
 
 /* What kvc_rotary takes; filled by kvc_rope_init, on the host, once. */
@@ -638,6 +638,8 @@ typedef struct {
   uint64_t turn[64]; /* a pair's turns per token, in 2^-64 of a turn */
 } kvc_rope;
 
+/* KVC_ERR_ARG, with *rope as it was, also where a frequency or the scaled base is not finite, or
+ * a pair makes 2^32 turns a token and more. */
 int kvc_rope_init(const kvc_rope_config* cfg, kvc_rope* rope);
 
 /* Turn the rows of q and k by their tokens' positions, in place or into other rows.
