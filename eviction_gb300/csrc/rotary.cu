@@ -2,9 +2,9 @@
 //
 // Pair (x, y) of a row goes to (x cos a - y sin a, x sin a + y cos a), a = pos f_i.  The
 // frequency is held in turns per token, in 2^-64 of a turn, so that pos * f_i in 64-bit
-// integers drops whole turns by itself: the angle is exact at any position, where an fp32
-// product is off by 0.06 radians at a million tokens.  The top 32 bits, signed, are the
-// angle in half turns, which sincospif takes.
+// integers drops whole turns by itself, where an fp32 product is off by up to 0.06 radians at a
+// million tokens.  The top 32 bits, signed, are the angle in half turns, within one: as a float, which
+// sincospif takes, it is rounded by up to 2^-25 of a half turn, 2^-23.3 radians, at any position.
 //
 // The rows are read and written once, which bounds the call: 8 x 4096 tokens of 32 heads of 128,
 // 537 MB, take 79 us, 6.8 TB/s.  A CTA has a few tokens and all of their heads: it computes their

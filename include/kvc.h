@@ -613,8 +613,9 @@ int kvc_cache8_free(kvc_handle* h, const kvc_cache8* c, int n, const int32_t* se
  *                    are interpolated ("YaRN: Efficient Context Window Extension of
  *                    Large Language Models", 3.2, which also scales the rows by
  *                    magnitude = 0.1 ln(factor) + 1).
- * Positions are multiplied in 64-bit fixed point: an angle is off by 2^-29 and 2^-51 of
- * itself at most.  Sines, products and sums are fp32, the result is rounded once. */
+ * Frequencies are fp64's; positions are multiplied in 64-bit fixed point: an angle is off by 2^-28
+ * and 2^-49 of itself at most (bases up to 10^6).  Without its whole turns it is rounded to fp32, by
+ * 2^-23 at most.  Sines, products and sums are fp32, the result is rounded once. */
 #define KVC_ROPE_NONE 0
 #define KVC_ROPE_LINEAR 1
 #define KVC_ROPE_NTK 2

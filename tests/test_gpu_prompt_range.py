@@ -2,10 +2,12 @@
 64 bits: as far as include/kvc.h says that they hold."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_prompt import Prompts
+from tests import prompt_ref as pr
+from tests.test_gpu_prompt import Prompts, _handle, _ints
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +56,34 @@ def test_prompt_logits_of_any_size(d):
                 assert ((got <= high + room) & (got >= low - room)).all(), exp
                 z = float(p.q[0, g, 0, 0]) * 1.5 * 2.0 ** exp * d ** -0.5
                 assert ((gl - z).abs() <= 2.0 ** -12 * abs(z) + math.log(n)).all(), exp
+
+
+@pytest.mark.parametrize("near,most", [(2.0 ** -14, 2 ** 20), (2.0 ** -18, 2 ** 22)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_angle_is_as_good_as_stated(interleaved, near, most):
+    """Sines of angles next to whole half turns, so that the result's own rounding (bf16 has 8 bits: half a
+    step is 2^-8 of a value of at most `near`) is no larger than the angle's: off by pi 2^-25 where the angle, up to
+    half a turn, is rounded to fp32, by 2^-28 and 2^-49 of itself before; then a step of a sine next to 0 (below 2^-37)."""
+    import eviction_gb300 as kvc
+    d, f = 64, pr.frequencies(64)
+    pos, pair = [], []
+    at = np.arange(1, most, dtype=np.float64)
+    for i in (1, 2, 3, 5, 8, 13):
+        found = at[np.abs(np.sin(at * f[i])) < near].astype(int)
+        assert len(found) > 2
+        pos += found.tolist() + (-found).tolist()
+        pair += [i] * (2 * len(found))
+    n = len(pos)
+    h = _handle(1, 1, d)
+    x = torch.zeros((1, 1, 1, n, d), dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros_like(x)
+    first, second = (lambda i: 2 * i, lambda i: 2 * i + 1) if interleaved else (lambda i: i, lambda i: i + d // 2)
+    rows = torch.arange(n)
+    i = torch.tensor(pair)
+    x[0, 0, 0, rows, first(i)] = 1.0
+    h.rotary(kvc.Rope(d, interleaved=interleaved), _ints([pos]), k=x, k_out=y)
+    a = torch.tensor(pos, dtype=torch.float64) * torch.tensor(f, dtype=torch.float64)[i]
+    got = y[0, 0, 0, rows, second(i)].double().cpu()
+    bound = math.pi * 2.0 ** -25 + 2.0 ** -28 + 2.0 ** -49 * a.abs() + 2.0 ** -8 * a.sin().abs() + 2.0 ** -37
+    off = (got - a.sin()).abs()
+    assert (off <= bound).all(), float((off / bound).max())
