@@ -18,8 +18,9 @@
 //
 // Measured: 64 sequences of 612 to 1112 tokens, 8 heads of 128 (e4m3, 61 MB) 15.5 us, 4 of 32768,
 // 4 heads (int8, 71 MB) 16 us, of which launch, the first copies' latency and the last stretch's end
-// are 6 us.  Up to 32 query rows: the other kernel takes 54 us for 12 to 32 rows of the former, this
-// one 19 to 28.
+// are 6 us.  Up to 32 query rows of a KV head (packed calls: of all sequences together, which is all that
+// the host knows): on the former batch 15.5 us for 8 rows, 19 for 12 and 16, 28 for 24 and 32, where the
+// other kernel takes 54; 36 to 64 rows take 55 there, 128 62, 188 65.
 #include "weigh.cuh"
 
 namespace kvc {

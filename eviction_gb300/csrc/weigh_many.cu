@@ -22,15 +22,17 @@
 //                     exponential, sum.  One tile's exponentials run while the other's
 //                     products do.
 // Exponentials and products take the same time (512 cycles of an SM for 128 x 128).  Measured, 8
-// sequences of 1536 tokens, all queries of 4 x 7 heads of 128: 82 us.  What bounds it are the weight
+// sequences of 1536 tokens, all queries of 4 x 7 heads of 128: 83 us.  What bounds it are the weight
 // warps, busy 85% of the time: 1200 cycles a tile and chunk, for 768 of exponentials alone, go by
 // on waits, TMEM loads and normalisers of shared memory.  (A warp of products for each tile 87 us; all
 // sixteen weight warps on one tile at a time 88; three buffers of 128 columns for both tiles 101.)
 // Chunks that a tile does not see are skipped.
 //
 // Work: pairs of tiles of all sequences, layers and heads, those with most queries first, dealt
-// to one CTA per SM in turns, back and forth.  Nothing is summed across CTAs: the result does
-// not depend on the schedule.  Every wait is bounded.
+// to one CTA per SM in turns, back and forth.  Where there are few pairs their queries are cut into
+// parts, whose sums a second launch adds up in order.  How many goes by the call's sizes (cap,
+// table, batch, rows) and the SMs, so that a token's last bits do too, but nothing depends on the
+// schedule.  Every wait is bounded.
 #include <climits>
 
 #include "weigh.cuh"
@@ -662,9 +664,13 @@ cudaError_t launch_d(const Cache& c, const WeighArgs& a, cudaStream_t s) {
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   // Where there are few pairs of tiles, their queries are cut into parts of 8 chunks and more, for
-  // two items an SM, which a second launch adds up.  Prompts of 1536 tokens, whole and cut: 24
+  // two items an SM, which a second launch adds up.  Both numbers are upper bounds, since the lengths are
+  // on the device: pairs from the room of cap and table, chunks from all rows of a packed call, whose
+  // sequences may have fewer (parts may be empty then).  Prompts of 1536 tokens, whole and cut: 24
   // pairs 82 and 24 us, 96 pairs 82 and 48, 192 pairs 85 and 82, but 288 pairs 105 and 113; and
-  // parts of less cost more than they save (64 queries, 192 pairs: 18 and 22 us).
+  // parts of less cost more than they save (64 queries, 192 pairs: 18 and 22 us).  With more room than
+  // tokens there are fewer parts (1 x 1536 tokens, 24 pairs: 24 us with cap 1536, 38 with 8192, 83 with
+  // 32768).
   const int tokens = min(a.cap, c.max_blocks * c.bs);
   p.pairs = (tokens + 2 * kTile - 1) / (2 * kTile);
   const long long most = static_cast<long long>(c.L) * c.B * c.H * p.pairs;
