@@ -58,6 +58,21 @@ def test_prompt_logits_of_any_size(d):
                 assert ((gl - z).abs() <= 2.0 ** -12 * abs(z) + math.log(n)).all(), exp
 
 
+@pytest.mark.parametrize("scale", [0.03, 1.0, 3.5])
+@pytest.mark.parametrize("packed", [True, False])
+def test_prompt_softmax_scale_of_the_configuration(packed, scale):
+    p = Prompts([150, 1, 333], 2, 3, 128, packed, q_scale=1.0)
+    p.h = _handle(2, 3, 128, softmax_scale=scale)
+    out, lse = p.run()
+    assert p.h.device_status() == 0
+    for b in range(3):
+        for hq in range(6):
+            w, l, tol, ltol = pr.attention(p.rows(b, p.q, hq), p.rows(b, p.k, hq // 3), p.rows(b, p.v, hq // 3),
+                                           float(np.float32(scale)))
+            assert ((p.rows(b, out, hq).double() - w).abs() <= tol).all()
+            assert ((p.rows(b, lse[..., None], hq)[..., 0].double() - l).abs() <= ltol).all()
+
+
 @pytest.mark.parametrize("near,most", [(2.0 ** -14, 2 ** 20), (2.0 ** -18, 2 ** 22)])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rotary_angle_is_as_good_as_stated(interleaved, near, most):
