@@ -24,12 +24,13 @@
 // or 32, 1298 with 14, 1340 with 8.  The maximum comes with the TMEM load.
 //
 // The arithmetic bounds this: 4 d operations a pair of tokens and head.  Measured, d = 128: one
-// sequence of 16384 tokens, 28 heads, 1.2 ms (1600 TFLOP/s; a step of both tiles 2900 cycles, its
-// 32 products alone 2048: S = Q K^T reads both operands at all of shared memory's bandwidth, beside
-// the copies); 16 sequences of 612 to 1112 tokens, 32 heads, 106 us, a quarter of it the changes of
-// items (a result written beside the next item's products slows those more than it hides: 111 us).
-// The last tile of
-// keys is cut to the columns (steps of 16) that some row of the tile sees, in both products.
+// sequence of 16384 tokens, 28 heads, 1.31 ms in a row (1470 TFLOP/s; power holds the clocks down) and
+// 1.21 ms in runs of a few (1590; a step of both tiles 3000 cycles, its 32 products alone 2048:
+// S = Q K^T reads both operands at all of shared memory's bandwidth, beside the copies); 16 sequences
+// of 612 to 1112 tokens, 32 heads, 108 us back to back in a graph, 113 as calls, a quarter of it the
+// changes of items (a result written beside the next item's products slows those more than it hides: 111
+// us, of 106 then).  The last tile of keys is cut to the columns (steps of 16) that some row of the tile
+// sees, in both products.
 // Rows of V behind a sequence's end are zeroed in shared memory first (their weights are
 // 0, and what stands there need not be finite).
 //

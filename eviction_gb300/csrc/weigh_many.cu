@@ -17,7 +17,7 @@
 //   MMA (1 warp)      128 x 192 products into the tile's columns of TMEM, with the keys read
 //                     from there: from shared memory, keys, queries, copies and normalisers
 //                     together asked for more than its bandwidth (98 us with 128 columns a
-//                     product, 84 us with 256, of what is 82 us below);
+//                     product, 84 us with 256, of 82 then);
 //   weights (16 warps)  two warps a lane quarter and tile, a half of the columns each: scale,
 //                     exponential, sum.  One tile's exponentials run while the other's
 //                     products do.
@@ -25,7 +25,8 @@
 // sequences of 1536 tokens, all queries of 4 x 7 heads of 128: 83 us.  What bounds it are the weight
 // warps, busy 85% of the time: 1200 cycles a tile and chunk, for 768 of exponentials alone, go by
 // on waits, TMEM loads and normalisers of shared memory.  (A warp of products for each tile 87 us; all
-// sixteen weight warps on one tile at a time 88; three buffers of 128 columns for both tiles 101.)
+// sixteen weight warps on one tile at a time 88; three buffers of 128 columns for both tiles 101.)  At
+// 80 registers up to 20 bytes a thread spill at d 128.
 // Chunks that a tile does not see are skipped.
 //
 // Work: pairs of tiles of all sequences, layers and heads, those with most queries first, dealt

@@ -627,7 +627,9 @@ int kvc_cache8_free(kvc_handle* h, const kvc_cache8* c, int n, const int32_t* se
  *                    times over `original` tokens keep f, those below `low` turns
  *                    are interpolated ("YaRN: Efficient Context Window Extension of
  *                    Large Language Models", 3.2, which also scales the rows by
- *                    magnitude = 0.1 ln(factor) + 1).
+ *                    magnitude = 0.1 ln(factor) + 1).  Implementations that ramp over
+ *                    the pair's number, between two rounded ones, have other
+ *                    frequencies between the ends
  * Frequencies are fp64's; positions are multiplied in 64-bit fixed point: an angle is off by 2^-28
  * and 2^-49 of itself at most (bases up to 10^6).  Without its whole turns it is rounded to fp32, by
  * 2^-23 at most.  Sines, products and sums are fp32, the result is rounded once. */
