@@ -700,7 +700,8 @@ int kvc_rotary(kvc_handle* h, const kvc_rope* rope, const kvc_rows* q, const kvc
  * 2^23.
  * Limits (KVC_ERR_UNSUPPORTED): n_seq <= 2^20, tokens (n packed, n_seq n padded) < 2^30, H*G <
  * 2^16, (tokens / 16 + n_seq) H G < 2^31, strides < 2^39 values; tokens' strides, and the
- * heads' of q, must not be 0. */
+ * heads' of q, must not be 0.  Many thousands of sequences cost time that grows with their square
+ * (of 6 tokens and 2 heads: 1000 0.3 ms with a first call's set-up, 20000 1.3 ms, 131072 41 ms). */
 int kvc_prompt_attend(kvc_handle* h, const kvc_rows* q, const kvc_rows* k, const kvc_rows* v,
                       int n_seq, int n, const int32_t* first, const int32_t* n_tok,
                       const kvc_rows* out, float* lse, void* stream);
